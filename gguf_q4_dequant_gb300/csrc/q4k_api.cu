@@ -22,6 +22,7 @@
 #include "q4k.h"
 #include "q4k_device.cuh"
 #include "q4k_internal.h"
+#include "q4k_serve.h"
 
 namespace q4k {
 
@@ -114,7 +115,8 @@ void init_device(int dev, DeviceState& st) {
     st.info.max_smem_optin = static_cast<int>(prop.sharedMemPerBlockOptin);
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess || gemv_setup(st.info) != cudaSuccess || tcgemv_setup(st.info) != cudaSuccess ||
-        gemm_setup(st.info) != cudaSuccess || encoder() == nullptr) {
+        gemm_setup(st.info) != cudaSuccess || attn_setup(st.info) != cudaSuccess || pick_setup() != cudaSuccess ||
+        encoder() == nullptr) {
         st.status = Q4K_ERR_CUDA;
         return;
     }
@@ -336,6 +338,26 @@ int check_matmul(int count, const void* const* W, const int64_t* N, int64_t K, c
 }
 
 }  // namespace
+
+int device_info(const DeviceInfo** info) { return current_device(info); }
+int pdl_mode() { return g_pdl.load(std::memory_order_relaxed); }
+
+bool encode_bf16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box) {
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i > 0) st[i - 1] = strides[i - 1];
+    }
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+                     const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace q4k
 
 using namespace q4k;
@@ -350,9 +372,10 @@ const char* q4k_status_string(int status) {
             return "Q4K_ERR_BAD_DIM: a size or mode is out of range (N, M >= 1; K >= 256, K % 256 == 0; "
                    "N, M < 2^31; K <= 2^24; group count 1..8; argmax M <= 16; PDL mode 0..2)";
         case Q4K_ERR_CUDA: return "Q4K_ERR_CUDA: a CUDA call or kernel launch failed";
-        case Q4K_ERR_ALIGN: return "Q4K_ERR_ALIGN: W, X, Y and out must be 16-byte aligned";
+        case Q4K_ERR_ALIGN: return "Q4K_ERR_ALIGN: a pointer lacks its alignment (W, X, Y and out: 16 bytes)";
         case Q4K_ERR_ARCH: return "Q4K_ERR_ARCH: the current device is not compute capability 10.3";
         case Q4K_ERR_TIMEOUT: return "Q4K_ERR_TIMEOUT: an in-kernel wait ran out of time";
+        case Q4K_ERR_SPACE: return "Q4K_ERR_SPACE: the workspace is smaller than the call needs";
     }
     return "unknown q4k status";
 }

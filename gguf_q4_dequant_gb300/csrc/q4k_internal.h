@@ -90,4 +90,13 @@ cudaError_t launch_gemm(const WeightGroup& grp, const CUtensorMap& tmapX, int M,
 // Sets the kernels' attributes and fills dev.gemm_clusters.
 cudaError_t gemm_setup(DeviceInfo& dev);
 
+// The current device's entry, set up on first use (a q4k_status), and the
+// process-wide PDL mode.
+int device_info(const DeviceInfo** info);
+int pdl_mode();
+// cuTensorMapEncodeTiled of a bf16 tensor with the 128-byte swizzle (zero fill
+// outside); `strides` in bytes, for dimensions 1 .. rank - 1.
+bool encode_bf16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box);
+
 }  // namespace q4k

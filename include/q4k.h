@@ -58,9 +58,11 @@ enum q4k_status {
                               K % 256 == 0, N and M below 2^31, K <= 2^24, 1 <= count <= 8
                               (grouped calls), M <= 16 (argmax calls), mode 0..2 (PDL) */
     Q4K_ERR_CUDA = -3,     /* a CUDA runtime call or kernel launch failed */
-    Q4K_ERR_ALIGN = -4,    /* W, X, Y or out not 16-byte aligned */
+    Q4K_ERR_ALIGN = -4,    /* a pointer lacks the alignment that the call states (W, X, Y and
+                              the float or bf16 arrays: 16 bytes) */
     Q4K_ERR_ARCH = -5,     /* current device is not compute capability 10.3 */
-    Q4K_ERR_TIMEOUT = -6   /* a bounded in-kernel wait ran out (device error word) */
+    Q4K_ERR_TIMEOUT = -6,  /* a bounded in-kernel wait ran out (device error word) */
+    Q4K_ERR_SPACE = -7     /* the workspace is smaller than the call needs */
 };
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -179,6 +181,187 @@ int q4k_device_error(int clear);
  * such call: it checks this library's own timeout mechanism.)
  */
 int q4k_selftest_timeout(int64_t limit_ns, void* stream);
+
+/* ======================================================================
+ * Between the products of a decode or prefill step
+ * ======================================================================
+ * What a served model does between two of the calls above: the q, k and v rows
+ * of a step go into a paged cache (q4k_cache_append), attention reads it
+ * (q4k_cache_attention), the pages are handed out, shared, given back and
+ * moved together as sequences come and go (q4k_pages_*), and the logits are
+ * adjusted before the greedy pick (q4k_logits_pick). The pages of the
+ * reference describe these parts of the runner around Op::DequantMatMul:
+ * resident K/V decode ("rlx-llama32" crate page, section "Decode"), the
+ * repetition penalty over recent tokens and the pick (nx_f32_llm_run_v3
+ * listing).
+ *
+ * The rules of the calls above hold: asynchronous on `stream`, no allocation,
+ * no host synchronisation, capturable, arguments checked before any launch.
+ * Device arrays are read when the call runs on the device, so their contents
+ * may be produced by earlier work on the stream; contents out of range (a
+ * sequence, page, length or token id) never lead outside the arrays, and what
+ * they mean is said at each call.
+ *
+ * A cache describes the K and V pages of all layers of a model:
+ *   element (layer, page, kv head, row, dim) of K is at
+ *     k[layer*layer_stride + page*page_stride + (head*page_size + row)*head_dim + dim],
+ *   and the same for V. Position p of sequence s lives in row p % page_size of
+ *   page table[s*width + p/page_size].
+ * refs[page] counts the sequences that hold the page; 0: the page is free.
+ * lens[s] is the number of positions of sequence s, 0: not in use. Entries of
+ * table past a sequence's pages are -1 (they are never followed).
+ *
+ * A step's batch is n sequences with new tokens: seqs[i] (device, distinct;
+ * NULL: 0..n-1) names the i-th one, and its new tokens are rows starts[i] to
+ * starts[i+1]-1 of the step's arrays (starts: device, n+1 ascending values; a
+ * sequence may have none). lens counts the new tokens: q4k_pages_reserve adds
+ * them, so new token r of a sequence with m of them is at position
+ * lens - m + r.
+ */
+typedef struct q4k_cache {
+    uint16_t* k;           /* device, bf16 bit patterns, 16-byte aligned */
+    uint16_t* v;
+    int64_t layer_stride;  /* elements; multiples of 8; layers and pages must not overlap */
+    int64_t page_stride;
+    int32_t* refs;         /* device, [n_pages] */
+    int32_t* table;        /* device, [n_seqs][width] */
+    int32_t* lens;         /* device, [n_seqs] */
+    int64_t n_pages;       /* 1 .. 2^30 */
+    int32_t layers;        /* 1 .. 65535 */
+    int32_t kv_heads;      /* 1 .. 1024 */
+    int32_t page_size;     /* 16, 32, 64 or 128 */
+    int32_t head_dim;      /* 64 or 128 */
+    int32_t n_seqs;        /* 1 .. 2^24 */
+    int32_t width;         /* pages per sequence at most; width*page_size <= 2^30 */
+} q4k_cache;
+
+/*
+ * Bytes of the workspace that the calls below take (device, 256-byte aligned),
+ * or a negative status. It must be zero-filled before its first use; every
+ * call leaves what later calls rely on, so one workspace serves any sequence
+ * of calls on one stream. Calls that may run at the same time need one each.
+ * The size depends on n_pages, head_dim and the device only.
+ */
+int64_t q4k_cache_workspace(const q4k_cache* c);
+
+/*
+ * Stores a step's keys and values in one layer, from the fp32 outputs of its
+ * q, k and v products (q4k_matmul_multi): for every new token
+ *   K page row = bf16(rot(norm(Yk row, k_norm))),  V page row = bf16(Yv row),
+ *   q_out row  = bf16(rot(norm(Yq row, q_norm))),
+ * per head. norm(x, w) = x / sqrt(mean(x^2) + eps) * w where the weights are
+ * given (head_dim floats, the per-head norm of Qwen3), else x. rot turns pairs
+ * of elements by the angle of the token's position p: (a, b) becomes
+ * (a cos - b sin, a sin + b cos), with cos = rope[p*head_dim + i] and sin =
+ * rope[p*head_dim + head_dim/2 + i] for pair i; pairs = 1: elements (2i, 2i+1),
+ * 2: (i, i + head_dim/2), 0: no rotation (rope may be NULL). Everything is
+ * computed in fp32 and rounded once.
+ *   Yq  device, [tokens][heads*head_dim] floats; Yk, Yv [tokens][kv_heads*head_dim]
+ *   q_out  device, [tokens][heads][head_dim] bf16
+ *   rope   device, [rope_rows][head_dim] floats, rope_rows >= width*page_size
+ * heads is a multiple of kv_heads. 1 <= n <= 4096; 1 <= tokens < 2^31.
+ * Rows of a sequence id, position or page out of range are not stored (their
+ * q_out is still written, unrotated when there is no position).
+ */
+int q4k_cache_append(const q4k_cache* c, int layer, const int32_t* seqs, int n, const int32_t* starts,
+                     int64_t tokens, const float* Yq, const float* Yk, const float* Yv,
+                     uint16_t* q_out, int heads, const float* rope, int64_t rope_rows, int pairs,
+                     const float* q_norm, const float* k_norm, float eps, void* stream);
+
+/*
+ * Attention of the step's new tokens over their sequences' pages in one layer:
+ * for the token at position p of its sequence and query head h (which reads kv
+ * head h / (heads/kv_heads)),
+ *   out = sum_j a_j v_j / sum_j a_j,   a_j = exp(scale q.k_j - max),
+ * over the positions j <= p and, with window > 0, only j > p - window or
+ * j < sinks (a sliding window, and first tokens that stay visible). A token
+ * that sees nothing (a position below 0, a sequence id out of range) gets
+ * zeros. What no token sees (rows past a sequence's length, other sequences'
+ * pages) does not enter, whatever it holds, NaN and infinities included; table
+ * entries out of range read as zeros.
+ *   Q, out  device, [tokens][heads][head_dim] bf16, 16-byte aligned; rows of
+ *           out that belong to no sequence of the batch are left as they are
+ *   max_new the largest number of new tokens of a sequence, as far as the
+ *           caller knows it: it only selects between kernels
+ *   scale   > 0, finite; window, sinks >= 0 (sinks is ignored with window 0)
+ *   ws      see q4k_cache_workspace; ws_bytes its size
+ * heads/kv_heads <= 128; 1 <= n <= 4096; 1 <= tokens < 2^31 / heads.
+ * Accumulates in fp32; the weights a_j are rounded to bf16 for the product
+ * with V, as V is bf16 itself. The result does not depend on timing.
+ */
+int q4k_cache_attention(const q4k_cache* c, int layer, const int32_t* seqs, int n,
+                        const int32_t* starts, int64_t tokens, const uint16_t* Q, uint16_t* out,
+                        int heads, int max_new, float scale, int window, int sinks, void* ws,
+                        int64_t ws_bytes, void* stream);
+
+/*
+ * Makes room for a step's new tokens: sequence seqs[i] grows by starts[i+1] -
+ * starts[i] positions, with pages from the lowest free ones, given out in the
+ * order of i. status[i] (device): 0, or 1 where the pages left over (or width)
+ * do not suffice, or the id is out of range; such a sequence keeps its length
+ * and pages. (Pages are given while the running total of the batch's needs
+ * fits the free pages; a sequence that needs none always succeeds.)
+ * 1 <= n <= 4096.
+ */
+int q4k_pages_reserve(const q4k_cache* c, const int32_t* seqs, int n, const int32_t* starts,
+                      int32_t* status, void* stream);
+
+/*
+ * Forks: sequence children[i], which must have length 0, becomes a copy of
+ * parents[i]. Full pages are shared (refs + 1); a partly filled last page is
+ * copied, in every layer, to the lowest free page, in the order of i. status[i]
+ * (device): 0, or 1 where no page is left, the child is in use or an id is out
+ * of range (nothing changes for it). A parent may appear several times; a child
+ * appears once and is no parent of the same call. 1 <= n <= 4096.
+ */
+int q4k_pages_fork(const q4k_cache* c, const int32_t* parents, const int32_t* children, int n,
+                   int32_t* status, void* ws, int64_t ws_bytes, void* stream);
+
+/*
+ * Ends the n distinct sequences: their pages lose a reference, their lengths
+ * become 0 and their table rows -1. Ids out of range are skipped.
+ */
+int q4k_pages_free(const q4k_cache* c, const int32_t* seqs, int n, void* stream);
+
+/*
+ * Copies page src[i] to page dst[i] in every layer, K and V (device arrays;
+ * the pages of dst are distinct and none is in src; pairs with an id out of
+ * range are skipped). refs and table are the caller's business. n < 2^31.
+ */
+int q4k_pages_copy(const q4k_cache* c, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/*
+ * Moves the pages in use to the lowest ids: with L of them, the i-th free page
+ * below L takes the i-th used page from L on, in every layer; refs and table
+ * follow. Pages from L on are free afterwards.
+ */
+int q4k_pages_compact(const q4k_cache* c, void* ws, int64_t ws_bytes, void* stream);
+
+/*
+ * Adjusts M rows of V logits and picks the largest of each: for a token that
+ * occurs count > 0 times in its row's history,
+ *   x = x > 0 ? x / repeat : x * repeat;  x = (x - count*frequency) - presence;
+ * then x = x + bias where the row has one for the token, then -inf where the
+ * row's grammar forbids it. pick[m] is the lowest index with the largest x
+ * among the allowed ones (NaN below every number), or -1 if none is allowed.
+ * fp32, every operation rounded by itself.
+ *   logits    device, [M][V] floats, 16-byte aligned
+ *   out       device, [M][V] floats, 16-byte aligned, may be logits itself; NULL: not kept
+ *   pick      device, [M] int64; NULL: no pick (out and pick are not both NULL)
+ *   history   device, token ids of row m at hist_starts[m] .. hist_starts[m+1]-1
+ *             (M+1 ascending offsets); NULL: none. Ids out of range are ignored.
+ *   penalties device, [M][3]: repeat, presence, frequency; required with history
+ *   bias_ids, bias, bias_starts  device, ids and values of row m likewise; NULL:
+ *             none. Ids out of range are ignored; of an id given twice in a row
+ *             the later entry counts.
+ *   mask      device, [M][ceil(V/32)] words, bit v % 32 of word v / 32 set:
+ *             token v is allowed; NULL: all are
+ * 1 <= M <= 65535; 1 <= V < 2^31.
+ */
+int q4k_logits_pick(const float* logits, int64_t M, int64_t V, float* out, int64_t* pick,
+                    const int32_t* history, const int32_t* hist_starts, const float* penalties,
+                    const int32_t* bias_ids, const float* bias, const int32_t* bias_starts,
+                    const uint32_t* mask, void* stream);
 
 #ifdef __cplusplus
 }
