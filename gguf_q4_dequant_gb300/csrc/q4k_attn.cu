@@ -1,102 +1,597 @@
-// q4k_attn.cu -- attention of a step's new tokens over the pages of one layer.
+// q4k_attn.cu -- attention of a step's new tokens over the pages of one layer:
+// the chunk kernel, for many rows (tokens x query heads) per kv head.
 //
-// One warp per (token, head): 32 keys at a time, a lane each for the scores
-// (running maximum and sum over the blocks), then the lanes share the
-// dimensions of V for the weighted sum, over the visible keys only.
+// out = (sum_j 2^(s_j - r) v_j) / (sum_j 2^(s_j - r)) with s_j = scale log2(e)
+// q.k_j and a running reference r per row: r follows the row's largest score,
+// but only once it has grown by 2^8 or more, so that the accumulated sums are
+// rarely rescaled (the weights stay below 2^8, exact as far as fp32 and bf16 go).
+//
+// An item is 2 x 128 rows of one kv head: each half is whole tokens times the
+// G query heads that share the kv head, so every key and value tile (128
+// positions) is used by 256 rows. Two products per half and key tile, both
+// 128 x 128 x head_dim on tcgen05:
+//   S = Q K^T   Q and K from shared memory (K-major, 128-byte swizzle), S in TMEM
+//   O += P V    P (bf16) in TMEM over S's columns, V from shared memory as the
+//               pages hold it (rows are k: MN-major)
+// While the tensor core works for one half, the other half's 128 threads (one
+// row each) turn S into P: the two halves take turns.
+//
+// Warp roles: 0-3 softmax of half 0, 4-7 of half 1, 8 TMA producer (pages of
+// K and V tiles, Q), 9 MMA issuer. K and V tiles go through one ring of
+// buffers, filled page by page: the tensor map's last coordinate is the page,
+// and pages past a sequence's end are asked for at page -1, which fills zeros.
+//
+// Values that no row may see can be NaN (pages are not cleared): scores are
+// selected, not added to, and V tiles that some row sees only in part are
+// searched for infinities and NaN, which are zeroed in shared memory and added
+// back, at the end, to the rows that do see them.
 #include <cuda_bf16.h>
 
-#include "q4k_device.cuh"
-#include "q4k_serve.h"
+#include "q4k_attn.cuh"
 
 namespace q4k {
 
-constexpr int kAttnWarps = 4;
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+constexpr int kChunkKeys = 128;
+constexpr int kChunkThreads = 384;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kAttnWarps)
-    q4k_attn_simple_kernel(const CacheLayer c, const Batch b, const uint16_t* __restrict__ Q,
-                           uint16_t* __restrict__ out, int heads, float scale, int window, int sinks) {
-    __shared__ float q_s[kAttnWarps][D];
+struct ChunkCfg {
+    static constexpr int kHalves = D / 64;                 // 64-element column blocks of a row
+    static constexpr int kTileBytes = kChunkKeys * D * 2;  // one K or V tile, one half of Q
+    static constexpr int kRing = D == 128 ? 5 : 8;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffRing = 2 * kTileBytes;
+    static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
+    // full[kRing] empty[kRing] qfull qempty sfull[2] pfull[2] ofull[2] wg[2] fin
+    static constexpr int kNumBars = 2 * kRing + 11;
+    static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // walk, tmem address, flags
+    static constexpr int kMiscBytes = 160;
+    static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;  // + alignment slack
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kMaxBatch * 8 <= kRing * kTileBytes, "the plan's scratch is the ring");
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kColS = 0, kColO = 256;        // S (and P) 2 x 128, O 2 x D
+    static constexpr int kPartFloats = (D + 2) * 128;        // a partial result of one half
+};
+
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    q4k_attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_q,
+                          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    using Cfg = ChunkCfg<D>;
+    constexpr int KT = kChunkKeys, R = Cfg::kRing;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t b_full = sbase + Cfg::kOffBar;
+    const uint32_t b_empty = b_full + 8 * R;
+    const uint32_t b_qfull = b_empty + 8 * R;
+    const uint32_t b_qempty = b_qfull + 8;
+    const uint32_t b_sfull = b_qempty + 8;
+    const uint32_t b_pfull = b_sfull + 16;
+    const uint32_t b_ofull = b_pfull + 16;
+    const uint32_t b_wg = b_ofull + 16;
+    const uint32_t b_fin = b_wg + 16;
+    AttnWalk* walk_s = reinterpret_cast<AttnWalk*>(smem + Cfg::kOffMisc);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 96);
+    volatile int* poison = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 112);  // [4] item tags
+    volatile int* last_s = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 128);  // [2]
+    static_assert(sizeof(AttnWalk) <= 96, "walk");
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R; ++i) {
+            mbar_init(b_full + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 1);
+        }
+        mbar_init(b_qfull, 1);
+        mbar_init(b_qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_sfull + 8 * i, 1);
+            mbar_init(b_pfull + 8 * i, 128);
+            mbar_init(b_ofull + 8 * i, 1);
+            mbar_init(b_wg + 8 * i, 128);
+            poison[2 * i] = poison[2 * i + 1] = 0;
+        }
+        mbar_init(b_fin, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), Cfg::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kAttnWarps + warp;
-    if (item >= static_cast<int64_t>(b.tokens) * heads) return;
-    const int t = static_cast<int>(item / heads), h = static_cast<int>(item % heads);
-    int i = 0;
-    for (int j = lane; j < b.n; j += 32) i += b.starts[j + 1] <= t;
-    i = __reduce_add_sync(0xffffffffu, i);
-    if (i >= b.n) return;
-    const SeqView s = seq_view(c, b, i);
-    if (t < s.t0 || t >= s.t0 + s.m) return;
-    const int p = s.len - s.m + (t - s.t0);
-    const int g = h / (heads / c.kv_heads);
-    for (int d = lane; d < D; d += 32) q_s[warp][d] = bf16_lo(Q[item * D + d]);
-    __syncwarp();
-    float acc[D / 32], top = -INFINITY, total = 0.f;
-    for (int d = 0; d < D / 32; ++d) acc[d] = 0.f;
-    const int mask = (1 << c.page_shift) - 1;
-    for (int j0 = 0; j0 <= p; j0 += 32) {
-        if (window > 0 && j0 >= sinks && j0 + 31 <= p - window) continue;
-        const int j = j0 + lane;
-        const bool sees = j <= p && (window == 0 || j > p - window || j < sinks);
-        int page = sees ? c.table[s.row + (j >> c.page_shift)] : -1;
-        if (page >= c.n_pages) page = -1;
-        const int64_t off = page < 0 ? -1 : page * c.page_stride + ((static_cast<int64_t>(g) << c.page_shift) + (j & mask)) * D;
-        float x = -INFINITY;
-        if (sees) {
-            x = 0.f;
-            if (off >= 0)
-                for (int d = 0; d < D; d += 8) {
-                    const uint4 kv = *reinterpret_cast<const uint4*>(c.k + off + d);
-                    const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
-                    for (int e = 0; e < 4; ++e) {
-                        x = fmaf(bf16_lo(w[e]), q_s[warp][d + 2 * e], x);
-                        x = fmaf(bf16_hi(w[e]), q_s[warp][d + 2 * e + 1], x);
+    const int tph = 128 / p.group, tt = 2 * tph;  // tokens per half and per item
+    plan_units<KT>(p, tt, reinterpret_cast<int64_t*>(smem + Cfg::kOffRing), walk_s);
+    // the plan's scratch (generic accesses) becomes the ring (TMA writes)
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    AttnWalk w = *walk_s;
+    AttnItem it{};
+    if (threadIdx.x == 0) pdl_launch_dependents();
+
+    if (warp >= 8) {
+        regs_dec<56>();
+        if (warp == 8) {
+            // ------------------------------------------------ TMA producer ---
+            int slot = 0, n_items = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const int pages = KT >> p.c.page_shift;   // per key tile
+            const int boxes = pages * Cfg::kHalves;
+            const uint32_t page_bytes = 128u << p.c.page_shift;  // of one column block
+            auto load_tile = [&](const CUtensorMap* map, int tile) {
+                if (!__all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, phase ^ 1, p.err))) return false;
+                if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * slot, Cfg::kTileBytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    const int pg = lane % pages, cb = lane / pages;
+                    const int64_t idx = static_cast<int64_t>(tile) * pages + pg;
+                    int page = -1;
+                    if (idx << p.c.page_shift < it.len) page = p.c.table[it.row + idx];
+                    if (page < 0 || page >= p.c.n_pages) page = -1;
+                    tma_load_5d(sbase + Cfg::kOffRing + slot * Cfg::kTileBytes + cb * (KT * 128) + pg * page_bytes, map,
+                                0, 0, cb, it.h, page, b_full + 8 * slot);
+                }
+                ++issued;
+                if (++slot == R) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                return true;
+            };
+            while (ok && next_item<KT>(p, w, tt, it)) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_qempty, (n_items & 1) ^ 1, p.err));
+                if (!ok) break;
+                const int halves = it.tokens > tph ? 2 : 1;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(b_qfull, static_cast<uint32_t>(halves * tph * p.group * D * 2));
+                __syncwarp();
+                if (lane < halves * Cfg::kHalves) {
+                    const int hf = lane / Cfg::kHalves, cb = lane % Cfg::kHalves;
+                    tma_load_4d(sbase + Cfg::kOffQ + hf * Cfg::kTileBytes + cb * (128 * 128), &map_q, 0,
+                                it.h * p.group, it.t_first + hf * tph, cb, b_qfull);
+                }
+                ++n_items;
+                for (int i = it.i0; ok && i < it.i1; ++i) {
+                    const int tile = it.keys.tile(i);
+                    ok = load_tile(&map_k, tile) && load_tile(&map_v, tile);
+                }
+            }
+            // before the CTA may end, every copy has landed: at most the last R
+            // tiles and the last Q can be on their way
+            for (int k = 0; k < R && k < issued; ++k) {
+                if (slot == 0) phase ^= 1;
+                slot = slot == 0 ? R - 1 : slot - 1;
+                mbar_wait(b_full + 8 * slot, phase, p.err, kDrainLimitNs);
+            }
+            if (n_items > 0) mbar_wait(b_qfull, (n_items - 1) & 1, p.err, kDrainLimitNs);
+        } else if (warp == 9) {
+            // -------------------------------------------------- MMA issuer ---
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, KT);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
+            int n_items = 0, slot = 0;
+            uint32_t phase = 0, p_phase[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t ph) {
+                const bool r = __all_sync(0xffffffffu, mbar_wait(bar, ph, p.err));
+                tc_fence_after();
+                return r;
+            };
+            auto scores = [&](int hf, int kslot) {  // S = Q K^T
+                if (elect_one()) {
+#pragma unroll
+                    for (int cb = 0; cb < Cfg::kHalves; ++cb) {
+                        const uint64_t a = sw128_desc(sbase + Cfg::kOffQ + hf * Cfg::kTileBytes + cb * (128 * 128));
+                        const uint64_t b = sw128_desc(sbase + Cfg::kOffRing + kslot * Cfg::kTileBytes + cb * (KT * 128));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_bf16(tmem + Cfg::kColS + hf * 128, a + 2 * kk, b + 2 * kk, idesc_s, cb + kk > 0);
+                    }
+                    tc_commit(b_sfull + 8 * hf);
+                }
+                __syncwarp();
+            };
+            auto values = [&](int hf, int vslot, bool first) {  // O += P V
+                if (elect_one()) {
+                    const uint64_t b = sw128_desc_mn(sbase + Cfg::kOffRing + vslot * Cfg::kTileBytes, KT * 128);
+#pragma unroll
+                    for (int kk = 0; kk < KT / 16; ++kk)
+                        tc_mma_bf16_ts(tmem + Cfg::kColO + hf * D, tmem + Cfg::kColS + hf * 128 + 8 * kk,
+                                       b + kk * (16 * 128 / 16), idesc_o, !first || kk > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint32_t bar) {
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            while (ok && next_item<KT>(p, w, tt, it)) {
+                const int halves = it.tokens > tph ? 2 : 1, n = it.i1 - it.i0;
+                ok = wait(b_qfull, n_items & 1) && wait(b_full + 8 * slot, phase);
+                if (!ok) break;
+                for (int hf = 0; hf < halves; ++hf) scores(hf, slot);
+                commit(b_empty + 8 * slot);
+                if (n == 1) commit(b_qempty);
+                for (int j = 0; ok && j < n; ++j) {
+                    int vslot = slot + 1 == R ? 0 : slot + 1;
+                    const uint32_t vphase = vslot == 0 ? phase ^ 1 : phase;
+                    int kslot = vslot + 1 == R ? 0 : vslot + 1;
+                    const uint32_t kphase = kslot == 0 ? vphase ^ 1 : vphase;
+                    const bool more = j + 1 < n;
+                    ok = wait(b_full + 8 * vslot, vphase);
+                    if (ok && more) ok = wait(b_full + 8 * kslot, kphase);
+                    for (int hf = 0; ok && hf < halves; ++hf) {
+                        ok = wait(b_pfull + 8 * hf, p_phase[hf]);
+                        if (!ok) break;
+                        p_phase[hf] ^= 1;
+                        values(hf, vslot, j == 0);
+                        if (more)
+                            scores(hf, kslot);
+                        else
+                            commit(b_ofull + 8 * hf);
+                    }
+                    if (!ok) break;
+                    commit(b_empty + 8 * vslot);
+                    slot = vslot;
+                    phase = vphase;
+                    if (more) {
+                        commit(b_empty + 8 * kslot);
+                        if (j + 2 == n) commit(b_qempty);
+                        slot = kslot;
+                        phase = kphase;
                     }
                 }
-            x *= scale;
+                if (++slot == R) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                ++n_items;
+            }
+            commit(b_fin);  // every MMA of this CTA has completed
         }
-        float m = x;
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m = fmaxf(m, top);
-        const float base = m == -INFINITY ? 0.f : m;
-        const float keep = expf(top - base);
-        const float a = sees ? expf(x - base) : 0.f;
-        top = m;
-        total = total * keep + a;
-        for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
-        uint32_t vis = __ballot_sync(0xffffffffu, sees);
-        while (vis) {
-            const int l = __ffs(vis) - 1;
-            vis &= vis - 1;
-            const float al = __shfl_sync(0xffffffffu, a, l);
-            const int64_t ol = __shfl_sync(0xffffffffu, off, l);
-            if (ol >= 0)
-                for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(al, bf16_lo(c.v[ol + d * 32 + lane]), acc[d]);
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax ---
+        regs_inc<216>();
+        const int hf = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_base + Cfg::kColS + hf * 128;
+        const uint32_t t_o = tmem + lane_base + Cfg::kColO + hf * D;
+        const int tok = r / p.group, g = r % p.group;
+        int n_items = 0, slot = 0;  // ring position of the item's first V tile is slot + 1
+        uint32_t phase = 0, s_phase = 0, o_phase = 0, wg_phase = 0;
+        bool ok = true;
+        while (ok && next_item<KT>(p, w, tt, it)) {
+            const int n = it.i1 - it.i0;
+            ++n_items;
+            const int first_slot = slot;
+            const uint32_t first_phase = phase;
+            {  // 2n tiles on
+                const int at = slot + 2 * n;
+                phase ^= (at / R) & 1;
+                slot = at % R;
+            }
+            const int mine = min(it.tokens - hf * tph, tph);  // tokens of this half
+            if (mine <= 0) continue;
+            const int h0 = it.p0 + hf * tph, h1 = h0 + mine - 1;  // positions of the half's tokens
+            const int pos = tok < mine ? h0 + tok : -1;
+            float ref = -INFINITY, sum = 0.f;
+            for (int j = 0; j < n; ++j) {
+                const int tile = it.keys.tile(it.i0 + j);
+                const bool item_full = tile_is_full<KT>(tile, it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
+                if (!__all_sync(0xffffffffu, mbar_wait(b_sfull + 8 * hf, s_phase, p.err))) {
+                    ok = false;
+                    break;
+                }
+                s_phase ^= 1;
+                tc_fence_after();
+                uint32_t sv[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, sv[c]);
+                tmem_ld_wait();
+                if (!item_full) {
+                    if (!tile_is_full<KT>(tile, h0, h1, p.window, p.sinks)) {
+                        // columns of this tile that the row sees: [0, sink) and (low, high]
+                        const int j0 = tile * KT, high = pos - j0;
+                        const int low = p.window > 0 ? max(pos - p.window, -1) - j0 : -1;
+                        const int sink = p.window > 0 ? p.sinks - j0 : 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int col = 32 * c + e;
+                                if (!(col <= high && (col > low || col < sink))) sv[c][e] = 0xFF800000u;
+                            }
+                    }
+                    // V values that are not finite: zero here, and remembered for the end
+                    const int at = first_slot + 2 * j + 1, vslot = at % R;
+                    if (!__all_sync(0xffffffffu, mbar_wait(b_full + 8 * vslot, first_phase ^ ((at / R) & 1), p.err))) {
+                        ok = false;
+                        break;
+                    }
+                    uint4* v4 = reinterpret_cast<uint4*>(smem + Cfg::kOffRing + vslot * Cfg::kTileBytes);
+                    for (int e = r; e < Cfg::kTileBytes / 16; e += 128) {
+                        uint4 x = v4[e];
+                        uint32_t* xw = &x.x;
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) bad |= bf16x2_non_finite(xw[i]);
+                        if (bad) {
+                            poison[n_items & 3] = n_items;
+                            __threadfence_block();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t m = bf16x2_non_finite(xw[i]);
+                                xw[i] &= ~((m >> 15) * 0xFFFFu);
+                            }
+                            v4[e] = x;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sv[c][e]));
+                mx *= p.scale_log2;
+                const bool grow = mx > ref + 8.f || (ref == -INFINITY && mx > ref);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2(ref - mx) : 1.f;
+                    if (grow) ref = mx;
+                    sum *= f;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(t_o + 32 * c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st_32x32b_x32(t_o + 32 * c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.f : ref;
+                uint64_t acc = pack2(0.f, 0.f);
+                const uint64_t k2 = pack2(p.scale_log2, p.scale_log2), b2 = pack2(-base, -base);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = unpack2(fma2(
+                            pack2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), k2, b2));
+                        const float a0 = ex2(x.x), a1 = ex2(x.y);
+                        acc = add2(acc, pack2(a0, a1));
+                        const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);
+                        pw[e] = *reinterpret_cast<const uint32_t*>(&pr);
+                    }
+                    tmem_st_32x32b_x16(t_s + 16 * c, pw);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(b_pfull + 8 * hf);
+                const float2 a = unpack2(acc);
+                sum += a.x + a.y;
+            }
+            if (!ok) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(b_ofull + 8 * hf, o_phase, p.err))) {
+                ok = false;
+                break;
+            }
+            o_phase ^= 1;
+            tc_fence_after();
+            const bool fix = poison[n_items & 3] == n_items;
+            const bool whole = it.i0 == 0 && it.i1 == it.keys.n;
+            // the non-finite values that were zeroed, back into 32 columns of the rows that see them
+            auto add_back = [&](float (&o)[32], int c0) {
+                for (int j = 0; j < n; ++j) {
+                    const int tile = it.keys.tile(it.i0 + j);
+                    if (tile_is_full<KT>(tile, it.p0, it.p0 + it.tokens - 1, p.window, p.sinks)) continue;
+                    for (int k = 0; k < KT; ++k) {
+                        const int key = tile * KT + k;
+                        if (pos < 0 || !sees(pos, key, p.window, p.sinks)) continue;
+                        const int page = p.c.table[it.row + (key >> p.c.page_shift)];
+                        if (page < 0 || page >= p.c.n_pages) continue;
+                        const uint16_t* v = p.c.v + page * p.c.page_stride +
+                                            ((static_cast<int64_t>(it.h) << p.c.page_shift) +
+                                             (key & ((1 << p.c.page_shift) - 1))) * D + c0;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
+                            if (!isfinite(x)) o[e] += x;
+                        }
+                    }
+                }
+            };
+            auto store = [&](const float (&o)[32], int c0, float inv) {
+                if (tok >= mine || r >= tph * p.group) return;
+                uint16_t* dst = p.out + (static_cast<int64_t>(it.t_first + hf * tph + tok) * p.heads +
+                                         it.h * p.group + g) * D + c0;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 q = __floats2bfloat162_rn(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
+                        y[i] = *reinterpret_cast<const uint32_t*>(&q);
+                    }
+                    *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            };
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32];
+                    float o[32];
+                    tmem_ld_32x32b_x32(t_o + 32 * c, ov);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
+                    if (fix) add_back(o, 32 * c);
+                    store(o, 32 * c, inv);
+                }
+                continue;
+            }
+            // part of a row tile: the partial sums go to the scratch, the last
+            // CTA to arrive adds them up in the CTAs' order
+            const AttnSplit sp = item_split(it, w.q);
+            auto part = [&](int cta) {
+                return p.scratch + (static_cast<int64_t>(sp.slot(cta)) * 2 + hf) * Cfg::kPartFloats;
+            };
+            float* out_part = part(blockIdx.x);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                float o[32];
+                tmem_ld_32x32b_x32(t_o + 32 * c, ov);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
+                if (fix) add_back(o, 32 * c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) __stcg(out_part + (32 * c + e) * 128 + r, o[e]);
+            }
+            __stcg(out_part + D * 128 + r, ref);
+            __stcg(out_part + (D + 1) * 128 + r, sum);
+            __threadfence();
+            auto wg_sync = [&] {
+                mbar_arrive(b_wg + 8 * hf);
+                const bool done = __all_sync(0xffffffffu, mbar_wait(b_wg + 8 * hf, wg_phase, p.err));
+                wg_phase ^= 1;
+                return done;
+            };
+            if (!(ok = wg_sync())) break;
+            if (r == 0) {
+                uint32_t* count = p.counters + 2 * sp.first + hf;
+                const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(sp.last - sp.first);
+                if (last) *count = 0u;  // as the next call expects it
+                __threadfence();
+                last_s[hf] = last;
+            }
+            if (!(ok = wg_sync())) break;
+            if (!last_s[hf]) continue;
+            float top = -INFINITY;
+            for (int cta = sp.first; cta <= sp.last; ++cta) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
+            const float zero_ref = top == -INFINITY ? 0.f : top;
+            float all = 0.f;
+            for (int cta = sp.first; cta <= sp.last; ++cta)
+                all += __ldcg(part(cta) + (D + 1) * 128 + r) * ex2(__ldcg(part(cta) + D * 128 + r) - zero_ref);
+            const float inv = all == 0.f ? 0.f : 1.f / all;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                for (int cta = sp.first; cta <= sp.last; ++cta) {
+                    const float* from = part(cta);
+                    const float f = ex2(__ldcg(from + D * 128 + r) - zero_ref);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(from + (32 * c + e) * 128 + r), f, o[e]);
+                }
+                store(o, 32 * c, inv);
+            }
         }
     }
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    for (int d = 0; d < D / 32; ++d) {
-        const __nv_bfloat16 y = __float2bfloat16_rn(total == 0.f ? 0.f : acc[d] / total);
-        out[item * D + d * 32 + lane] = __bfloat16_as_ushort(y);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        mbar_wait(b_fin, 0, p.err);
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::kTmemCols);
     }
+}
+
+// ------------------------------------------------------------------ host ---
+
+// K or V of one layer: {64 of head_dim, row of the page, column block, kv head, page}.
+static bool encode_pages(CUtensorMap* map, const uint16_t* base, const CacheLayer& c, int head_dim) {
+    const int page = 1 << c.page_shift;
+    const uint64_t dims[5] = {64, static_cast<uint64_t>(page), static_cast<uint64_t>(head_dim / 64),
+                              static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(c.n_pages)};
+    const uint64_t strides[4] = {static_cast<uint64_t>(head_dim) * 2, 128,
+                                 static_cast<uint64_t>(page) * head_dim * 2,
+                                 static_cast<uint64_t>(c.page_stride) * 2};
+    const uint32_t box[5] = {64, static_cast<uint32_t>(page), 1, 1, 1};
+    return encode_bf16_sw128(map, base, 5, dims, strides, box);
+}
+
+// Q: {64 of head_dim, query head, token, column block}; a box is the rows of half an item.
+static bool encode_q(CUtensorMap* map, const AttnArgs& a, int tokens, int group) {
+    const uint64_t row = static_cast<uint64_t>(a.head_dim) * 2;
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(a.heads), static_cast<uint64_t>(tokens),
+                              static_cast<uint64_t>(a.head_dim / 64)};
+    const uint64_t strides[3] = {row, row * a.heads, 128};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(group), static_cast<uint32_t>(128 / group), 1};
+    return encode_bf16_sw128(map, a.Q, 4, dims, strides, box);
+}
+
+template <int D>
+static cudaError_t launch_chunk(const AttnParams& p, const AttnArgs& a, cudaStream_t stream, const DeviceInfo& dev,
+                                int pdl) {
+    CUtensorMap mq, mk, mv;
+    if (!encode_q(&mq, a, p.b.tokens, p.group) || !encode_pages(&mk, p.c.k, p.c, D) ||
+        !encode_pages(&mv, p.c.v, p.c, D))
+        return cudaErrorInvalidValue;
+    return launch_serve(q4k_attn_chunk_kernel<D>, dim3(dev.num_sms), dim3(kChunkThreads), ChunkCfg<D>::kSmem, stream,
+                        pdl, 1, p, mq, mk, mv);
 }
 
 cudaError_t launch_attention(const CacheLayer& c, const Batch& b, const AttnArgs& a, int max_new,
                              cudaStream_t stream, const DeviceInfo& dev, int pdl) {
     (void)max_new;
-    (void)dev;
-    auto kernel = a.head_dim == 64 ? q4k_attn_simple_kernel<64> : q4k_attn_simple_kernel<128>;
-    const int64_t items = static_cast<int64_t>(b.tokens) * a.heads;
-    return launch_serve(kernel, dim3(static_cast<unsigned>((items + kAttnWarps - 1) / kAttnWarps)),
-                        dim3(32 * kAttnWarps), 0, stream, pdl, 1, c, b, a.Q, a.out, a.heads, a.scale, a.window,
-                        a.sinks);
+    AttnParams p;
+    p.c = c;
+    p.b = b;
+    p.out = a.out;
+    p.Q = a.Q;
+    p.heads = a.heads;
+    p.group = a.heads / c.kv_heads;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.counters = a.counters;
+    p.scratch = static_cast<float*>(a.scratch);
+    p.err = dev.err;
+    return a.head_dim == 64 ? launch_chunk<64>(p, a, stream, dev, pdl) : launch_chunk<128>(p, a, stream, dev, pdl);
 }
 
-int64_t attn_scratch_bytes(const DeviceInfo&, int) { return 0; }
-cudaError_t attn_setup(DeviceInfo&) { return cudaSuccess; }
+int64_t attn_scratch_bytes(const DeviceInfo& dev, int head_dim) {
+    const int64_t part = head_dim == 64 ? ChunkCfg<64>::kPartFloats : ChunkCfg<128>::kPartFloats;
+    return static_cast<int64_t>(dev.num_sms) * 4 * part * 4;
+}
+
+cudaError_t attn_setup(DeviceInfo& dev) {
+    if (2 * dev.num_sms > kPageTicket) return cudaErrorInvalidValue;  // counters of the workspace
+    cudaError_t e = cudaFuncSetAttribute(q4k_attn_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         ChunkCfg<64>::kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(q4k_attn_chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ChunkCfg<128>::kSmem);
+}
 
 }  // namespace q4k

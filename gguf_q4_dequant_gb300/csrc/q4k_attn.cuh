@@ -1,0 +1,231 @@
+// q4k_attn.cuh -- how the attention kernels share out a step's work.
+//
+// The rows of a kv head (its G query heads of each new token) are cut into row
+// tiles of whole tokens, the positions into key tiles. One unit of work is one
+// (row tile, key tile) that the mask does not rule out; the units of all
+// sequences, kv heads and row tiles are numbered in that order, and CTA c of
+// the grid takes units [c*q, (c+1)*q) with q = ceil(total / grid). So every CTA
+// has the same number of key tiles whatever the sequences' lengths are, on the
+// device's own numbers. A row tile that lies in several CTAs' ranges is put
+// together from their partial results by whichever of them finishes last, in
+// the order of the CTAs: the result does not depend on which one that is.
+#pragma once
+
+#include "q4k_device.cuh"
+#include "q4k_serve.h"
+
+namespace q4k {
+
+struct AttnParams {
+    CacheLayer c;
+    Batch b;
+    uint16_t* out;
+    const uint16_t* Q;
+    int heads, group;     // query heads; query heads per kv head
+    float scale_log2;     // scale * log2(e): weights are 2^(s * scale_log2 - reference)
+    int window, sinks;
+    uint32_t* counters;
+    float* scratch;
+    unsigned int* err;
+};
+
+// Key tiles that some row of a row tile with positions p0 .. p1 sees: tiles
+// 0 .. st-1 (first tokens), then w0, w0 + 1, ...; n in all, at least 1 (a row
+// tile that sees nothing still writes its zeros).
+struct KeyTiles {
+    int st, w0, n;
+    __device__ __forceinline__ int tile(int i) const { return i < st ? i : w0 + (i - st); }
+};
+
+template <int KT>
+__device__ __forceinline__ KeyTiles key_tiles(int p0, int p1, int window, int sinks) {
+    KeyTiles k{0, 0, 1};
+    if (p1 < 0) return k;
+    const int end = p1 / KT + 1;
+    if (window > 0) {
+        const int64_t lo = static_cast<int64_t>(p0) - window + 1;
+        k.w0 = lo > 0 ? static_cast<int>(lo) / KT : 0;
+        k.st = min((min(sinks, p1 + 1) + KT - 1) / KT, k.w0);
+    }
+    k.n = k.st + end - k.w0;
+    return k;
+}
+
+// Every row with a position in p0 .. p1 sees every key of the tile.
+template <int KT>
+__device__ __forceinline__ bool tile_is_full(int tile, int p0, int p1, int window, int sinks) {
+    const int j0 = tile * KT, j1 = j0 + KT - 1;
+    return j1 <= p0 && (window == 0 || j0 > p1 - window || j1 < sinks);
+}
+
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
+    return j <= p && (window == 0 || j > p - window || j < sinks);
+}
+
+// What one CTA does, item by item.
+struct AttnItem {
+    int t_first, tokens;  // rows of the step's arrays
+    int p0;               // position of the first token (negative: sees nothing)
+    int h;                // kv head
+    int64_t row;          // the sequence's row of the table
+    int len;
+    KeyTiles keys;
+    int i0, i1;           // this CTA's part of the key tiles' list
+    int64_t u0;           // number of the row tile's first unit
+};
+
+struct AttnWalk {
+    int64_t u, u_end;  // units left to do
+    int64_t q;
+    int b, h, tile, off;
+    SeqView s;
+};
+
+// The next item, or false. `tt`: tokens of a row tile.
+template <int KT>
+__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, AttnItem& it) {
+    if (w.u >= w.u_end) return false;
+    while (w.tile * tt >= w.s.m) {  // the sequence's row tiles are done for this head
+        w.tile = 0;
+        if (w.s.m == 0 || ++w.h == p.c.kv_heads) {
+            w.h = 0;
+            w.s = seq_view(p.c, p.b, ++w.b);  // exists: there are units left
+        }
+    }
+    it.t_first = w.s.t0 + w.tile * tt;
+    it.tokens = min(tt, w.s.m - w.tile * tt);
+    it.p0 = w.s.len - w.s.m + w.tile * tt;
+    it.h = w.h;
+    it.row = w.s.row;
+    it.len = w.s.len;
+    it.keys = key_tiles<KT>(it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
+    it.i0 = w.off;
+    it.i1 = static_cast<int>(min(static_cast<int64_t>(it.keys.n), it.i0 + (w.u_end - w.u)));
+    it.u0 = w.u - it.i0;
+    w.u += it.i1 - it.i0;
+    w.off = 0;
+    ++w.tile;
+    return true;
+}
+
+// Units of the row tiles of one sequence and kv head.
+template <int KT>
+__device__ __forceinline__ int64_t tile_units(const AttnParams& p, const SeqView& s, int tile, int tt) {
+    const int p0 = s.len - s.m + tile * tt;
+    return key_tiles<KT>(p0, p0 + min(tt, s.m - tile * tt) - 1, p.window, p.sinks).n;
+}
+
+// The CTA's range, found by all threads of the block: `units` holds n words of
+// shared memory, `found` takes the result. Ends with __syncthreads().
+template <int KT>
+__device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int64_t* units, AttnWalk* found) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
+        const int i = i0 + lane;
+        SeqView s{0, 0, 0, 0};
+        if (i < p.b.n) s = seq_view(p.c, p.b, i);
+        const int tiles = (s.m + tt - 1) / tt;
+        int64_t u = 0;
+        if (tiles <= 4)
+            for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
+        // many row tiles: the warp counts them together
+        uint32_t many = __ballot_sync(0xffffffffu, tiles > 4);
+        while (many) {
+            const int l = __ffs(many) - 1;
+            many &= many - 1;
+            SeqView o;
+            o.m = __shfl_sync(0xffffffffu, s.m, l);
+            o.len = __shfl_sync(0xffffffffu, s.len, l);
+            const int ot = (o.m + tt - 1) / tt;
+            int64_t x = 0;
+            for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+            if (lane == l) u = x;
+        }
+        if (i < p.b.n) units[i] = u * p.c.kv_heads;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t total = 0;
+        for (int i = lane; i < p.b.n; i += 32) total += units[i];
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+        AttnWalk w;
+        w.q = (total + gridDim.x - 1) / gridDim.x;
+        w.u = blockIdx.x * w.q;
+        w.u_end = min(total, w.u + w.q);
+        w.b = w.h = w.tile = w.off = 0;
+        w.s = SeqView{0, 0, 0, 0};
+        if (w.u < w.u_end) {
+            int64_t at = 0;
+            for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+                const int64_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0;
+                int64_t incl = mine;
+#pragma unroll
+                for (int k = 1; k < 32; k <<= 1) {
+                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, k);
+                    if (lane >= k) incl += v;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, at + incl > w.u);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    w.b = i0 + l;
+                    at += __shfl_sync(0xffffffffu, incl - mine, l);
+                    break;
+                }
+                at += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            w.s = seq_view(p.c, p.b, w.b);
+            const int64_t per_head = units[w.b] / p.c.kv_heads;
+            w.h = static_cast<int>((w.u - at) / per_head);
+            int64_t rest = (w.u - at) - w.h * per_head;
+            for (int t0 = 0;; t0 += 32) {
+                const int64_t mine = (t0 + lane) * tt < w.s.m ? tile_units<KT>(p, w.s, t0 + lane, tt) : 0;
+                int64_t incl = mine;
+#pragma unroll
+                for (int k = 1; k < 32; k <<= 1) {
+                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, k);
+                    if (lane >= k) incl += v;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, incl > rest);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    w.tile = t0 + l;
+                    w.off = static_cast<int>(rest - __shfl_sync(0xffffffffu, incl - mine, l));
+                    break;
+                }
+                rest -= __shfl_sync(0xffffffffu, incl, 31);
+                if ((t0 + 32) * static_cast<int64_t>(tt) >= w.s.m) break;  // not reached: the units add up
+            }
+        }
+        if (lane == 0) *found = w;
+    }
+    __syncthreads();
+}
+
+// Where a partial result goes. CTA c has at most two split row tiles: one that
+// began in an earlier CTA (slot 0) and one that goes on in a later (slot 1).
+struct AttnSplit {
+    int first, last;  // CTAs that share the row tile
+    __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (cta == first); }
+};
+
+__device__ __forceinline__ AttnSplit item_split(const AttnItem& it, int64_t q) {
+    return AttnSplit{static_cast<int>(it.u0 / q), static_cast<int>((it.u0 + it.keys.n - 1) / q)};
+}
+
+// 2^x by the special function unit (flushes subnormal results to zero, which a
+// softmax weight may be).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bit 15 and 31: that half of a bf16 pair is an infinity or NaN.
+__device__ __forceinline__ uint32_t bf16x2_non_finite(uint32_t w) {
+    return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+}  // namespace q4k
