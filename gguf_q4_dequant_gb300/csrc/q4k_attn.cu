@@ -528,18 +528,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
 // ------------------------------------------------------------------ host ---
 
-// K or V of one layer: {64 of head_dim, row of the page, column block, kv head, page}.
-static bool encode_pages(CUtensorMap* map, const uint16_t* base, const CacheLayer& c, int head_dim) {
-    const int page = 1 << c.page_shift;
-    const uint64_t dims[5] = {64, static_cast<uint64_t>(page), static_cast<uint64_t>(head_dim / 64),
-                              static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(c.n_pages)};
-    const uint64_t strides[4] = {static_cast<uint64_t>(head_dim) * 2, 128,
-                                 static_cast<uint64_t>(page) * head_dim * 2,
-                                 static_cast<uint64_t>(c.page_stride) * 2};
-    const uint32_t box[5] = {64, static_cast<uint32_t>(page), 1, 1, 1};
-    return encode_bf16_sw128(map, base, 5, dims, strides, box);
-}
-
 // Q: {64 of head_dim, query head, token, column block}; a box is the rows of half an item.
 static bool encode_q(CUtensorMap* map, const AttnArgs& a, int tokens, int group) {
     const uint64_t row = static_cast<uint64_t>(a.head_dim) * 2;
@@ -554,8 +542,8 @@ template <int D>
 static cudaError_t launch_chunk(const AttnParams& p, const AttnArgs& a, cudaStream_t stream, const DeviceInfo& dev,
                                 int pdl) {
     CUtensorMap mq, mk, mv;
-    if (!encode_q(&mq, a, p.b.tokens, p.group) || !encode_pages(&mk, p.c.k, p.c, D) ||
-        !encode_pages(&mv, p.c.v, p.c, D))
+    if (!encode_q(&mq, a, p.b.tokens, p.group) || !encode_pages(&mk, p.c.k, p.c, D, 1) ||
+        !encode_pages(&mv, p.c.v, p.c, D, 1))
         return cudaErrorInvalidValue;
     return launch_serve(q4k_attn_chunk_kernel<D>, dim3(dev.num_sms), dim3(kChunkThreads), ChunkCfg<D>::kSmem, stream,
                         pdl, 1, p, mq, mk, mv);
@@ -563,7 +551,6 @@ static cudaError_t launch_chunk(const AttnParams& p, const AttnArgs& a, cudaStre
 
 cudaError_t launch_attention(const CacheLayer& c, const Batch& b, const AttnArgs& a, int max_new,
                              cudaStream_t stream, const DeviceInfo& dev, int pdl) {
-    (void)max_new;
     AttnParams p;
     p.c = c;
     p.b = b;
@@ -577,6 +564,10 @@ cudaError_t launch_attention(const CacheLayer& c, const Batch& b, const AttnArgs
     p.counters = a.counters;
     p.scratch = static_cast<float*>(a.scratch);
     p.err = dev.err;
+    // at most one row tile of 16 per sequence and kv head: bound by the memory,
+    // not by the tensor core
+    if (static_cast<int64_t>(max_new) * p.group <= 16 && p.group <= 16)
+        return launch_attn_decode(p, a.head_dim, stream, dev, pdl);
     return a.head_dim == 64 ? launch_chunk<64>(p, a, stream, dev, pdl) : launch_chunk<128>(p, a, stream, dev, pdl);
 }
 
@@ -587,7 +578,9 @@ int64_t attn_scratch_bytes(const DeviceInfo& dev, int head_dim) {
 
 cudaError_t attn_setup(DeviceInfo& dev) {
     if (2 * dev.num_sms > kPageTicket) return cudaErrorInvalidValue;  // counters of the workspace
-    cudaError_t e = cudaFuncSetAttribute(q4k_attn_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = attn_decode_setup();
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(q4k_attn_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          ChunkCfg<64>::kSmem);
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(q4k_attn_chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -215,6 +215,23 @@ __device__ __forceinline__ AttnSplit item_split(const AttnItem& it, int64_t q) {
     return AttnSplit{static_cast<int>(it.u0 / q), static_cast<int>((it.u0 + it.keys.n - 1) / q)};
 }
 
+// K or V of one layer as a tensor map: {64 of head_dim, row of the page, column
+// block, kv head, page}; a box is `blocks` column blocks of one page of one head.
+inline bool encode_pages(CUtensorMap* map, const uint16_t* base, const CacheLayer& c, int head_dim, int blocks) {
+    const int page = 1 << c.page_shift;
+    const uint64_t dims[5] = {64, static_cast<uint64_t>(page), static_cast<uint64_t>(head_dim / 64),
+                              static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(c.n_pages)};
+    const uint64_t strides[4] = {static_cast<uint64_t>(head_dim) * 2, 128,
+                                 static_cast<uint64_t>(page) * head_dim * 2,
+                                 static_cast<uint64_t>(c.page_stride) * 2};
+    const uint32_t box[5] = {64, static_cast<uint32_t>(page), static_cast<uint32_t>(blocks), 1, 1};
+    return encode_bf16_sw128(map, base, 5, dims, strides, box);
+}
+
+// The kernel for few rows per kv head (group <= 16).
+cudaError_t launch_attn_decode(const AttnParams& p, int head_dim, cudaStream_t stream, const DeviceInfo& dev, int pdl);
+cudaError_t attn_decode_setup();
+
 // 2^x by the special function unit (flushes subnormal results to zero, which a
 // softmax weight may be).
 __device__ __forceinline__ float ex2(float x) {
