@@ -42,10 +42,10 @@ struct ChunkCfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = 2 * kTileBytes;
     static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
-    // full[kRing] empty[kRing] qfull qempty sfull[2] pfull[2] ofull[2] wg[2] fin
-    static constexpr int kNumBars = 2 * kRing + 11;
-    static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // walk, tmem address, flags
-    static constexpr int kMiscBytes = 160;
+    // full[kRing] empty[kRing] qfull qempty sfull[2] pfull[2] ofull[2] wg[2] fin ifull[kItemRing] iempty[kItemRing]
+    static constexpr int kNumBars = 2 * kRing + 11 + 2 * kItemRing;
+    static constexpr int kOffMisc = kOffBar + 8 * ((kNumBars + 1) / 2 * 2);  // walk, tmem address, flags, items
+    static constexpr int kMiscBytes = 144 + kItemRing * sizeof(AttnItem);
     static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(kMaxBatch * 8 <= kRing * kTileBytes, "the plan's scratch is the ring");
@@ -85,11 +85,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t b_ofull = b_pfull + 16;
     const uint32_t b_wg = b_ofull + 16;
     const uint32_t b_fin = b_wg + 16;
+    const uint32_t b_ifull = b_fin + 8;
+    const uint32_t b_iempty = b_ifull + 8 * kItemRing;
     AttnWalk* walk_s = reinterpret_cast<AttnWalk*>(smem + Cfg::kOffMisc);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 96);
     volatile int* poison = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 112);  // [4] item tags
     volatile int* last_s = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 128);  // [2]
-    static_assert(sizeof(AttnWalk) <= 96, "walk");
+    AttnItem* items = reinterpret_cast<AttnItem*>(smem + Cfg::kOffMisc + 144);
+    static_assert(sizeof(AttnWalk) <= 96 && sizeof(AttnItem) % 8 == 0, "layout");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
@@ -106,6 +109,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             poison[2 * i] = poison[2 * i + 1] = 0;
         }
         mbar_init(b_fin, 1);
+        for (int i = 0; i < kItemRing; ++i) {
+            mbar_init(b_ifull + 8 * i, 1);
+            mbar_init(b_iempty + 8 * i, 9);  // the MMA warp and eight softmax warps
+        }
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -126,14 +133,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    AttnWalk w = *walk_s;
-    AttnItem it{};
     if (threadIdx.x == 0) pdl_launch_dependents();
 
     if (warp >= 8) {
-        regs_dec<56>();
+        regs_dec<72>();
         if (warp == 8) {
             // ------------------------------------------------ TMA producer ---
+            AttnWalk w = *walk_s;
+            AttnItem it{};
             int slot = 0, n_items = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -160,7 +167,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 return true;
             };
-            while (ok && next_item<KT>(p, w, tt, it)) {
+            for (;;) {
+                const bool more = next_item<KT>(p, w, tt, it);
+                const int k = n_items % kItemRing;
+                ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
+                if (!ok) break;
+                if (lane == 0) {
+                    items[k] = it;
+                    mbar_arrive(b_ifull + 8 * k);
+                }
+                if (!more) break;
                 ok = __all_sync(0xffffffffu, mbar_wait(b_qempty, (n_items & 1) ^ 1, p.err));
                 if (!ok) break;
                 const int halves = it.tokens > tph ? 2 : 1;
@@ -177,6 +193,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const int tile = it.keys.tile(i);
                     ok = load_tile(&map_k, tile) && load_tile(&map_v, tile);
                 }
+                if (!ok) break;
             }
             // before the CTA may end, every copy has landed: at most the last R
             // tiles and the last Q can be on their way
@@ -226,8 +243,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (elect_one()) tc_commit(bar);
                 __syncwarp();
             };
-            while (ok && next_item<KT>(p, w, tt, it)) {
-                const int halves = it.tokens > tph ? 2 : 1, n = it.i1 - it.i0;
+            for (;;) {
+                const int ik = n_items % kItemRing;
+                ok = wait(b_ifull + 8 * ik, (n_items / kItemRing) & 1);
+                if (!ok) break;
+                const int halves = items[ik].tokens > tph ? 2 : 1, n = items[ik].i1 - items[ik].i0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_iempty + 8 * ik);
+                if (n == 0) break;
                 ok = wait(b_qfull, n_items & 1) && wait(b_full + 8 * slot, phase);
                 if (!ok) break;
                 for (int hf = 0; hf < halves; ++hf) scores(hf, slot);
@@ -262,6 +285,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         phase = kphase;
                     }
                 }
+                if (!ok) break;
                 if (++slot == R) {
                     slot = 0;
                     phase ^= 1;
@@ -282,8 +306,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int n_items = 0, slot = 0;  // ring position of the item's first V tile is slot + 1
         uint32_t phase = 0, s_phase = 0, o_phase = 0, wg_phase = 0;
         bool ok = true;
-        while (ok && next_item<KT>(p, w, tt, it)) {
+        for (;;) {
+            // done with the item before
+            __syncwarp();
+            if (n_items > 0 && lane == 0) mbar_arrive(b_iempty + 8 * ((n_items - 1) % kItemRing));
+            const int ik = n_items % kItemRing;
+            if (!__all_sync(0xffffffffu, mbar_wait(b_ifull + 8 * ik, (n_items / kItemRing) & 1, p.err))) break;
+            const AttnItem& it = items[ik];
             const int n = it.i1 - it.i0;
+            if (n == 0) break;
             ++n_items;
             const int first_slot = slot;
             const uint32_t first_phase = phase;
@@ -300,6 +331,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int j = 0; j < n; ++j) {
                 const int tile = it.keys.tile(it.i0 + j);
                 const bool item_full = tile_is_full<KT>(tile, it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
+                if (!item_full) {
+                    // V values that are not finite: zero here, and remembered for the end
+                    const int at = first_slot + 2 * j + 1, vslot = at % R;
+                    if (!__all_sync(0xffffffffu, mbar_wait(b_full + 8 * vslot, first_phase ^ ((at / R) & 1), p.err))) {
+                        ok = false;
+                        break;
+                    }
+                    uint4* v4 = reinterpret_cast<uint4*>(smem + Cfg::kOffRing + vslot * Cfg::kTileBytes) + r;
+#pragma unroll
+                    for (int e = 0; e < Cfg::kTileBytes / 16 / 128; e += 4) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = v4[128 * (e + i)];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 m = make_uint4(bf16x2_non_finite(x[i].x), bf16x2_non_finite(x[i].y),
+                                                       bf16x2_non_finite(x[i].z), bf16x2_non_finite(x[i].w));
+                            if ((m.x | m.y | m.z | m.w) == 0u) continue;
+                            poison[n_items & 3] = n_items;
+                            __threadfence_block();
+                            v4[128 * (e + i)] = make_uint4(x[i].x & ~((m.x >> 15) * 0xFFFFu), x[i].y & ~((m.y >> 15) * 0xFFFFu),
+                                                           x[i].z & ~((m.z >> 15) * 0xFFFFu), x[i].w & ~((m.w >> 15) * 0xFFFFu));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
                 if (!__all_sync(0xffffffffu, mbar_wait(b_sfull + 8 * hf, s_phase, p.err))) {
                     ok = false;
                     break;
@@ -310,45 +367,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, sv[c]);
                 tmem_ld_wait();
-                if (!item_full) {
-                    if (!tile_is_full<KT>(tile, h0, h1, p.window, p.sinks)) {
-                        // columns of this tile that the row sees: [0, sink) and (low, high]
-                        const int j0 = tile * KT, high = pos - j0;
-                        const int low = p.window > 0 ? max(pos - p.window, -1) - j0 : -1;
-                        const int sink = p.window > 0 ? p.sinks - j0 : 0;
+                if (!tile_is_full<KT>(tile, h0, h1, p.window, p.sinks)) {
+                    // columns of this tile that the row sees: [0, sink) and (low, high]
+                    const int j0 = tile * KT, high = pos - j0;
+                    const int low = p.window > 0 ? max(pos - p.window, -1) - j0 : -1;
+                    const int sink = p.window > 0 ? p.sinks - j0 : 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int col = 32 * c + e;
-                                if (!(col <= high && (col > low || col < sink))) sv[c][e] = 0xFF800000u;
-                            }
-                    }
-                    // V values that are not finite: zero here, and remembered for the end
-                    const int at = first_slot + 2 * j + 1, vslot = at % R;
-                    if (!__all_sync(0xffffffffu, mbar_wait(b_full + 8 * vslot, first_phase ^ ((at / R) & 1), p.err))) {
-                        ok = false;
-                        break;
-                    }
-                    uint4* v4 = reinterpret_cast<uint4*>(smem + Cfg::kOffRing + vslot * Cfg::kTileBytes);
-                    for (int e = r; e < Cfg::kTileBytes / 16; e += 128) {
-                        uint4 x = v4[e];
-                        uint32_t* xw = &x.x;
-                        uint32_t bad = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) bad |= bf16x2_non_finite(xw[i]);
-                        if (bad) {
-                            poison[n_items & 3] = n_items;
-                            __threadfence_block();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t m = bf16x2_non_finite(xw[i]);
-                                xw[i] &= ~((m >> 15) * 0xFFFFu);
-                            }
-                            v4[e] = x;
+                        for (int e = 0; e < 32; ++e) {
+                            const int col = 32 * c + e;
+                            if (!(col <= high && (col > low || col < sink))) sv[c][e] = 0xFF800000u;
                         }
-                    }
-                    fence_proxy_async_smem();
                 }
                 float mx = -INFINITY;
 #pragma unroll
@@ -459,9 +489,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             // part of a row tile: the partial sums go to the scratch, the last
             // CTA to arrive adds them up in the CTAs' order
-            const AttnSplit sp = item_split(it, w.q);
+            const int first = it.first, last = it.last;
             auto part = [&](int cta) {
-                return p.scratch + (static_cast<int64_t>(sp.slot(cta)) * 2 + hf) * Cfg::kPartFloats;
+                return p.scratch + (static_cast<int64_t>(it.slot(cta)) * 2 + hf) * Cfg::kPartFloats;
             };
             float* out_part = part(blockIdx.x);
 #pragma unroll 1
@@ -487,33 +517,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             };
             if (!(ok = wg_sync())) break;
             if (r == 0) {
-                uint32_t* count = p.counters + 2 * sp.first + hf;
-                const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(sp.last - sp.first);
-                if (last) *count = 0u;  // as the next call expects it
+                uint32_t* count = p.counters + 2 * first + hf;
+                const bool here = atomicAdd(count, 1u) == static_cast<uint32_t>(last - first);
+                if (here) *count = 0u;  // as the next call expects it
                 __threadfence();
-                last_s[hf] = last;
+                last_s[hf] = here;
             }
             if (!(ok = wg_sync())) break;
             if (!last_s[hf]) continue;
             float top = -INFINITY;
-            for (int cta = sp.first; cta <= sp.last; ++cta) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
+            for (int cta = first; cta <= last; ++cta) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
             const float zero_ref = top == -INFINITY ? 0.f : top;
             float all = 0.f;
-            for (int cta = sp.first; cta <= sp.last; ++cta)
+            for (int cta = first; cta <= last; ++cta)
                 all += __ldcg(part(cta) + (D + 1) * 128 + r) * ex2(__ldcg(part(cta) + D * 128 + r) - zero_ref);
             const float inv = all == 0.f ? 0.f : 1.f / all;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
+            for (int c = 0; c < D / 64; ++c) {  // 64 columns' loads at a time
+                float o[2][32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                for (int cta = sp.first; cta <= sp.last; ++cta) {
+                for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = 0.f;
+                for (int cta = first; cta <= last; ++cta) {
                     const float* from = part(cta);
+                    float x[64];
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) x[e] = __ldcg(from + (64 * c + e) * 128 + r);
                     const float f = ex2(__ldcg(from + D * 128 + r) - zero_ref);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(from + (32 * c + e) * 128 + r), f, o[e]);
+                    for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = fmaf(x[e], f, o[e >> 5][e & 31]);
                 }
-                store(o, 32 * c, inv);
+                store(o[0], 64 * c, inv);
+                store(o[1], 64 * c + 32, inv);
             }
         }
     }

@@ -71,8 +71,16 @@ struct AttnItem {
     int len;
     KeyTiles keys;
     int i0, i1;           // this CTA's part of the key tiles' list
-    int64_t u0;           // number of the row tile's first unit
+    int first, last;      // CTAs that share the row tile (equal: this one has all of it)
+
+    // Where a partial result goes: a CTA has at most two split row tiles, one
+    // that began in an earlier CTA (slot 0) and one that goes on in a later (slot 1).
+    __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (cta == first); }
 };
+
+// The producer warp works the items out and hands them to the other warps
+// through a small ring in shared memory; an item without key tiles is the end.
+constexpr int kItemRing = 4;
 
 struct AttnWalk {
     int64_t u, u_end;  // units left to do
@@ -84,6 +92,7 @@ struct AttnWalk {
 // The next item, or false. `tt`: tokens of a row tile.
 template <int KT>
 __device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, AttnItem& it) {
+    it.i0 = it.i1 = 0;
     if (w.u >= w.u_end) return false;
     while (w.tile * tt >= w.s.m) {  // the sequence's row tiles are done for this head
         w.tile = 0;
@@ -101,7 +110,10 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int 
     it.keys = key_tiles<KT>(it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
     it.i0 = w.off;
     it.i1 = static_cast<int>(min(static_cast<int64_t>(it.keys.n), it.i0 + (w.u_end - w.u)));
-    it.u0 = w.u - it.i0;
+    const int64_t u0 = w.u - it.i0;  // the row tile's first unit
+    it.first = it.last = blockIdx.x;
+    if (it.i0 > 0) it.first = static_cast<int>(u0 / w.q);
+    if (it.i1 < it.keys.n) it.last = static_cast<int>((u0 + it.keys.n - 1) / w.q);
     w.u += it.i1 - it.i0;
     w.off = 0;
     ++w.tile;
@@ -202,17 +214,6 @@ __device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int64_t*
         if (lane == 0) *found = w;
     }
     __syncthreads();
-}
-
-// Where a partial result goes. CTA c has at most two split row tiles: one that
-// began in an earlier CTA (slot 0) and one that goes on in a later (slot 1).
-struct AttnSplit {
-    int first, last;  // CTAs that share the row tile
-    __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (cta == first); }
-};
-
-__device__ __forceinline__ AttnSplit item_split(const AttnItem& it, int64_t q) {
-    return AttnSplit{static_cast<int>(it.u0 / q), static_cast<int>((it.u0 + it.keys.n - 1) / q)};
 }
 
 // K or V of one layer as a tensor map: {64 of head_dim, row of the page, column

@@ -28,9 +28,9 @@ struct DecodeCfg {
     static constexpr int kRing = D == 128 ? 3 : 6;
     static constexpr int kOffJoin = kRing * kStageBytes;          // [8 warps][8 rows][D]
     static constexpr int kOffRef = kOffJoin + kDecWarps * 8 * D * 4;   // [8 warps][16] references, sums
-    static constexpr int kOffBar = kOffRef + kDecWarps * 16 * 8;  // full[kRing] empty[kRing] join
-    static constexpr int kOffMisc = kOffBar + 8 * (2 * kRing + 1);
-    static constexpr int kSmem = kOffMisc + 120 + 1024;
+    static constexpr int kOffBar = kOffRef + kDecWarps * 16 * 8;  // full[kRing] empty[kRing] join ifull[] iempty[]
+    static constexpr int kOffMisc = kOffBar + 8 * (2 * kRing + 2 + 2 * kItemRing);
+    static constexpr int kSmem = kOffMisc + 112 + kItemRing * sizeof(AttnItem) + 1024;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(kMaxBatch * 8 <= kRing * kStageBytes, "the plan's scratch is the ring");
     static constexpr int kPartFloats = 16 * (D + 2);
@@ -72,15 +72,22 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint32_t b_full = sbase + Cfg::kOffBar;
     const uint32_t b_empty = b_full + 8 * R;
     const uint32_t b_join = b_empty + 8 * R;
+    const uint32_t b_ifull = b_join + 8;
+    const uint32_t b_iempty = b_ifull + 8 * kItemRing;
     AttnWalk* walk_s = reinterpret_cast<AttnWalk*>(smem + Cfg::kOffMisc);
     volatile int* last_s = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 96);
-    static_assert(sizeof(AttnWalk) <= 96, "walk");
+    AttnItem* items = reinterpret_cast<AttnItem*>(smem + Cfg::kOffMisc + 112);
+    static_assert(sizeof(AttnWalk) <= 96 && sizeof(AttnItem) % 8 == 0, "layout");
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, kDecWarps);
         }
         mbar_init(b_join, kDecWarps);
+        for (int i = 0; i < kItemRing; ++i) {
+            mbar_init(b_ifull + 8 * i, 1);
+            mbar_init(b_iempty + 8 * i, kDecWarps);
+        }
         fence_barrier_init();
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
@@ -88,21 +95,30 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     pdl_wait();
     const int tt = 16 / p.group;  // tokens of a row tile
     plan_units<KT>(p, tt, reinterpret_cast<int64_t*>(smem), walk_s);
-    AttnWalk w = *walk_s;
     fence_proxy_async_smem();  // the plan's scratch becomes the ring
     __syncthreads();
     if (threadIdx.x == 0) pdl_launch_dependents();
-    AttnItem it{};
     const int page = 1 << p.c.page_shift;
 
     if (warp == kDecWarps) {
         // ---------------------------------------------------- TMA producer ---
+        AttnWalk w = *walk_s;
+        AttnItem it{};
         int slot = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
         const int pages = KT >> p.c.page_shift;
         const uint32_t page_bytes = static_cast<uint32_t>(page) * D * 2;
-        while (ok && next_item<KT>(p, w, tt, it)) {
+        for (int n_items = 0; ok; ++n_items) {
+            const bool more = next_item<KT>(p, w, tt, it);
+            const int k = n_items % kItemRing;
+            ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
+            if (!ok) break;
+            if (lane == 0) {
+                items[k] = it;
+                mbar_arrive(b_ifull + 8 * k);
+            }
+            if (!more) break;
             for (int i = it.i0; i < it.i1; ++i) {
                 const int tile = it.keys.tile(i);
                 const int pg = lane % pages;
@@ -152,7 +168,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     float* join_ref = reinterpret_cast<float*>(smem + Cfg::kOffRef);
     float* join_sum = join_ref + kDecWarps * 16;
 
-    while (next_item<KT>(p, w, tt, it)) {
+    for (int n_items = 0;; ++n_items) {
+        // done with the item before
+        __syncwarp();
+        if (n_items > 0 && lane == 0) mbar_arrive(b_iempty + 8 * ((n_items - 1) % kItemRing));
+        const int ik = n_items % kItemRing;
+        if (!__all_sync(0xffffffffu, mbar_wait(b_ifull + 8 * ik, (n_items / kItemRing) & 1, p.err))) return;
+        const AttnItem it = items[ik];
+        if (it.i1 == it.i0) return;
         const int rows = it.tokens * p.group, p1 = it.p0 + it.tokens - 1;
         uint32_t q[D / 16][4];
         {
@@ -310,7 +333,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // the warps' results: eight rows at a time through shared memory, a warp
         // per row adds them up
         const bool whole = it.i0 == 0 && it.i1 == it.keys.n;
-        const AttnSplit sp = item_split(it, w.q);
         constexpr int V = D / 32;  // consecutive columns per lane
         auto out_row = [&](int r) {
             return p.out + (static_cast<int64_t>(it.t_first + r / p.group) * p.heads + it.h * p.group + r % p.group) * D + V * lane;
@@ -354,7 +376,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 if (whole) {
                     store(r, x, sum);
                 } else {
-                    float* to = p.scratch + static_cast<int64_t>(sp.slot(blockIdx.x)) * Cfg::kPartFloats;
+                    float* to = p.scratch + static_cast<int64_t>(it.slot(blockIdx.x)) * Cfg::kPartFloats;
 #pragma unroll
                     for (int e = 0; e < V; ++e) __stcg(to + r * D + V * lane + e, x[e]);
                     if (lane == 0) {
@@ -373,8 +395,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         __threadfence();
         if (!join()) return;
         if (threadIdx.x == 0) {
-            uint32_t* count = p.counters + sp.first;
-            const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(sp.last - sp.first);
+            uint32_t* count = p.counters + it.first;
+            const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(it.last - it.first);
             if (last) *count = 0u;  // as the next call expects it
             __threadfence();
             *last_s = last;
@@ -382,9 +404,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (!join()) return;
         if (!*last_s) continue;
         for (int r = warp; r < rows; r += kDecWarps) {
-            auto part = [&](int cta) { return p.scratch + static_cast<int64_t>(sp.slot(cta)) * Cfg::kPartFloats; };
+            auto part = [&](int cta) { return p.scratch + static_cast<int64_t>(it.slot(cta)) * Cfg::kPartFloats; };
             float top = -INFINITY;
-            for (int cta = sp.first + lane; cta <= sp.last; cta += 32) top = fmaxf(top, __ldcg(part(cta) + 16 * D + r));
+            for (int cta = it.first + lane; cta <= it.last; cta += 32) top = fmaxf(top, __ldcg(part(cta) + 16 * D + r));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float z = top == -INFINITY ? 0.f : top;
@@ -392,7 +414,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
             for (int e = 0; e < V; ++e) x[e] = 0.f;
 #pragma unroll 4
-            for (int cta = sp.first; cta <= sp.last; ++cta) {
+            for (int cta = it.first; cta <= it.last; ++cta) {
                 const float* from = part(cta);
                 const float f = ex2(__ldcg(from + 16 * D + r) - z);
                 sum = fmaf(__ldcg(from + 16 * D + 16 + r), f, sum);
