@@ -17,14 +17,15 @@
 // row each) turn S into P: the two halves take turns.
 //
 // Warp roles: 0-3 softmax of half 0, 4-7 of half 1, 8 TMA producer (pages of
-// K and V tiles, Q), 9 MMA issuer. K and V tiles go through one ring of
+// K and V tiles, Q), 9 MMA issuer, 10-11 scan (below). K and V tiles go through one ring of
 // buffers, filled page by page: the tensor map's last coordinate is the page,
 // and pages past a sequence's end are asked for at page -1, which fills zeros.
 //
 // Values that no row may see can be NaN (pages are not cleared): scores are
 // selected, not added to, and V tiles that some row sees only in part are
-// searched for infinities and NaN, which are zeroed in shared memory and added
-// back, at the end, to the rows that do see them.
+// searched, by two warps ahead of the MMAs, for infinities and NaN, which are
+// zeroed in shared memory and added back, at the end, to the rows that do see
+// them.
 #include <cuda_bf16.h>
 
 #include "q4k_attn.cuh"
@@ -33,6 +34,7 @@ namespace q4k {
 
 constexpr int kChunkKeys = 128;
 constexpr int kChunkThreads = 384;
+constexpr int kScanWarps = 2;
 
 template <int D>
 struct ChunkCfg {
@@ -43,7 +45,8 @@ struct ChunkCfg {
     static constexpr int kOffRing = 2 * kTileBytes;
     static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
     // full[kRing] empty[kRing] qfull qempty sfull[2] pfull[2] ofull[2] wg[2] fin ifull[kItemRing] iempty[kItemRing]
-    static constexpr int kNumBars = 2 * kRing + 11 + 2 * kItemRing;
+    // vclean[kRing]
+    static constexpr int kNumBars = 3 * kRing + 11 + 2 * kItemRing;
     static constexpr int kOffMisc = kOffBar + 8 * ((kNumBars + 1) / 2 * 2);  // walk, tmem address, flags, items
     static constexpr int kMiscBytes = 144 + kItemRing * sizeof(AttnItem);
     static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;  // + alignment slack
@@ -87,6 +90,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t b_fin = b_wg + 16;
     const uint32_t b_ifull = b_fin + 8;
     const uint32_t b_iempty = b_ifull + 8 * kItemRing;
+    const uint32_t b_vclean = b_iempty + 8 * kItemRing;
     AttnWalk* walk_s = reinterpret_cast<AttnWalk*>(smem + Cfg::kOffMisc);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 96);
     volatile int* poison = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 112);  // [4] item tags
@@ -97,7 +101,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 1 + kScanWarps);  // the MMA's commit, the scan warps
+            mbar_init(b_vclean + 8 * i, kScanWarps);
         }
         mbar_init(b_qfull, 1);
         mbar_init(b_qempty, 1);
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(b_fin, 1);
         for (int i = 0; i < kItemRing; ++i) {
             mbar_init(b_ifull + 8 * i, 1);
-            mbar_init(b_iempty + 8 * i, 9);  // the MMA warp and eight softmax warps
+            mbar_init(b_iempty + 8 * i, 9 + kScanWarps);  // MMA, softmax and scan warps
         }
         fence_barrier_init();
     }
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             constexpr uint32_t idesc_s = idesc_bf16_f32(128, KT);
             constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
             int n_items = 0, slot = 0;
-            uint32_t phase = 0, p_phase[2] = {0, 0};
+            uint32_t phase = 0, p_phase[2] = {0, 0}, clean_phase = 0;  // (a bit per ring slot)
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t ph) {
                 const bool r = __all_sync(0xffffffffu, mbar_wait(bar, ph, p.err));
@@ -248,6 +253,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ok = wait(b_ifull + 8 * ik, (n_items / kItemRing) & 1);
                 if (!ok) break;
                 const int halves = items[ik].tokens > tph ? 2 : 1, n = items[ik].i1 - items[ik].i0;
+                const int i0 = items[ik].i0, p0 = items[ik].p0, p1 = p0 + items[ik].tokens - 1;
+                const KeyTiles keys = items[ik].keys;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_iempty + 8 * ik);
                 if (n == 0) break;
@@ -263,6 +270,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const uint32_t kphase = kslot == 0 ? vphase ^ 1 : vphase;
                     const bool more = j + 1 < n;
                     ok = wait(b_full + 8 * vslot, vphase);
+                    if (ok && !tile_is_full<KT>(keys.tile(i0 + j), p0, p1, p.window, p.sinks)) {
+                        ok = wait(b_vclean + 8 * vslot, clean_phase >> vslot & 1);
+                        clean_phase ^= 1u << vslot;
+                    }
                     if (ok && more) ok = wait(b_full + 8 * kslot, kphase);
                     for (int hf = 0; ok && hf < halves; ++hf) {
                         ok = wait(b_pfull + 8 * hf, p_phase[hf]);
@@ -293,6 +304,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ++n_items;
             }
             commit(b_fin);  // every MMA of this CTA has completed
+        } else {
+            // ---------------------------------------------------------- scan ---
+            int slot = 0;
+            uint32_t phase = 0;
+            for (int n_items = 0;; ++n_items) {
+                const int ik = n_items % kItemRing;
+                if (!__all_sync(0xffffffffu, mbar_wait(b_ifull + 8 * ik, (n_items / kItemRing) & 1, p.err))) break;
+                const int i0 = items[ik].i0, n = items[ik].i1 - i0, p0 = items[ik].p0, p1 = p0 + items[ik].tokens - 1;
+                const KeyTiles keys = items[ik].keys;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_iempty + 8 * ik);
+                if (n == 0) break;
+                bool ok = true;
+                // every buffer of the ring in its turn (so that none is passed over
+                // or met a round late), the V tiles of partly seen key tiles read
+                for (int j = 0; ok && j < 2 * n; ++j) {
+                    const int vslot = slot;
+                    ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * vslot, phase, p.err));
+                    if (!ok) break;
+                    if (++slot == R) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    if (!(j & 1) || tile_is_full<KT>(keys.tile(i0 + (j >> 1)), p0, p1, p.window, p.sinks)) {
+                        if (lane == 0) mbar_arrive(b_empty + 8 * vslot);
+                        continue;
+                    }
+                    uint4* v4 = reinterpret_cast<uint4*>(smem + Cfg::kOffRing + vslot * Cfg::kTileBytes) +
+                                (threadIdx.x - 32 * 10);
+                    constexpr int kStep = 32 * kScanWarps;
+#pragma unroll 1
+                    for (int e = 0; e < Cfg::kTileBytes / 16 / kStep; e += 8) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = v4[kStep * (e + i)];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 m = make_uint4(bf16x2_non_finite(x[i].x), bf16x2_non_finite(x[i].y),
+                                                       bf16x2_non_finite(x[i].z), bf16x2_non_finite(x[i].w));
+                            if ((m.x | m.y | m.z | m.w) == 0u) continue;
+                            poison[(n_items + 1) & 3] = n_items + 1;
+                            v4[kStep * (e + i)] = make_uint4(
+                                x[i].x & ~((m.x >> 15) * 0xFFFFu), x[i].y & ~((m.y >> 15) * 0xFFFFu),
+                                x[i].z & ~((m.z >> 15) * 0xFFFFu), x[i].w & ~((m.w >> 15) * 0xFFFFu));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(b_vclean + 8 * vslot);
+                        mbar_arrive(b_empty + 8 * vslot);
+                    }
+                }
+                if (!ok) break;
+            }
         }
         __syncwarp();
     } else {
@@ -303,8 +369,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t t_s = tmem + lane_base + Cfg::kColS + hf * 128;
         const uint32_t t_o = tmem + lane_base + Cfg::kColO + hf * D;
         const int tok = r / p.group, g = r % p.group;
-        int n_items = 0, slot = 0;  // ring position of the item's first V tile is slot + 1
-        uint32_t phase = 0, s_phase = 0, o_phase = 0, wg_phase = 0;
+        int n_items = 0;
+        uint32_t s_phase = 0, o_phase = 0, wg_phase = 0;
         bool ok = true;
         for (;;) {
             // done with the item before
@@ -316,13 +382,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int n = it.i1 - it.i0;
             if (n == 0) break;
             ++n_items;
-            const int first_slot = slot;
-            const uint32_t first_phase = phase;
-            {  // 2n tiles on
-                const int at = slot + 2 * n;
-                phase ^= (at / R) & 1;
-                slot = at % R;
-            }
             const int mine = min(it.tokens - hf * tph, tph);  // tokens of this half
             if (mine <= 0) continue;
             const int h0 = it.p0 + hf * tph, h1 = h0 + mine - 1;  // positions of the half's tokens
@@ -330,33 +389,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             float ref = -INFINITY, sum = 0.f;
             for (int j = 0; j < n; ++j) {
                 const int tile = it.keys.tile(it.i0 + j);
-                const bool item_full = tile_is_full<KT>(tile, it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
-                if (!item_full) {
-                    // V values that are not finite: zero here, and remembered for the end
-                    const int at = first_slot + 2 * j + 1, vslot = at % R;
-                    if (!__all_sync(0xffffffffu, mbar_wait(b_full + 8 * vslot, first_phase ^ ((at / R) & 1), p.err))) {
-                        ok = false;
-                        break;
-                    }
-                    uint4* v4 = reinterpret_cast<uint4*>(smem + Cfg::kOffRing + vslot * Cfg::kTileBytes) + r;
-#pragma unroll
-                    for (int e = 0; e < Cfg::kTileBytes / 16 / 128; e += 4) {
-                        uint4 x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = v4[128 * (e + i)];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 m = make_uint4(bf16x2_non_finite(x[i].x), bf16x2_non_finite(x[i].y),
-                                                       bf16x2_non_finite(x[i].z), bf16x2_non_finite(x[i].w));
-                            if ((m.x | m.y | m.z | m.w) == 0u) continue;
-                            poison[n_items & 3] = n_items;
-                            __threadfence_block();
-                            v4[128 * (e + i)] = make_uint4(x[i].x & ~((m.x >> 15) * 0xFFFFu), x[i].y & ~((m.y >> 15) * 0xFFFFu),
-                                                           x[i].z & ~((m.z >> 15) * 0xFFFFu), x[i].w & ~((m.w >> 15) * 0xFFFFu));
-                        }
-                    }
-                    fence_proxy_async_smem();
-                }
                 if (!__all_sync(0xffffffffu, mbar_wait(b_sfull + 8 * hf, s_phase, p.err))) {
                     ok = false;
                     break;
@@ -368,17 +400,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, sv[c]);
                 tmem_ld_wait();
                 if (!tile_is_full<KT>(tile, h0, h1, p.window, p.sinks)) {
-                    // columns of this tile that the row sees: [0, sink) and (low, high]
+                    // columns of this tile that the row sees: [0, sink) and (low, high], as 32 bits per block
                     const int j0 = tile * KT, high = pos - j0;
                     const int low = p.window > 0 ? max(pos - p.window, -1) - j0 : -1;
                     const int sink = p.window > 0 ? p.sinks - j0 : 0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        auto below = [&](int col) {  // bits of the columns under col
+                            const int k = min(max(col - 32 * c, 0), 32);
+                            return static_cast<uint32_t>((1ull << k) - 1);
+                        };
+                        const uint32_t seen = below(high + 1) & (~below(low + 1) | below(sink));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int col = 32 * c + e;
-                            if (!(col <= high && (col > low || col < sink))) sv[c][e] = 0xFF800000u;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen >> e & 1u)) sv[c][e] = 0xFF800000u;
+                    }
                 }
                 float mx = -INFINITY;
 #pragma unroll
