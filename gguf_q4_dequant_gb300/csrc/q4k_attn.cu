@@ -28,6 +28,8 @@
 // them.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "q4k_attn.cuh"
 
 namespace q4k {
@@ -35,6 +37,12 @@ namespace q4k {
 constexpr int kChunkKeys = 128;
 constexpr int kChunkThreads = 384;
 constexpr int kScanWarps = 2;
+#ifndef Q4K_CHUNK_SNAP
+#define Q4K_CHUNK_SNAP 2
+#endif
+#define Q4K_REGS_DEC 88
+constexpr int kChunkMinUnits = 1;
+constexpr int kChunkSnap = Q4K_CHUNK_SNAP;
 
 template <int D>
 struct ChunkCfg {
@@ -51,7 +59,7 @@ struct ChunkCfg {
     static constexpr int kMiscBytes = 144 + kItemRing * sizeof(AttnItem);
     static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(kMaxBatch * 8 <= kRing * kTileBytes, "the plan's scratch is the ring");
+    static_assert(kMaxBatch * 4 <= kRing * kTileBytes, "the plan's scratch is the ring");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kColS = 0, kColO = 256;        // S (and P) 2 x 128, O 2 x D
     static constexpr int kPartFloats = (D + 2) * 128;        // a partial result of one half
@@ -131,7 +139,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     pdl_wait();
     const int tph = 128 / p.group, tt = 2 * tph;  // tokens per half and per item
-    plan_units<KT>(p, tt, reinterpret_cast<int64_t*>(smem + Cfg::kOffRing), walk_s);
+    plan_units<KT>(p, tt, kChunkMinUnits, kChunkSnap, reinterpret_cast<uint32_t*>(smem + Cfg::kOffRing), walk_s);
     // the plan's scratch (generic accesses) becomes the ring (TMA writes)
     fence_proxy_async_smem();
     tc_fence_before();
@@ -141,7 +149,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (threadIdx.x == 0) pdl_launch_dependents();
 
     if (warp >= 8) {
-        regs_dec<72>();
+        regs_dec<Q4K_REGS_DEC>();
         if (warp == 8) {
             // ------------------------------------------------ TMA producer ---
             AttnWalk w = *walk_s;
@@ -173,7 +181,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 return true;
             };
             for (;;) {
-                const bool more = next_item<KT>(p, w, tt, it);
+                const bool more = next_item<KT>(p, w, tt, kChunkSnap, it);
                 const int k = n_items % kItemRing;
                 ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
                 if (!ok) break;
@@ -363,7 +371,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax ---
-        regs_inc<216>();
+        regs_inc<(504 - Q4K_REGS_DEC) / 2 / 8 * 8>();
         const int hf = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lane_base + Cfg::kColS + hf * 128;
@@ -636,8 +644,8 @@ cudaError_t launch_attention(const CacheLayer& c, const Batch& b, const AttnArgs
     p.err = dev.err;
     // at most one row tile of 16 per sequence and kv head: bound by the memory,
     // not by the tensor core
-    if (static_cast<int64_t>(max_new) * p.group <= 16 && p.group <= 16)
-        return launch_attn_decode(p, a.head_dim, stream, dev, pdl);
+    const int64_t rows = std::max(static_cast<int64_t>(max_new) * p.group, static_cast<int64_t>(p.group));
+    if (rows <= 16) return launch_attn_decode(p, static_cast<int>(rows), a.head_dim, stream, dev, pdl);
     return a.head_dim == 64 ? launch_chunk<64>(p, a, stream, dev, pdl) : launch_chunk<128>(p, a, stream, dev, pdl);
 }
 

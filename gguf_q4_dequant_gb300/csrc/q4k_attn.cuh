@@ -4,9 +4,11 @@
 // tiles of whole tokens, the positions into key tiles. One unit of work is one
 // (row tile, key tile) that the mask does not rule out; the units of all
 // sequences, kv heads and row tiles are numbered in that order, and CTA c of
-// the grid takes units [c*q, (c+1)*q) with q = ceil(total / grid). So every CTA
-// has the same number of key tiles whatever the sequences' lengths are, on the
-// device's own numbers. A row tile that lies in several CTAs' ranges is put
+// the grid takes about units [c*q, (c+1)*q) with q = ceil(total / grid). So every
+// CTA has about the same number of key tiles whatever the sequences' lengths
+// are, on the device's own numbers. (Units are counted in 32 bits: a step of
+// more than 2^32 key tiles of at least 16 x 128 x 64 products would take hours.)
+// A row tile that lies in several CTAs' ranges is put
 // together from their partial results by whichever of them finishes last, in
 // the order of the CTAs: the result does not depend on which one that is.
 #pragma once
@@ -83,15 +85,15 @@ struct AttnItem {
 constexpr int kItemRing = 4;
 
 struct AttnWalk {
-    int64_t u, u_end;  // units left to do
-    int64_t q;
+    uint32_t u, u_end;  // units left to do
+    uint32_t q;
     int b, h, tile, off;
     SeqView s;
 };
 
 // The next item, or false. `tt`: tokens of a row tile.
 template <int KT>
-__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, AttnItem& it) {
+__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, int snap, AttnItem& it) {
     it.i0 = it.i1 = 0;
     if (w.u >= w.u_end) return false;
     while (w.tile * tt >= w.s.m) {  // the sequence's row tiles are done for this head
@@ -109,11 +111,13 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int 
     it.len = w.s.len;
     it.keys = key_tiles<KT>(it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
     it.i0 = w.off;
-    it.i1 = static_cast<int>(min(static_cast<int64_t>(it.keys.n), it.i0 + (w.u_end - w.u)));
-    const int64_t u0 = w.u - it.i0;  // the row tile's first unit
+    it.i1 = static_cast<int>(min(static_cast<uint32_t>(it.keys.n), it.i0 + (w.u_end - w.u)));
     it.first = it.last = blockIdx.x;
-    if (it.i0 > 0) it.first = static_cast<int>(u0 / w.q);
-    if (it.i1 < it.keys.n) it.last = static_cast<int>((u0 + it.keys.n - 1) / w.q);
+    if (it.i0 > 0 || it.i1 < it.keys.n) {
+        const uint32_t u0 = w.u - it.i0, u1 = u0 + it.keys.n;  // the row tile's units
+        it.first = static_cast<int>((u0 + snap) / w.q);        // one before the first boundary inside
+        it.last = static_cast<int>((u1 - snap - 1) / w.q);     // the last boundary inside
+    }
     w.u += it.i1 - it.i0;
     w.off = 0;
     ++w.tile;
@@ -122,22 +126,98 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int 
 
 // Units of the row tiles of one sequence and kv head.
 template <int KT>
-__device__ __forceinline__ int64_t tile_units(const AttnParams& p, const SeqView& s, int tile, int tt) {
+__device__ __forceinline__ int tile_units(const AttnParams& p, const SeqView& s, int tile, int tt) {
     const int p0 = s.len - s.m + tile * tt;
     return key_tiles<KT>(p0, p0 + min(tt, s.m - tile * tt) - 1, p.window, p.sinks).n;
 }
 
-// The CTA's range, found by all threads of the block: `units` holds n words of
-// shared memory, `found` takes the result. Ends with __syncthreads().
+// A row tile that a range's end falls into near one of its own ends is not cut
+// there: the end moves by up to `snap` key tiles, since putting two parts
+// together costs about as much time. So boundary c, at first c * q, lies inside
+// a row tile of units [a, b) only if a + snap < c * q < b - snap.
+struct AttnCut {
+    uint32_t u;        // the boundary, moved
+    int b, h, tile, off;  // where it lies (off > 0: inside the row tile)
+    SeqView s;
+};
+
+// Found by one warp: the row tile that holds unit u < total, from the units of
+// the sequences.
 template <int KT>
-__device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int64_t* units, AttnWalk* found) {
+__device__ __forceinline__ AttnCut find_cut(const AttnParams& p, int tt, const uint32_t* units, uint32_t u, int snap) {
+    const int lane = threadIdx.x & 31;
+    AttnCut c;
+    c.b = c.h = c.tile = c.off = 0;
+    uint32_t at = 0;
+    for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+        const uint32_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0;
+        uint32_t incl = mine;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, k);
+            if (lane >= k) incl += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, at + incl > u);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            c.b = i0 + l;
+            at += __shfl_sync(0xffffffffu, incl - mine, l);
+            break;
+        }
+        at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    c.s = seq_view(p.c, p.b, c.b);
+    const uint32_t per_head = units[c.b] / p.c.kv_heads;
+    c.h = static_cast<int>((u - at) / per_head);
+    uint32_t rest = (u - at) - c.h * per_head;
+    int n = per_head;
+    if (c.s.m > tt) {
+        for (int t0 = 0; t0 < (c.s.m + tt - 1) / tt; t0 += 32) {
+            const int t = t0 + lane;
+            const uint32_t mine = static_cast<int64_t>(t) * tt < c.s.m ? tile_units<KT>(p, c.s, t, tt) : 0;
+            uint32_t incl = mine;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, k);
+                if (lane >= k) incl += v;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, incl > rest);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                c.tile = t0 + l;
+                n = __shfl_sync(0xffffffffu, mine, l);
+                rest -= __shfl_sync(0xffffffffu, incl - mine, l);
+                break;
+            }
+            rest -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    c.u = u;
+    c.off = static_cast<int>(rest);
+    if (c.off <= snap) {
+        c.u -= c.off;
+        c.off = 0;
+    } else if (n - c.off <= snap) {
+        c.u += n - c.off;
+        c.off = 0;
+        ++c.tile;  // (one past the last: the walk goes on to the next head or sequence)
+    }
+    return c;
+}
+
+// The CTA's range, found by all threads of the block: `units` holds n words of
+// shared memory, `found` takes the result. Ends with __syncthreads(). `q_min`:
+// units that a range has at least.
+template <int KT>
+__device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int q_min, int snap, uint32_t* units,
+                                           AttnWalk* found) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
         const int i = i0 + lane;
         SeqView s{0, 0, 0, 0};
         if (i < p.b.n) s = seq_view(p.c, p.b, i);
         const int tiles = (s.m + tt - 1) / tt;
-        int64_t u = 0;
+        uint32_t u = 0;
         if (tiles <= 4)
             for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
         // many row tiles: the warp counts them together
@@ -149,69 +229,39 @@ __device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int64_t*
             o.m = __shfl_sync(0xffffffffu, s.m, l);
             o.len = __shfl_sync(0xffffffffu, s.len, l);
             const int ot = (o.m + tt - 1) / tt;
-            int64_t x = 0;
+            uint32_t x = 0;
             for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+            x = __reduce_add_sync(0xffffffffu, x);
             if (lane == l) u = x;
         }
         if (i < p.b.n) units[i] = u * p.c.kv_heads;
     }
     __syncthreads();
-    if (warp == 0) {
-        int64_t total = 0;
+    // warp 0 finds where the range begins, warp 1 where it ends
+    if (warp < 2) {
+        uint32_t total = 0;
         for (int i = lane; i < p.b.n; i += 32) total += units[i];
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
-        AttnWalk w;
-        w.q = (total + gridDim.x - 1) / gridDim.x;
-        w.u = blockIdx.x * w.q;
-        w.u_end = min(total, w.u + w.q);
-        w.b = w.h = w.tile = w.off = 0;
-        w.s = SeqView{0, 0, 0, 0};
-        if (w.u < w.u_end) {
-            int64_t at = 0;
-            for (int i0 = 0; i0 < p.b.n; i0 += 32) {
-                const int64_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0;
-                int64_t incl = mine;
-#pragma unroll
-                for (int k = 1; k < 32; k <<= 1) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, k);
-                    if (lane >= k) incl += v;
-                }
-                const uint32_t past = __ballot_sync(0xffffffffu, at + incl > w.u);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    w.b = i0 + l;
-                    at += __shfl_sync(0xffffffffu, incl - mine, l);
-                    break;
-                }
-                at += __shfl_sync(0xffffffffu, incl, 31);
-            }
-            w.s = seq_view(p.c, p.b, w.b);
-            const int64_t per_head = units[w.b] / p.c.kv_heads;
-            w.h = static_cast<int>((w.u - at) / per_head);
-            int64_t rest = (w.u - at) - w.h * per_head;
-            for (int t0 = 0;; t0 += 32) {
-                const int64_t mine = (t0 + lane) * tt < w.s.m ? tile_units<KT>(p, w.s, t0 + lane, tt) : 0;
-                int64_t incl = mine;
-#pragma unroll
-                for (int k = 1; k < 32; k <<= 1) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, k);
-                    if (lane >= k) incl += v;
-                }
-                const uint32_t past = __ballot_sync(0xffffffffu, incl > rest);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    w.tile = t0 + l;
-                    w.off = static_cast<int>(rest - __shfl_sync(0xffffffffu, incl - mine, l));
-                    break;
-                }
-                rest -= __shfl_sync(0xffffffffu, incl, 31);
-                if ((t0 + 32) * static_cast<int64_t>(tt) >= w.s.m) break;  // not reached: the units add up
+        total = __reduce_add_sync(0xffffffffu, total);
+        const uint32_t q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(q_min));
+        const uint64_t u = static_cast<uint64_t>(blockIdx.x + warp) * q;
+        AttnCut c;
+        c.u = total;
+        c.b = c.h = c.tile = c.off = 0;
+        c.s = SeqView{0, 0, 0, 0};
+        if (u < total) c = find_cut<KT>(p, tt, units, static_cast<uint32_t>(u), snap);
+        if (lane == 0) {
+            if (warp == 0) {
+                found->u = c.u;
+                found->q = q;
+                found->b = c.b;
+                found->h = c.h;
+                found->tile = c.tile;
+                found->off = c.off;
+                found->s = c.s;
+            } else {
+                found->u_end = c.u;
             }
         }
-        if (lane == 0) *found = w;
     }
     __syncthreads();
 }
@@ -229,8 +279,9 @@ inline bool encode_pages(CUtensorMap* map, const uint16_t* base, const CacheLaye
     return encode_bf16_sw128(map, base, 5, dims, strides, box);
 }
 
-// The kernel for few rows per kv head (group <= 16).
-cudaError_t launch_attn_decode(const AttnParams& p, int head_dim, cudaStream_t stream, const DeviceInfo& dev, int pdl);
+// The kernel for few rows per kv head: `rows` <= 16 of them in a row tile (group <= rows).
+cudaError_t launch_attn_decode(const AttnParams& p, int rows, int head_dim, cudaStream_t stream,
+                               const DeviceInfo& dev, int pdl);
 cudaError_t attn_decode_setup();
 
 // 2^x by the special function unit (flushes subnormal results to zero, which a
