@@ -61,6 +61,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded libq4k.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -132,6 +134,9 @@ def _ptr(t) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # the same address without building a Stream object (2.9 us of a call's host time)
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

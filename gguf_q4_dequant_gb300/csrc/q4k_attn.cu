@@ -154,22 +154,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // ------------------------------------------------ TMA producer ---
             AttnWalk w = *walk_s;
             AttnItem it{};
+            PageIds ids;
             int slot = 0, n_items = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
             const int pages = KT >> p.c.page_shift;   // per key tile
             const int boxes = pages * Cfg::kHalves;
             const uint32_t page_bytes = 128u << p.c.page_shift;  // of one column block
-            auto load_tile = [&](const CUtensorMap* map, int tile) {
+            auto load_tile = [&](const CUtensorMap* map, int page) {
                 if (!__all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, phase ^ 1, p.err))) return false;
                 if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * slot, Cfg::kTileBytes);
                 __syncwarp();
                 if (lane < boxes) {
                     const int pg = lane % pages, cb = lane / pages;
-                    const int64_t idx = static_cast<int64_t>(tile) * pages + pg;
-                    int page = -1;
-                    if (idx << p.c.page_shift < it.len) page = p.c.table[it.row + idx];
-                    if (page < 0 || page >= p.c.n_pages) page = -1;
                     tma_load_5d(sbase + Cfg::kOffRing + slot * Cfg::kTileBytes + cb * (KT * 128) + pg * page_bytes, map,
                                 0, 0, cb, it.h, page, b_full + 8 * slot);
                 }
@@ -202,9 +199,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                 it.h * p.group, it.t_first + hf * tph, cb, b_qfull);
                 }
                 ++n_items;
+                ids.begin();
                 for (int i = it.i0; ok && i < it.i1; ++i) {
                     const int tile = it.keys.tile(i);
-                    ok = load_tile(&map_k, tile) && load_tile(&map_v, tile);
+                    const int page = ids.get(p, it, tile * pages, lane % pages);
+                    ok = load_tile(&map_k, page) && load_tile(&map_v, page);
                 }
                 if (!ok) break;
             }

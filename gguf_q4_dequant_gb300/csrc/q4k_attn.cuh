@@ -284,6 +284,29 @@ cudaError_t launch_attn_decode(const AttnParams& p, int rows, int head_dim, cuda
                                const DeviceInfo& dev, int pdl);
 cudaError_t attn_decode_setup();
 
+// The page ids of a sequence's key tiles, for one warp: 32 entries of its table
+// row at a time, a lane each, and the next 32 already on their way.
+struct PageIds {
+    int base, ids, next;
+
+    __device__ __forceinline__ int load(const AttnParams& p, const AttnItem& it, int64_t at) const {
+        if (at << p.c.page_shift >= it.len) return -1;  // (asked for as page -1: reads as zeros)
+        const int id = p.c.table[it.row + at];
+        return id < p.c.n_pages ? max(id, -1) : -1;
+    }
+    __device__ __forceinline__ void begin() { base = -1; }
+    // Entry first + k of the row, for the lanes' own k < 32; first is the same for all and a multiple of `pages` | 32.
+    __device__ __forceinline__ int get(const AttnParams& p, const AttnItem& it, int first, int k) {
+        if (base < 0 || first < base || first >= base + 32) {
+            const int lane = threadIdx.x & 31;
+            ids = base >= 0 && first == base + 32 ? next : load(p, it, static_cast<int64_t>(first) + lane);
+            base = first;
+            next = load(p, it, static_cast<int64_t>(first) + 32 + lane);
+        }
+        return __shfl_sync(0xffffffffu, ids, first - base + k);
+    }
+};
+
 // 2^x by the special function unit (flushes subnormal results to zero, which a
 // softmax weight may be).
 __device__ __forceinline__ float ex2(float x) {

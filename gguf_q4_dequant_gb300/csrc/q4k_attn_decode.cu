@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // ---------------------------------------------------- TMA producer ---
         AttnWalk w = *walk_s;
         AttnItem it{};
+        PageIds ids;
         int slot = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -140,13 +141,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 mbar_arrive(b_ifull + 8 * k);
             }
             if (!more) break;
+            ids.begin();
             for (int i = it.i0; i < it.i1; ++i) {
                 const int tile = it.keys.tile(i);
-                const int pg = lane % pages;
-                const int64_t idx = static_cast<int64_t>(tile) * pages + pg;
-                int id = -1;
-                if (idx << p.c.page_shift < it.len) id = p.c.table[it.row + idx];
-                if (id < 0 || id >= p.c.n_pages) id = -1;  // fills zeros
+                const int pg = lane % pages, id = ids.get(p, it, tile * pages, pg);
                 ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, phase ^ 1, p.err));
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * slot, Cfg::kStageBytes);
