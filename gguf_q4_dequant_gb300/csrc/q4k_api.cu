@@ -115,7 +115,7 @@ void init_device(int dev, DeviceState& st) {
     st.info.max_smem_optin = static_cast<int>(prop.sharedMemPerBlockOptin);
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess || gemv_setup(st.info) != cudaSuccess || tcgemv_setup(st.info) != cudaSuccess ||
-        gemm_setup(st.info) != cudaSuccess || attn_setup(st.info) != cudaSuccess || pick_setup() != cudaSuccess ||
+        gemm_setup(st.info) != cudaSuccess || attn_setup(st.info) != cudaSuccess || pick_setup(st.info) != cudaSuccess ||
         encoder() == nullptr) {
         st.status = Q4K_ERR_CUDA;
         return;

@@ -22,6 +22,8 @@ struct DeviceInfo {
     // tensor-core decode kernel, same indexing (C up to 8)
     int tc_occ[2][5] = {};
     int tc_clusters[2][5][9] = {};
+    // logits pick: resident clusters of C CTAs (index C, 2..8)
+    int pick_clusters[9] = {};
 };
 
 cudaError_t launch_dequant(const uint8_t* W, int64_t N, int64_t K, float* out, cudaStream_t stream,

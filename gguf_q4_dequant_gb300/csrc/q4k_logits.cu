@@ -4,14 +4,27 @@
 // A logit is read once (and written once if kept): the bound is the memory's
 // rate for many rows, and latency for one. A cluster of CTAs shares a row, so
 // that one row is spread over several SMs without a second launch: the CTAs'
-// best candidates meet in the first one's shared memory. A CTA takes its part
-// of the row in chunks of 16 logits per thread, loaded into registers first;
-// while they are on their way, the row's history is counted into a table of the
-// chunk in shared memory (integer atomics: order does not matter), and the
-// bias entries leave their index there (the largest wins).
+// best candidates meet in the first one's shared memory.
+//
+// Few tokens of a row are penalised or biased, so these are taken apart, by four
+// warps of their own, while the other warps stream all logits past the grammar
+// mask at a few instructions each, four at a time, with one comparison per four.
+// The four warps count the history into a table of the CTA's part of the row in
+// shared memory (integer atomics: their order does not matter; 16 bits per logit
+// unless the history is long enough to overflow them); whoever counts a token
+// first puts it on a list, and the tokens of the list are adjusted one by one
+// and go over the streamed logits at the end. A thread whose largest logit turns
+// out to be one of them has its logits looked through again, by a warp, without
+// the ones on the list.
+// (Penalties applied where the logits stream by took 68 instructions per logit,
+// half of the warps dividing for one lane's token: 43 us for 64 rows of 151936,
+// issue-bound. The same steps before or after the stream, by all warps, left the
+// memory idle through four dependent loads: 33 and 35 us.)
 //
 // Rows start at any multiple of 4 bytes (V may be odd), so a row is cut into
 // the 16-byte groups of the memory, the first and last of them partly used.
+#include <algorithm>
+
 #include "q4k_device.cuh"
 #include "q4k_serve.h"
 
@@ -20,25 +33,102 @@ namespace q4k {
 namespace {
 
 constexpr int kPickThreads = 512;
-constexpr int kPickGroups = 4;  // groups of 4 logits per thread and chunk
-constexpr int kPickChunk = kPickThreads * kPickGroups;  // groups
+constexpr int kPickApart = 128;          // threads that see to the penalised and biased tokens
+constexpr int kPickBatch = 4;            // groups of 4 logits that a thread has in flight
+constexpr int kPickTableGroups = 7168;   // groups that the tables cover at most
+constexpr int kPickList = 1024;          // adjusted tokens that wait for the end of the stream
 constexpr int kPickMaxCluster = 8;
 
-// Orders floats as unsigned integers: numbers by value (-0 as 0) above NaN (1)
-// above a token that is not allowed (0).
-__device__ __forceinline__ uint32_t pick_order(float x, bool allowed) {
-    const uint32_t u = __float_as_uint(x + 0.f);
-    const uint32_t o = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-    return !allowed ? 0u : x != x ? 1u : o;
+// Bytes of the tables of `groups` groups (a multiple of 32): two bits per logit
+// (seen to apart; not on the list for want of room), 16-bit counts; the list.
+__host__ __device__ constexpr int pick_marks_bytes(int groups) { return groups / 2; }
+__host__ __device__ constexpr int pick_tables_bytes(int groups) {
+    return 2 * pick_marks_bytes(groups) + 8 * groups + 8 * kPickList;
+}
+
+// The largest number met and its token: by value, then by lower token.
+struct Best {
+    float x;
+    uint32_t v;
+    __device__ __forceinline__ void take(float y, uint32_t w) {
+        if (y > x || (y == x && w < v)) {
+            x = y;
+            v = w;
+        }
+    }
+    // Larger is better as an unsigned integer; no number above -infinity: 1 if a
+    // token was allowed, else 0. (-0 counts as 0.)
+    __device__ __forceinline__ unsigned long long key(bool any) const {
+        if (!(x > -INFINITY)) return any;
+        const uint32_t u = __float_as_uint(x + 0.f);
+        const uint32_t o = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+        return static_cast<unsigned long long>(o) << 32 | (0xFFFFFFFFu - v);
+    }
+};
+
+struct RowRules {
+    int h0, h1, b0, b1;  // the row's history and biases
+    float repeat, presence, frequency;
+    const uint32_t* mask;
+
+    __device__ __forceinline__ bool allowed(int64_t v) const { return mask == nullptr || (mask[v >> 5] >> (v & 31) & 1u); }
+    __device__ __forceinline__ float penalise(float x, uint32_t count) const {
+        const float y = x > 0.f ? __fdiv_rn(x, repeat) : __fmul_rn(x, repeat);
+        return __fsub_rn(__fsub_rn(y, __fmul_rn(static_cast<float>(count), frequency)), presence);
+    }
+    // the last entry of the token counts
+    __device__ __forceinline__ float add_bias(const PickArgs& a, float x, int v) const {
+        for (int i = b1 - 1; i >= b0; --i)
+            if (a.bias_ids[i] == v) return __fadd_rn(x, a.bias[i]);
+        return x;
+    }
+};
+
+// The pick of a row that allows some token, but has no number above -infinity:
+// the lowest allowed -infinity, else the lowest allowed NaN. One CTA looks
+// through the row.
+__device__ __noinline__ int64_t pick_rest(const PickArgs& a, RowRules rules, int64_t row) {
+    __shared__ int lowest[2];
+    if (threadIdx.x < 2) lowest[threadIdx.x] = 0x7FFFFFFF;
+    __syncthreads();
+    constexpr int kEach = 8;
+    for (int64_t v0 = 0; v0 < a.V; v0 += kEach * kPickThreads) {
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t v = v0 + e * kPickThreads + threadIdx.x;
+            if (v >= a.V || !rules.allowed(v)) continue;
+            float x;
+            if (a.out != nullptr) {
+                x = __ldcg(a.out + row + v);  // adjusted already
+            } else {
+                x = a.logits[row + v];
+                if (x == x) {
+                    uint32_t count = 0;
+                    for (int i = rules.h0; i < rules.h1; ++i) count += a.history[i] == v;
+                    if (count) x = rules.penalise(x, count);
+                    x = rules.add_bias(a, x, static_cast<int>(v));
+                }
+            }
+            atomicMin(lowest + (x != x), static_cast<int>(v));
+        }
+        __syncthreads();
+        if (lowest[0] != 0x7FFFFFFF) break;  // (read by all before anyone writes again: the loop's barrier is next)
+        __syncthreads();
+    }
+    __syncthreads();
+    return lowest[0] != 0x7FFFFFFF ? lowest[0] : lowest[1];
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kPickThreads)
-    q4k_pick_kernel(const PickArgs a, int C) {
-    extern __shared__ uint32_t tables[];  // counts, bias indices: one word per logit of the chunk
+// kAligned: rows begin at multiples of 16 bytes. kApart: there are histories or biases.
+template <bool kAligned, bool kApart>
+__global__ void __launch_bounds__(kPickThreads, 3)
+    q4k_pick_kernel(const __grid_constant__ PickArgs a, int C, int table_groups) {
+    constexpr int T = kApart ? kPickThreads - kPickApart : kPickThreads;  // threads that stream
+    extern __shared__ __align__(16) uint8_t tables[];
     __shared__ unsigned long long best_s[kPickThreads / 32];
     __shared__ unsigned long long cluster_best[kPickMaxCluster];
+    __shared__ int ids_s[kApart ? kPickApart : 1], again_s[kApart ? kPickThreads : 1], listed, again;
     if (C > 1) cluster_arrive_relaxed();
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -46,142 +136,231 @@ __global__ void __launch_bounds__(kPickThreads)
     const int rank = blockIdx.x % C;
     const int64_t m = blockIdx.x / C;
     const int64_t V = a.V, row = m * V;
-    const int s = static_cast<int>(row & 3);  // the row begins s logits into its first group
-    const float* in = a.logits + (row - s);
-    float* out = a.out != nullptr ? a.out + (row - s) : nullptr;
-    const int64_t groups = (V + s + 3) >> 2, per = (groups + C - 1) / C;
-    const int64_t g_end = min(groups, (rank + 1) * per);
+    const int s = kAligned ? 0 : static_cast<int>(row & 3);  // the row begins s logits into its first group
+    const int groups = static_cast<int>((V + s + 3) >> 2), per = (groups + C - 1) / C;
+    const int g_begin = min(rank * per, groups), g_end = min(g_begin + per, groups);
 
-    int h0 = 0, h1 = 0, b0 = 0, b1 = 0;
-    float repeat = 1.f, presence = 0.f, frequency = 0.f;
-    if (a.history != nullptr) {
-        h0 = a.hist_starts[m];
-        h1 = a.hist_starts[m + 1];
-        repeat = a.penalties[3 * m];
-        presence = a.penalties[3 * m + 1];
-        frequency = a.penalties[3 * m + 2];
+    RowRules rules{0, 0, 0, 0, 1.f, 0.f, 0.f, a.mask != nullptr ? a.mask + m * ((V + 31) >> 5) : nullptr};
+    if (kApart && a.history != nullptr) {
+        rules.h0 = a.hist_starts[m];
+        rules.h1 = a.hist_starts[m + 1];
+        rules.repeat = a.penalties[3 * m];
+        rules.presence = a.penalties[3 * m + 1];
+        rules.frequency = a.penalties[3 * m + 2];
     }
-    if (a.bias_ids != nullptr) {
-        b0 = a.bias_starts[m];
-        b1 = a.bias_starts[m + 1];
+    if (kApart && a.bias_ids != nullptr) {
+        rules.b0 = a.bias_starts[m];
+        rules.b1 = a.bias_starts[m + 1];
     }
-    const bool counted = h1 > h0, biased = b1 > b0;
-    uint32_t* counts = tables;
-    uint32_t* places = tables + (a.history != nullptr ? 4 * kPickChunk : 0);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int e = 0; e < kPickGroups; ++e) {
-        if (counted) reinterpret_cast<uint4*>(counts)[tid + e * kPickThreads] = zero;
-        if (biased) reinterpret_cast<uint4*>(places)[tid + e * kPickThreads] = zero;
-    }
-    const uint32_t* mask = a.mask != nullptr ? a.mask + m * ((V + 31) >> 5) : nullptr;
+    const bool wide = rules.h1 - rules.h0 > 65535;
+    uint32_t* marks = reinterpret_cast<uint32_t*>(tables);
+    uint32_t* late = marks + pick_marks_bytes(table_groups) / 4;
+    uint32_t* counts = late + pick_marks_bytes(table_groups) / 4;
+    int2* list = reinterpret_cast<int2*>(counts + 2 * table_groups);  // token, its bias entry or -1; then its value's bits
+    const int step = kApart ? (wide ? table_groups / 2 : table_groups) : groups;  // groups that the tables cover at a time
 
-    uint32_t top = 0u, top_at = 0u;
-    for (int64_t ga = rank * per; ga < g_end; ga += kPickChunk) {
-        float x[kPickGroups][4];
-        uint32_t bits[kPickGroups];
+    Best best{-INFINITY, 0xFFFFFFFFu};
+    uint32_t any = rules.mask == nullptr;  // bits 0..3: some token is allowed
+    for (int g_tab = g_begin; g_tab < g_end; g_tab += step) {
+        const int n = min(step, g_end - g_tab);
+        const int64_t first = s - 4 * static_cast<int64_t>(g_tab);  // logit v is entry v + first of the tables
+        // a token's place in the tables, or -1
+        auto place = [&](int v) {
+            const int64_t at = v + first;
+            return v >= 0 && v < V && at >= 0 && at < 4 * n ? static_cast<int>(at) : -1;
+        };
+        auto adjusted = [&](int at, int v, float bias, bool has_bias) {
+            float y = a.logits[row + v];
+            const bool ok = rules.allowed(v);
+            if (rules.h1 > rules.h0) {
+                const uint32_t c = wide ? counts[at] : counts[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
+                if (c) y = rules.penalise(y, c);
+            }
+            if (has_bias) y = __fadd_rn(y, bias);
+            if (!ok) y = -INFINITY;
+            best.take(y, v);
+            return y;
+        };
+        float top = -INFINITY;  // the largest of this thread's groups, and the first logit that has it
+        uint32_t top_v = 0xFFFFFFFFu;
+        const float4* in = reinterpret_cast<const float4*>(a.logits + (row - s));
+        float4* out = reinterpret_cast<float4*>(a.out != nullptr ? a.out + (row - s) : nullptr);
+        // groups that the row fills
+        const int f0 = max(g_tab, s != 0 ? 1 : 0), f1 = min(g_tab + n, static_cast<int>((V + s) >> 2));
+        auto masked = [&](float4 y, const uint32_t* word, uint32_t sh) {
+            uint32_t ok = word[0];
+            if (kAligned)
+                ok >>= sh;
+            else
+                ok = __funnelshift_r(ok, sh > 28u ? word[1] : 0u, sh);
+            any |= ok & 15u;
+            y.x = ok & 1u ? y.x : -INFINITY;
+            y.y = ok & 2u ? y.y : -INFINITY;
+            y.z = ok & 4u ? y.z : -INFINITY;
+            y.w = ok & 8u ? y.w : -INFINITY;
+            return y;
+        };
+        if (!kApart || tid < T) {
+            // ------------------------------------------------------- the stream ---
+            // A thread's groups are T apart, a multiple of 8: their mask bits lie
+            // at the same place of words T / 8 apart.
+            int g = f0 + tid, top_g = -1;
+            const uint32_t mask_sh = (4u * g - s) & 31u;
+            const uint32_t* mask_p = rules.mask + ((4u * g - s) >> 5);
+            float4 top_y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (; g < f1; g += kPickBatch * T, mask_p += kPickBatch * (T / 8)) {
+                float4 x[kPickBatch] = {};
+                auto each = [&](int e) {
+                    float4 y = x[e];
+                    if (rules.mask != nullptr) y = masked(y, mask_p + e * (T / 8), mask_sh);
+                    if (out != nullptr) __stcs(out + (g + e * T), y);
+                    const float t = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+                    if (t > top) {
+                        top = t;
+                        top_y = y;
+                        top_g = g + e * T;
+                    }
+                };
+                if (g + (kPickBatch - 1) * T < f1) {
 #pragma unroll
-        for (int e = 0; e < kPickGroups; ++e) {
-            const int64_t g = ga + tid + e * kPickThreads, v0 = 4 * g - s;
-            bits[e] = 0u;
-            if (g >= g_end) continue;
-            if (v0 >= 0 && v0 + 4 <= V) {
-                const float4 f = __ldcs(reinterpret_cast<const float4*>(in) + g);
-                x[e][0] = f.x;
-                x[e][1] = f.y;
-                x[e][2] = f.z;
-                x[e][3] = f.w;
-                bits[e] = 15u;
-            } else {
+                    for (int e = 0; e < kPickBatch; ++e) x[e] = __ldcs(in + g + e * T);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool is = v0 + k >= 0 && v0 + k < V;
-                    x[e][k] = is ? in[4 * g + k] : 0.f;
-                    bits[e] |= is ? 1u << k : 0u;
-                }
-            }
-            if (mask != nullptr) {
-                const int64_t w = (v0 < 0 ? 0 : v0) >> 5;
-                const int sh = static_cast<int>(v0 & 31);
-                const uint32_t lo = mask[w];
-                uint32_t ok;
-                if (v0 < 0)
-                    ok = lo << -v0;
-                else
-                    ok = __funnelshift_r(lo, sh > 28 && 32 * (w + 1) < V ? mask[w + 1] : 0u, sh);
-                bits[e] |= (~ok & 15u) << 4;  // forbidden
-            }
-        }
-        if (counted || biased) {
-            __syncthreads();  // the tables are clear
-            // logit v of the row is entry v + first of the chunk's tables
-            const int64_t first = s - 4 * ga;
-            const int64_t entries = 4 * min(static_cast<int64_t>(kPickChunk), g_end - ga);
-            for (int i = h0 + tid; i < h1; i += kPickThreads) {
-                const int v = a.history[i];
-                const int64_t at = v + first;
-                if (v >= 0 && v < V && at >= 0 && at < entries) atomicAdd(counts + at, 1u);
-            }
-            for (int i = b0 + tid; i < b1; i += kPickThreads) {
-                const int v = a.bias_ids[i];
-                const int64_t at = v + first;
-                if (v >= 0 && v < V && at >= 0 && at < entries) atomicMax(places + at, static_cast<uint32_t>(i - b0) + 1u);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int e = 0; e < kPickGroups; ++e) {
-            const int64_t g = ga + tid + e * kPickThreads, v0 = 4 * g - s;
-            if (g >= g_end) continue;
-            if (counted) {
-                uint4* slot = reinterpret_cast<uint4*>(counts) + tid + e * kPickThreads;
-                const uint4 c4 = *slot;
-                if ((c4.x | c4.y | c4.z | c4.w) != 0u) {
-                    *slot = zero;  // for the next chunk
-                    const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c[k] != 0u) {
-                            const float y = x[e][k] > 0.f ? __fdiv_rn(x[e][k], repeat) : __fmul_rn(x[e][k], repeat);
-                            x[e][k] = __fsub_rn(__fsub_rn(y, __fmul_rn(static_cast<float>(c[k]), frequency)), presence);
-                        }
-                }
-            }
-            if (biased) {
-                uint4* slot = reinterpret_cast<uint4*>(places) + tid + e * kPickThreads;
-                const uint4 p4 = *slot;
-                if ((p4.x | p4.y | p4.z | p4.w) != 0u) {
-                    *slot = zero;
-                    const uint32_t p[4] = {p4.x, p4.y, p4.z, p4.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (p[k] != 0u) x[e][k] = __fadd_rn(x[e][k], a.bias[b0 + p[k] - 1u]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool allowed = (bits[e] >> k & 0x11u) == 1u;
-                if ((bits[e] >> (k + 4)) & 1u) x[e][k] = -INFINITY;
-                const uint32_t o = pick_order(x[e][k], allowed);
-                if (o > top) {
-                    top = o;
-                    top_at = static_cast<uint32_t>(v0 + k);
-                }
-            }
-            if (out != nullptr) {
-                if ((bits[e] & 15u) == 15u) {
-                    __stcs(reinterpret_cast<float4*>(out) + g, make_float4(x[e][0], x[e][1], x[e][2], x[e][3]));
+                    for (int e = 0; e < kPickBatch; ++e) each(e);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (bits[e] >> k & 1u) out[4 * g + k] = x[e][k];
+                    for (int e = 0; e < kPickBatch; ++e)
+                        if (g + e * T < f1) x[e] = __ldcs(in + g + e * T);
+#pragma unroll
+                    for (int e = 0; e < kPickBatch; ++e)
+                        if (g + e * T < f1) each(e);
                 }
             }
+            if (top_g >= 0)
+                top_v = 4u * top_g - s + (top_y.x == top ? 0u : top_y.y == top ? 1u : top_y.z == top ? 2u : 3u);
+        } else {
+            // -------------------------------------------- the tokens set apart ---
+            const int t = tid - T;
+            auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kPickApart) : "memory"); };
+            const int h0 = rules.h0, h1 = rules.h1, b0 = rules.b0, b1 = rules.b1;
+            if (t == 0) listed = again = 0;
+            for (int i = t; i < (n + 7) / 8; i += kPickApart) marks[i] = late[i] = 0u;
+            if (h1 > h0)
+                for (int i = t; i < (n + 1) / 2 * (wide ? 2 : 1); i += kPickApart)
+                    reinterpret_cast<uint4*>(counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+            sync();
+            auto enlist = [&](int at, int v, int bias_at) {
+                const int k = atomicAdd(&listed, 1);
+                if (k < kPickList)
+                    list[k] = make_int2(v, bias_at);
+                else
+                    atomicOr(late + (at >> 5), 1u << (at & 31));
+            };
+            // biases: the last entry of a token counts, so the entries go by from
+            // the end, a block at a time, and yield to a later one of their block
+            for (int i1 = b1; i1 > b0; i1 -= kPickApart) {
+                const int i0 = max(b0, i1 - kPickApart), k = i1 - i0;
+                const int v = t < k ? a.bias_ids[i0 + t] : -1;
+                ids_s[t] = v;
+                sync();
+                bool later = false;
+                for (int j = t + 1; j < k; ++j) later |= ids_s[j] == v;
+                const int at = place(v);
+                if (at >= 0 && !later) {
+                    const uint32_t bit = 1u << (at & 31);
+                    if (!(atomicOr(marks + (at >> 5), bit) & bit)) enlist(at, v, i0 + t);
+                }
+                sync();
+            }
+            constexpr int kUnroll = 8;  // history entries in flight
+            for (int i0 = h0 + t; i0 < h1; i0 += kUnroll * kPickApart) {
+                int v[kUnroll];
+#pragma unroll
+                for (int e = 0; e < kUnroll; ++e) v[e] = i0 + e * kPickApart < h1 ? a.history[i0 + e * kPickApart] : -1;
+#pragma unroll
+                for (int e = 0; e < kUnroll; ++e) {
+                    const int at = place(v[e]);
+                    if (at < 0) continue;
+                    const int sh = wide ? 0 : 16 * (at & 1);
+                    const uint32_t old = atomicAdd(counts + (wide ? at : at >> 1), 1u << sh);
+                    if (wide ? old != 0u : (old >> sh & 0xFFFFu) != 0u) continue;
+                    const uint32_t bit = 1u << (at & 31);
+                    if (!(atomicOr(marks + (at >> 5), bit) & bit)) enlist(at, v[e], -1);  // (else a bias has it)
+                }
+            }
+            sync();
+            for (int i = t; i < min(listed, kPickList); i += kPickApart) {
+                const int2 e = list[i];
+                const float bias = e.y >= 0 ? a.bias[e.y] : 0.f;
+                list[i].y = __float_as_int(adjusted(place(e.x), e.x, bias, e.y >= 0));
+            }
         }
+        auto marked = [&](int64_t v) { return kApart && (marks[(v + first) >> 5] >> ((v + first) & 31) & 1u); };
+        if (kApart) {
+            __syncthreads();  // all is listed, and the logits are written
+            if (a.out != nullptr)
+                for (int i = tid; i < min(listed, kPickList); i += kPickThreads)
+                    a.out[row + list[i].x] = __int_as_float(list[i].y);
+            if (listed > kPickList) {  // the others, by whoever takes them first
+                auto take = [&](int v) {
+                    const int at = place(v);
+                    if (at < 0) return;
+                    const uint32_t bit = 1u << (at & 31);
+                    if (!(atomicAnd(late + (at >> 5), ~bit) & bit)) return;
+                    float bias = 0.f;
+                    bool has_bias = false;
+                    for (int i = rules.b1 - 1; i >= rules.b0 && !has_bias; --i)
+                        if (a.bias_ids[i] == v) {
+                            bias = a.bias[i];
+                            has_bias = true;
+                        }
+                    const float y = adjusted(at, v, bias, has_bias);
+                    if (a.out != nullptr) a.out[row + v] = y;
+                };
+                for (int i = rules.h0 + tid; i < rules.h1; i += kPickThreads) take(a.history[i]);
+                for (int i = rules.b0 + tid; i < rules.b1; i += kPickThreads) take(a.bias_ids[i]);
+            }
+        }
+        if (top_v != 0xFFFFFFFFu) {
+            if (!marked(top_v))
+                best.take(top, top_v);
+            else
+                again_s[atomicAdd(&again, 1)] = tid;
+        }
+        if (kApart) {
+            __syncthreads();
+            // the logits of a thread whose largest was set apart, without those that were
+            for (int i = warp; i < again; i += kPickThreads / 32)
+                for (int g = f0 + again_s[i] + lane * T; g < f1; g += 32 * T) {
+                    float4 y = out != nullptr ? __ldcg(out + g) : in[g];
+                    const uint32_t v0 = 4u * g - s;
+                    if (out == nullptr && rules.mask != nullptr) y = masked(y, rules.mask + (v0 >> 5), v0 & 31u);
+                    const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (!marked(v0 + k)) best.take(z[k], v0 + k);
+                }
+        }
+        // the logits of the groups at the row's ends that it fills in part
+        if (tid < 8) {
+            const int64_t v = tid < 4 ? tid : ((V + s) >> 2 << 2) - s + (tid - 4);
+            const int64_t at = v + first;
+            const bool mine = tid < 4 ? s != 0 && tid < 4 - s : v >= (s != 0 ? 4 - s : 0);
+            if (mine && v < V && at >= 0 && at < 4 * n && !marked(v)) {
+                const bool ok = rules.allowed(v);
+                any |= ok;
+                const float y = ok ? a.logits[row + v] : -INFINITY;
+                if (a.out != nullptr) a.out[row + v] = y;
+                best.take(y, static_cast<uint32_t>(v));
+            }
+        }
+        if (kApart && g_tab + step < g_end) __syncthreads();  // the tables are read
     }
 
-    // larger value first, then lower index
-    unsigned long long key = static_cast<unsigned long long>(top) << 32 | (0xFFFFFFFFu - top_at);
+    if (a.pick == nullptr) {
+        if (C > 1) cluster_wait();  // (each arrival waits once)
+        return;
+    }
+    unsigned long long key = best.key(any != 0u);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
@@ -189,13 +368,11 @@ __global__ void __launch_bounds__(kPickThreads)
     }
     if (lane == 0) best_s[warp] = key;
     __syncthreads();
-    if (warp == 0) {
-        key = lane < kPickThreads / 32 ? best_s[lane] : 0ull;
+    key = lane < kPickThreads / 32 ? best_s[lane] : 0ull;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
-            key = k > key ? k : key;
-        }
+    for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
+        key = k > key ? k : key;
     }
     if (C > 1) {
         cluster_wait();  // every CTA of the cluster has begun
@@ -204,24 +381,58 @@ __global__ void __launch_bounds__(kPickThreads)
                          "l"(key)
                          : "memory");
         cluster_sync_all();
-        if (rank == 0 && tid == 0)
+        if (rank == 0)
             for (int r = 0; r < C; ++r) key = cluster_best[r] > key ? cluster_best[r] : key;
     }
-    if (rank == 0 && tid == 0 && a.pick != nullptr)
-        a.pick[m] = (key >> 32) == 0ull ? -1 : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    if (rank != 0) return;
+    int64_t pick = key == 0ull ? -1 : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    if (key == 1ull) {
+        __syncthreads();
+        pick = pick_rest(a, rules, row);
+    }
+    if (tid == 0) a.pick[m] = pick;
 }
 
 cudaError_t launch_pick(const PickArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
-    // as many CTAs per row as still run at once, and no more than have a chunk's worth
-    int C = kPickMaxCluster;
-    while (C > 1 && (a.M * C > 3 * dev.num_sms || (a.V + 3) / 4 <= static_cast<int64_t>(kPickChunk) * (C / 2))) C /= 2;
-    const size_t smem = static_cast<size_t>((a.history != nullptr) + (a.bias_ids != nullptr)) * 16 * kPickChunk;
-    return launch_serve(q4k_pick_kernel, dim3(static_cast<unsigned>(a.M * C)), dim3(kPickThreads), smem, stream, pdl, C,
-                        a, C);
+    // as many CTAs per row as still run at once, and none without a batch for every thread
+    const int64_t groups = (a.V + 6) / 4;
+    int64_t C = std::min<int64_t>(groups / (kPickThreads * kPickBatch) + 1, kPickMaxCluster);
+    while (C > 1 && a.M > dev.pick_clusters[C]) --C;
+    const int64_t per = (groups + C - 1) / C;
+    const int table_groups = static_cast<int>(std::min<int64_t>(kPickTableGroups, (per + 31) / 32 * 32));
+    const bool aligned = a.V % 4 == 0, apart = a.history != nullptr || a.bias_ids != nullptr;
+    auto kernel = aligned ? (apart ? q4k_pick_kernel<true, true> : q4k_pick_kernel<true, false>)
+                          : (apart ? q4k_pick_kernel<false, true> : q4k_pick_kernel<false, false>);
+    return launch_serve(kernel, dim3(static_cast<unsigned>(a.M * C)), dim3(kPickThreads),
+                        apart ? pick_tables_bytes(table_groups) : 0, stream, pdl, static_cast<int>(C), a,
+                        static_cast<int>(C), table_groups);
 }
 
-cudaError_t pick_setup() {
-    return cudaFuncSetAttribute(q4k_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 16 * kPickChunk);
+cudaError_t pick_setup(DeviceInfo& dev) {
+    const int smem = pick_tables_bytes(kPickTableGroups);
+    cudaError_t e = cudaFuncSetAttribute(q4k_pick_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(q4k_pick_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    for (int c = 2; c <= kPickMaxCluster; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(c);
+        cfg.blockDim = dim3(kPickThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = c;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, q4k_pick_kernel<true, true>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        dev.pick_clusters[c] = n;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace q4k

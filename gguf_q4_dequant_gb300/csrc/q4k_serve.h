@@ -96,7 +96,7 @@ struct PickArgs {
     const uint32_t* mask;
     int64_t M, V;
 };
-cudaError_t pick_setup();
+cudaError_t pick_setup(DeviceInfo& dev);  // fills dev.pick_clusters
 cudaError_t launch_pick(const PickArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
 
 // Launch with programmatic stream serialisation when the PDL mode asks for it

@@ -678,5 +678,38 @@ def test_pick_special_values(q4k):
     allowed[5, :40] = False
     allowed[6, 10] = False
     allowed[7, :150] = False
-    _, got = pick_run(q4k, x, allowed=allowed)
-    assert got.tolist() == [7, 0, 0, 9, 100, 40, 20, 150]
+    for keep in (True, False):
+        _, got = pick_run(q4k, x, allowed=allowed, keep=keep)
+        assert got.tolist() == [7, 0, 0, 9, 100, 40, 20, 150]
+    # adjusted to -inf and NaN: a ban by bias, infinities that meet, in rows that have nothing else
+    x = np.full((4, V), -inf, np.float32)
+    x[0, :] = 1.0
+    x[1, 3:6] = 2.0
+    x[2, :] = nan
+    x[2, 77] = inf
+    x[3, 9] = inf
+    allowed = np.zeros((4, V), bool)
+    allowed[0, [20, 30]] = True    # both banned
+    allowed[1, 3:6] = True         # one of them not
+    allowed[2, 70:80] = True       # inf - inf is NaN like the others
+    allowed[3, [9, 12]] = True     # inf - inf is NaN, -inf beside it
+    bias = [[(20, -inf), (30, -inf)], [(3, -inf), (4, -inf), (5, -1.0)], [(77, -inf)], [(9, -inf)]]
+    hist = [[20, 20, 30], [], [], [12]]
+    pen = [[1.0, 0.5, 0.5]] * 4
+    for keep in (True, False):
+        out, got = pick_run(q4k, x, hist, pen, bias, allowed, keep=keep)
+        assert got.tolist() == [20, 5, 70, 12]
+
+
+@pytest.mark.parametrize("R,V", [(1, 300000), (2, 151937), (600, 70001)])
+def test_pick_long_rows_and_histories(q4k, R, V):
+    """More logits than one set of tables covers, and a token that occurs more often than 16 bits count."""
+    rng = np.random.default_rng(V)
+    x = (rng.integers(-40, 41, (R, V)) / 8).astype(np.float32)
+    long_one = 70000 if R < 10 else 50
+    hist = [[int(rng.integers(0, V))] * long_one + rng.integers(0, V, 90).tolist() for _ in range(R)]
+    pen = [[2.0, 0.5, 1.0 / 1024]] * R
+    bias = [[(int(v), float(rng.integers(-16, 17)) / 4) for v in rng.integers(0, V, 5)] for _ in range(R)]
+    y, best, _ = pick_ref(x, hist, pen, bias, None)
+    out, got = pick_run(q4k, x, hist, pen, bias)
+    assert np.array_equal(got, best) and np.array_equal(out, y.astype(np.float32))
