@@ -205,6 +205,9 @@ __global__ void __launch_bounds__(kPickThreads, 3)
             // A thread's groups are T apart, a multiple of 8: their mask bits lie
             // at the same place of words T / 8 apart.
             int g = f0 + tid, top_g = -1;
+            // asked for at once, into L2: a thread's own loads are too few to fill the memory's queue
+            if (tid == 0 && f1 > f0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(in + f0), "r"(16 * (f1 - f0)) : "memory");
             const uint32_t mask_sh = (4u * g - s) & 31u;
             const uint32_t* mask_p = rules.mask + ((4u * g - s) >> 5);
             float4 top_y = make_float4(0.f, 0.f, 0.f, 0.f);
