@@ -116,6 +116,7 @@ void init_device(int dev, DeviceState& st) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess || gemv_setup(st.info) != cudaSuccess || tcgemv_setup(st.info) != cudaSuccess ||
         gemm_setup(st.info) != cudaSuccess || attn_setup(st.info) != cudaSuccess || pick_setup(st.info) != cudaSuccess ||
+        pages_setup() != cudaSuccess ||
         encoder() == nullptr) {
         st.status = Q4K_ERR_CUDA;
         return;

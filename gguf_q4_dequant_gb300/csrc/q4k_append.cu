@@ -8,7 +8,10 @@
 // 16-byte load, one 8-byte store): adjacent pairs lie in one lane, and the
 // partner of a pair (i, i + head_dim/2) is half a row's lanes away, so both
 // pairings and the norm's sum stay inside the row's lanes. One block per token
-// finds the token's sequence and page once for all heads.
+// finds the token's sequence and page once for all heads, while the first rows
+// are on their way: that takes four loads, each from the result of the one
+// before (26 us for 2894 tokens of 48 rows when the rows were loaded after it,
+// and the norm's and rotation's steps were taken whether wanted or not).
 #include <cuda_bf16.h>
 
 #include "q4k_device.cuh"
@@ -23,16 +26,33 @@ __device__ __forceinline__ uint2 bf16x4(float4 x) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppThreads)
+constexpr int kAppRows = 6;  // rows that a thread has in flight
+
+template <int D, int kPairs, bool kNorm>
+__global__ void __launch_bounds__(kAppThreads, 4)
     q4k_append_kernel(const CacheLayer c, const Batch b, const float* __restrict__ Yq,
                       const float* __restrict__ Yk, const float* __restrict__ Yv,
-                      uint16_t* __restrict__ q_out, int heads, const float* __restrict__ rope, int pairs,
+                      uint16_t* __restrict__ q_out, int heads, const float* __restrict__ rope,
                       const float* __restrict__ q_norm, const float* __restrict__ k_norm, float eps) {
-    constexpr int L = D / 4;  // lanes per row
+    constexpr int L = D / 4;                // lanes per row
+    constexpr int kStep = kAppThreads / L;  // rows that the block holds at a time
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
-    const int t = blockIdx.x;
+    const int t = blockIdx.x, G = c.kv_heads, rows = heads + 2 * G;
+    const int lane = threadIdx.x % L, r = threadIdx.x / L;
+    float4 x[kAppRows];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int e = 0; e < kAppRows; ++e) {
+            const int h = h0 + e * kStep;
+            if (h >= rows) continue;
+            const float* src = h < heads       ? Yq + (static_cast<int64_t>(t) * heads + h) * D
+                               : h < heads + G ? Yk + (static_cast<int64_t>(t) * G + h - heads) * D
+                                               : Yv + (static_cast<int64_t>(t) * G + h - heads - G) * D;
+            x[e] = __ldcs(reinterpret_cast<const float4*>(src) + lane);
+        }
+    };
+    load(r);
     // the sequence: as many of starts[1 ..] as are not above t
     int i = 0;
     for (int j = 0; j < b.n; j += kAppThreads)
@@ -40,20 +60,19 @@ __global__ void __launch_bounds__(kAppThreads)
     int64_t pos = -1, off = -1;
     if (i < b.n) {
         const SeqView s = seq_view(c, b, i);
-        const int r = t - s.t0;
-        if (r >= 0 && r < s.m) pos = static_cast<int64_t>(s.len) - s.m + r;
+        const int at = t - s.t0;
+        if (at >= 0 && at < s.m) pos = static_cast<int64_t>(s.len) - s.m + at;
         if (pos >= 0) {
             const int page = c.table[s.row + (pos >> c.page_shift)];
             if (page >= 0 && page < c.n_pages)
                 off = page * c.page_stride + (pos & ((1 << c.page_shift) - 1)) * D;
         }
     }
-    const int lane = threadIdx.x % L;
+    // the new element is x * cs + (the pair's other element) * sn
     float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool turn = pairs != 0 && pos >= 0;
-    if (turn) {
+    if (kPairs != 0 && pos >= 0) {
         const float* row = rope + pos * D;
-        if (pairs == 1) {
+        if (kPairs == 1) {
             const float2 c2 = *reinterpret_cast<const float2*>(row + 2 * lane);
             const float2 s2 = *reinterpret_cast<const float2*>(row + D / 2 + 2 * lane);
             cs = make_float4(c2.x, c2.x, c2.y, c2.y);
@@ -65,58 +84,70 @@ __global__ void __launch_bounds__(kAppThreads)
             if (lane < L / 2) sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
         }
     }
-    const int G = c.kv_heads, rows = heads + 2 * G;
+    const bool turn = kPairs != 0 && pos >= 0;
     // whole warps keep together: the shuffles need every lane of a row
-    for (int h0 = 0; h0 < rows; h0 += kAppThreads / L) {
-        const int h = h0 + threadIdx.x / L;
-        const bool in = h < rows;
-        const bool is_q = h < heads, is_v = h >= heads + G;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in) {
-            const float* src = is_q   ? Yq + (static_cast<int64_t>(t) * heads + h) * D
-                               : is_v ? Yv + (static_cast<int64_t>(t) * G + h - heads - G) * D
-                                      : Yk + (static_cast<int64_t>(t) * G + h - heads) * D;
-            x = __ldcs(reinterpret_cast<const float4*>(src) + lane);
-        }
-        const float* w = is_q ? q_norm : is_v ? nullptr : k_norm;
-        float ss = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w;
+    for (int h0 = r; h0 - r < rows; h0 += kAppRows * kStep) {
+        if (h0 != r) load(h0);
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w != nullptr) {
-            const float4 wv = *reinterpret_cast<const float4*>(w + 4 * lane);
-            const float f = 1.f / sqrtf(ss * (1.f / D) + eps);
-            x = make_float4(x.x * f * wv.x, x.y * f * wv.y, x.z * f * wv.z, x.w * f * wv.w);
-        }
-        float4 y;  // the other element of each pair
-        if (pairs == 2) {
-            y.x = __shfl_xor_sync(0xffffffffu, x.x, L / 2);
-            y.y = __shfl_xor_sync(0xffffffffu, x.y, L / 2);
-            y.z = __shfl_xor_sync(0xffffffffu, x.z, L / 2);
-            y.w = __shfl_xor_sync(0xffffffffu, x.w, L / 2);
-        } else {
-            y = make_float4(x.y, x.x, x.w, x.z);
-        }
-        if (turn && !is_v)
-            x = make_float4(x.x * cs.x + y.x * sn.x, x.y * cs.y + y.y * sn.y, x.z * cs.z + y.z * sn.z,
-                            x.w * cs.w + y.w * sn.w);
-        if (!in) continue;
-        if (is_q) {
-            *(reinterpret_cast<uint2*>(q_out + (static_cast<int64_t>(t) * heads + h) * D) + lane) = bf16x4(x);
-        } else if (off >= 0) {
-            const int g = is_v ? h - heads - G : h - heads;
-            uint16_t* dst = (is_v ? c.v : c.k) + off + (static_cast<int64_t>(g) << c.page_shift) * D;
-            *(reinterpret_cast<uint2*>(dst) + lane) = bf16x4(x);
+        for (int e = 0; e < kAppRows; ++e) {
+            if (h0 - r + e * kStep >= rows) break;
+            const int h = h0 + e * kStep;
+            const bool in = h < rows, is_q = h < heads, is_v = h >= heads + G;
+            float4 y = in ? x[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (kNorm) {
+                const float* w = is_q ? q_norm : is_v ? nullptr : k_norm;
+                float ss = y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (w != nullptr) {
+                    const float4 wv = *reinterpret_cast<const float4*>(w + 4 * lane);
+                    const float f = 1.f / sqrtf(ss * (1.f / D) + eps);
+                    y = make_float4(y.x * f * wv.x, y.y * f * wv.y, y.z * f * wv.z, y.w * f * wv.w);
+                }
+            }
+            if (kPairs != 0) {
+                float4 z;  // the other element of each pair
+                if (kPairs == 2) {
+                    z.x = __shfl_xor_sync(0xffffffffu, y.x, L / 2);
+                    z.y = __shfl_xor_sync(0xffffffffu, y.y, L / 2);
+                    z.z = __shfl_xor_sync(0xffffffffu, y.z, L / 2);
+                    z.w = __shfl_xor_sync(0xffffffffu, y.w, L / 2);
+                } else {
+                    z = make_float4(y.y, y.x, y.w, y.z);
+                }
+                if (turn && !is_v)
+                    y = make_float4(y.x * cs.x + z.x * sn.x, y.y * cs.y + z.y * sn.y, y.z * cs.z + z.z * sn.z,
+                                    y.w * cs.w + z.w * sn.w);
+            }
+            if (is_q) {
+                *(reinterpret_cast<uint2*>(q_out + (static_cast<int64_t>(t) * heads + h) * D) + lane) = bf16x4(y);
+            } else if (in && off >= 0) {
+                const int g = is_v ? h - heads - G : h - heads;
+                uint16_t* dst = (is_v ? c.v : c.k) + off + (static_cast<int64_t>(g) << c.page_shift) * D;
+                *(reinterpret_cast<uint2*>(dst) + lane) = bf16x4(y);
+            }
         }
     }
+}
+
+template <int D>
+static cudaError_t launch_d(const CacheLayer& c, const Batch& b, const float* Yq, const float* Yk, const float* Yv,
+                            uint16_t* q_out, int heads, const float* rope, int pairs, const float* q_norm,
+                            const float* k_norm, float eps, cudaStream_t stream, int pdl) {
+    const bool norm = q_norm != nullptr || k_norm != nullptr;
+    auto kernel = pairs == 0   ? (norm ? q4k_append_kernel<D, 0, true> : q4k_append_kernel<D, 0, false>)
+                  : pairs == 1 ? (norm ? q4k_append_kernel<D, 1, true> : q4k_append_kernel<D, 1, false>)
+                               : (norm ? q4k_append_kernel<D, 2, true> : q4k_append_kernel<D, 2, false>);
+    return launch_serve(kernel, dim3(b.tokens), dim3(kAppThreads), 0, stream, pdl, 1, c, b, Yq, Yk, Yv, q_out,
+                        heads, rope, q_norm, k_norm, eps);
 }
 
 cudaError_t launch_append(const CacheLayer& c, const Batch& b, const float* Yq, const float* Yk,
                           const float* Yv, uint16_t* q_out, int heads, int head_dim, const float* rope,
                           int pairs, const float* q_norm, const float* k_norm, float eps,
                           cudaStream_t stream, int pdl) {
-    auto kernel = head_dim == 64 ? q4k_append_kernel<64> : q4k_append_kernel<128>;
-    return launch_serve(kernel, dim3(b.tokens), dim3(kAppThreads), 0, stream, pdl, 1, c, b, Yq, Yk, Yv, q_out,
-                        heads, rope, pairs, q_norm, k_norm, eps);
+    return (head_dim == 64 ? launch_d<64> : launch_d<128>)(c, b, Yq, Yk, Yv, q_out, heads, rope, pairs, q_norm,
+                                                           k_norm, eps, stream, pdl);
 }
 
 }  // namespace q4k

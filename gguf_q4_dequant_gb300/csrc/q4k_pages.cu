@@ -197,41 +197,48 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // Forks. Every block works out the whole plan for itself from the state (a few
-// thousand loads at most), counts itself in, and copies its share of the pages;
-// the block that counts in last, when no block reads the state any more, writes
-// the new tables, lengths, references and the statuses.
+// loads; the plan lies in shared memory, three words per fork) and counts itself
+// in. The block that counts in last, when no block reads any more what it
+// changes, writes the new tables, lengths, references and the statuses; all copy
+// their share of the pages. (Parents' lengths and tables do not change.)
 __global__ void __launch_bounds__(kCopyThreads)
     q4k_pages_fork_kernel(const PageGeom g, const int32_t* __restrict__ parents,
                           const int32_t* __restrict__ children, int n, int32_t* __restrict__ status, int n_seqs,
                           int width, int page_size, int64_t n_pages, int32_t* refs, int32_t* table,
                           int32_t* lens, int parts, uint32_t* ticket) {
-    __shared__ int32_t rank_s[kMaxBatch];   // copies before i, or ~that where i may not fork
-    __shared__ int32_t fresh[kMaxBatch];    // the lowest free pages
+    extern __shared__ int32_t plan_s[];
+    int32_t* rank_s = plan_s;        // copies before i, or ~that where i may not fork
+    int32_t* src_s = plan_s + n;     // the parent's last page if it is copied, else -1
+    int32_t* fresh = plan_s + 2 * n; // the lowest free pages
     __shared__ int warp_sums[32];
     __shared__ bool last;
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
     const int64_t cap = static_cast<int64_t>(width) * page_size;
     auto length = [&](int id) { return static_cast<int>(min(max(static_cast<int64_t>(lens[id]), int64_t(0)), cap)); };
-    auto last_page = [&](int id, int len) { return table[static_cast<int64_t>(id) * width + len / page_size]; };
     int copies = 0;
     for (int i0 = 0; i0 < n; i0 += kCopyThreads) {
         const int i = i0 + threadIdx.x;
-        bool may = false, need = false;
+        bool may = false;
+        int src = -1;
         if (i < n) {
             const int p = parents[i], ch = children[i];
             if (p >= 0 && p < n_seqs && ch >= 0 && ch < n_seqs && lens[ch] == 0) {
                 const int len = length(p);
                 may = true;
                 if (len % page_size != 0) {
-                    const int src = last_page(p, len);
-                    need = may = src >= 0 && src < n_pages;
+                    src = table[static_cast<int64_t>(p) * width + len / page_size];
+                    if (src >= n_pages) src = -1;
+                    may = src >= 0;
                 }
             }
         }
         int here;
-        const int r = copies + block_rank<kCopyThreads>(need, warp_sums, here);
-        if (i < n) rank_s[i] = may ? r : ~r;
+        const int r = copies + block_rank<kCopyThreads>(src >= 0, warp_sums, here);
+        if (i < n) {
+            rank_s[i] = may ? r : ~r;
+            src_s[i] = src;
+        }
         copies += here;
     }
     int found = 0;
@@ -245,22 +252,20 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
     found = min(found, copies);
     __syncthreads();
-    // this block's share of the copies: (child, layer, K or V, part)
-    const int64_t per_child = static_cast<int64_t>(g.layers) * 2 * parts, total = n * per_child;
-    for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-        const int i = static_cast<int>(w / per_child);
-        const int r = rank_s[i];
-        if (r < 0 || r >= found) continue;
-        const int p = parents[i], len = length(p);
-        if (len % page_size == 0) continue;
-        const int u = static_cast<int>(w - i * per_child);
-        copy_part(g, last_page(p, len), fresh[r], u / (2 * parts), (u / parts) & 1, u % parts);
-    }
-    __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         last = atomicAdd(ticket, 1u) == gridDim.x - 1;
         if (last) *ticket = 0u;
+    }
+    // this block's share of the copies: (child, layer, K or V, part)
+    const int per_child = g.layers * 2 * parts;
+    const int64_t total = static_cast<int64_t>(n) * per_child;
+    for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+        const int i = total <= 0x7FFFFFFF ? static_cast<int>(w) / per_child : static_cast<int>(w / per_child);
+        const int r = rank_s[i];
+        if (src_s[i] < 0 || r < 0 || r >= found) continue;
+        const int u = static_cast<int>(w - static_cast<int64_t>(i) * per_child);
+        copy_part(g, src_s[i], fresh[r], u / (2 * parts), (u / parts) & 1, u % parts);
     }
     __syncthreads();
     if (!last) return;
@@ -270,7 +275,8 @@ __global__ void __launch_bounds__(kCopyThreads)
         bool ok = r >= 0;
         if (ok) {
             const int p = parents[i], ch = children[i], len = length(p);
-            const int full = len / page_size, part = len % page_size != 0;
+            const int full = len / page_size;
+            const bool part = src_s[i] >= 0;
             ok = !part || r < found;
             if (ok) {
                 const int32_t* from = table + static_cast<int64_t>(p) * width;
@@ -396,9 +402,14 @@ cudaError_t launch_pages_fork(const q4k_cache& c, const int32_t* parents, const 
     const PageGeom g = geom(c);
     const int parts = parts_per_page(g);
     return launch_serve(q4k_pages_fork_kernel,
-                        dim3(copy_grid(static_cast<int64_t>(n) * g.layers * 2 * parts, dev)), dim3(kCopyThreads), 0,
-                        stream, pdl, 1, g, parents, children, n, status, c.n_seqs, c.width, c.page_size,
+                        dim3(copy_grid(static_cast<int64_t>(n) * g.layers * 2 * parts, dev)), dim3(kCopyThreads),
+                        12 * static_cast<size_t>(n), stream, pdl, 1, g, parents, children, n, status, c.n_seqs, c.width, c.page_size,
                         c.n_pages, c.refs, c.table, c.lens, parts, counters + kPageTicket);
+}
+
+cudaError_t pages_setup() {
+    // 48 KB of plan for the most forks, beside the kernel's own
+    return cudaFuncSetAttribute(q4k_pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kMaxBatch);
 }
 
 int64_t pages_scratch_bytes(int64_t n_pages) { return 256 + 4 * (2 * (n_pages / 2 + 1) + n_pages); }

@@ -83,6 +83,7 @@ cudaError_t launch_pages_copy(const q4k_cache& c, const int32_t* src, const int3
 cudaError_t launch_pages_compact(const q4k_cache& c, void* scratch, cudaStream_t stream,
                                  const DeviceInfo& dev, int pdl);
 int64_t pages_scratch_bytes(int64_t n_pages);
+cudaError_t pages_setup();
 
 struct PickArgs {
     const float* logits;

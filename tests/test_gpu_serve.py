@@ -553,6 +553,35 @@ def test_page_calls(q4k, seed, page, kv, dim, n_pages, layers, n_seqs, shared):
     assert refused > 0 or n_pages > 1000
 
 
+def test_most_sequences(q4k):
+    """4096 sequences in one call: reserve, fork, append, attention and free."""
+    n, page, dim = 4096, 16, 64
+    k = torch.randn(1, 2 * n, 1, page, dim, device=DEV).to(torch.bfloat16)
+    cache = q4k.Cache(k, torch.randn_like(k), ints([0] * (2 * n)),
+                      torch.full((2 * n, 4), -1, dtype=torch.int32, device=DEV), ints([0] * (2 * n)))
+    model, ws = Model(cache), cache.workspace()
+    news = [1 + i % 20 for i in range(n)]
+    starts, status = ints(np.concatenate([[0], np.cumsum(news)])), ints([9] * n)
+    q4k.q4k_pages_reserve(cache, None, starts, status)
+    assert status.tolist() == model.reserve(range(n), news) and sum(status.tolist()) == 0
+    kids = list(range(n, 2 * n))
+    q4k.q4k_pages_fork(cache, ints(range(n)), ints(kids), status, ws)
+    want = model.fork(list(range(n)), kids)
+    assert status.tolist() == want and 0 < sum(want) < n
+    model.check(cache)
+    T = sum(news)
+    Y = [torch.randn(T, dim, device=DEV) for _ in range(3)]
+    q = torch.empty(T, 1, dim, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_cache_append(cache, 0, None, starts, *Y, q, 1)
+    out = attend(q4k, cache, 0, None, news, q, 1, ws=ws)
+    picks = [0, 17, 2000, 4095]
+    rows = [r for s in picks for r in range(sum(news[:s]), sum(news[:s + 1]))]
+    y, tol = attention_ref(cache, 0, picks, [news[s] for s in picks], q[rows], 1, dim ** -0.5, 0, 0)
+    assert bool(((out[rows].cpu().double() - y).abs() <= tol).all())
+    q4k.q4k_pages_free(cache, ints(range(2 * n)))
+    assert int(cache.refs.abs().sum()) == 0 and int(cache.lens.sum()) == 0
+
+
 def test_pages_copy(q4k):
     cache = make_cache(q4k, [100], 16, 3, 64, layers=4, spare=20)
     k0, v0 = cache.k.clone(), cache.v.clone()
