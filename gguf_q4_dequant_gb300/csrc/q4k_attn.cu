@@ -48,10 +48,11 @@ template <int D>
 struct ChunkCfg {
     static constexpr int kHalves = D / 64;                 // 64-element column blocks of a row
     static constexpr int kTileBytes = kChunkKeys * D * 2;  // one K or V tile, one half of Q
-    static constexpr int kRing = D == 128 ? 5 : 8;
+    static constexpr int kRing = D == 128 ? 4 : 8;
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = 2 * kTileBytes;
-    static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
+    static constexpr int kOffStage = kOffRing + kRing * kTileBytes;  // output rows, 4 KB per softmax warp
+    static constexpr int kOffBar = kOffStage + 8 * 4096;
     // full[kRing] empty[kRing] qfull qempty sfull[2] pfull[2] ofull[2] wg[2] fin ifull[kItemRing] iempty[kItemRing]
     // vclean[kRing]
     static constexpr int kNumBars = 3 * kRing + 11 + 2 * kItemRing;
@@ -479,8 +480,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_fence_after();
             const bool fix = poison[n_items & 3] == n_items;
             const bool whole = it.i0 == 0 && it.i1 == it.keys.n;
-            // the non-finite values that were zeroed, back into 32 columns of the rows that see them
-            auto add_back = [&](float (&o)[32], int c0) {
+            // the non-finite values that were zeroed, back into 64 columns of the rows that see them
+            auto add_back = [&](float (&o)[64], int c0) {
                 for (int j = 0; j < n; ++j) {
                     const int tile = it.keys.tile(it.i0 + j);
                     if (tile_is_full<KT>(tile, it.p0, it.p0 + it.tokens - 1, p.window, p.sinks)) continue;
@@ -493,40 +494,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                             ((static_cast<int64_t>(it.h) << p.c.page_shift) +
                                              (key & ((1 << p.c.page_shift) - 1))) * D + c0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 64; ++e) {
                             const float x = __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
                             if (!isfinite(x)) o[e] += x;
                         }
                     }
                 }
             };
-            auto store = [&](const float (&o)[32], int c0, float inv) {
-                if (tok >= mine || r >= tph * p.group) return;
-                uint16_t* dst = p.out + (static_cast<int64_t>(it.t_first + hf * tph + tok) * p.heads +
-                                         it.h * p.group + g) * D + c0;
+            auto accumulators = [&](float (&o)[64], int c0) {
+                uint32_t ov[2][32];
+                tmem_ld_32x32b_x32(t_o + c0, ov[0]);
+                tmem_ld_32x32b_x32(t_o + c0 + 32, ov[1]);
+                tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < 64; ++e) o[e] = __uint_as_float(ov[e >> 5][e & 31]);
+                if (fix) add_back(o, c0);
+            };
+            // 64 columns of the warp's 32 rows: turned in shared memory (16-byte
+            // chunk index XOR row % 8), so that eight lanes write a row's 128 bytes
+            const int out_row = tok < mine && r < tph * p.group
+                                    ? (it.t_first + hf * tph + tok) * p.heads + it.h * p.group + g : -1;
+            uint8_t* stage = smem + Cfg::kOffStage + warp * 4096;
+            auto store = [&](const float (&o)[64], int c0, float inv) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
                     uint32_t y[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 q = __floats2bfloat162_rn(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
+                        const __nv_bfloat162 q = __floats2bfloat162_rn(o[8 * c + 2 * i] * inv, o[8 * c + 2 * i + 1] * inv);
                         y[i] = *reinterpret_cast<const uint32_t*>(&q);
                     }
-                    *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = 4 * k + (lane >> 3), to = __shfl_sync(0xffffffffu, out_row, row);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                    if (to >= 0) *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * D + c0 + 8 * (lane & 7)) = v;
+                }
+                __syncwarp();
             };
             if (whole) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t ov[32];
-                    float o[32];
-                    tmem_ld_32x32b_x32(t_o + 32 * c, ov);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
-                    if (fix) add_back(o, 32 * c);
-                    store(o, 32 * c, inv);
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    float o[64];
+                    accumulators(o, c0);
+                    store(o, c0, inv);
                 }
                 continue;
             }
@@ -538,16 +553,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             };
             float* out_part = part(blockIdx.x);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t ov[32];
-                float o[32];
-                tmem_ld_32x32b_x32(t_o + 32 * c, ov);
-                tmem_ld_wait();
+            for (int c0 = 0; c0 < D; c0 += 64) {
+                float o[64];
+                accumulators(o, c0);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
-                if (fix) add_back(o, 32 * c);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) __stcg(out_part + (32 * c + e) * 128 + r, o[e]);
+                for (int e = 0; e < 64; ++e) __stcg(out_part + (c0 + e) * 128 + r, o[e]);
             }
             __stcg(out_part + D * 128 + r, ref);
             __stcg(out_part + (D + 1) * 128 + r, sum);
@@ -568,29 +578,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             if (!(ok = wg_sync())) break;
             if (!last_s[hf]) continue;
+            // two parts' loads at a time (two parts are what there mostly are)
             float top = -INFINITY;
-            for (int cta = first; cta <= last; ++cta) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
+            for (int cta = first; cta <= last; cta += 2) {
+                const float a0 = __ldcg(part(cta) + D * 128 + r), a1 = __ldcg(part(min(cta + 1, last)) + D * 128 + r);
+                top = fmaxf(top, fmaxf(a0, a1));
+            }
             const float zero_ref = top == -INFINITY ? 0.f : top;
             float all = 0.f;
-            for (int cta = first; cta <= last; ++cta)
-                all += __ldcg(part(cta) + (D + 1) * 128 + r) * ex2(__ldcg(part(cta) + D * 128 + r) - zero_ref);
-            const float inv = all == 0.f ? 0.f : 1.f / all;
+            constexpr int kCols = 32;
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {  // 64 columns' loads at a time
-                float o[2][32];
+            for (int c0 = 0; c0 < D; c0 += 64) {
+                float o[64];
+                all = 0.f;
 #pragma unroll
-                for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = 0.f;
-                for (int cta = first; cta <= last; ++cta) {
-                    const float* from = part(cta);
-                    float x[64];
+                for (int e = 0; e < 64; ++e) o[e] = 0.f;
+                for (int cta = first; cta <= last; cta += 2) {
+                    const bool pair = cta < last;
+                    const float *f0 = part(cta), *f1 = part(pair ? cta + 1 : cta);
+                    const float w0 = ex2(__ldcg(f0 + D * 128 + r) - zero_ref);
+                    const float w1 = pair ? ex2(__ldcg(f1 + D * 128 + r) - zero_ref) : 0.f;
+                    const float s0 = __ldcg(f0 + (D + 1) * 128 + r), s1 = __ldcg(f1 + (D + 1) * 128 + r);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) x[e] = __ldcg(from + (64 * c + e) * 128 + r);
-                    const float f = ex2(__ldcg(from + D * 128 + r) - zero_ref);
+                    for (int c = 0; c < 64; c += kCols) {
+                        float x0[kCols], x1[kCols];
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = fmaf(x[e], f, o[e >> 5][e & 31]);
+                        for (int e = 0; e < kCols; ++e) x0[e] = __ldcg(f0 + (c0 + c + e) * 128 + r);
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e) x1[e] = pair ? __ldcg(f1 + (c0 + c + e) * 128 + r) : 0.f;
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e) o[c + e] = fmaf(x1[e], w1, fmaf(x0[e], w0, o[c + e]));
+                    }
+                    all = fmaf(s0, w0, all);
+                    if (pair) all = fmaf(s1, w1, all);
                 }
-                store(o[0], 64 * c, inv);
-                store(o[1], 64 * c + 32, inv);
+                store(o, c0, all == 0.f ? 0.f : 1.f / all);
             }
         }
     }

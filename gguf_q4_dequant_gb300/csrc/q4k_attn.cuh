@@ -149,7 +149,7 @@ __device__ __forceinline__ AttnCut find_cut(const AttnParams& p, int tt, const u
     AttnCut c;
     c.b = c.h = c.tile = c.off = 0;
     uint32_t at = 0;
-    for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+    for (int i0 = 0; p.b.n > 1 && i0 < p.b.n; i0 += 32) {
         const uint32_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0;
         uint32_t incl = mine;
 #pragma unroll
@@ -212,29 +212,40 @@ template <int KT>
 __device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int q_min, int snap, uint32_t* units,
                                            AttnWalk* found) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
-        const int i = i0 + lane;
-        SeqView s{0, 0, 0, 0};
-        if (i < p.b.n) s = seq_view(p.c, p.b, i);
-        const int tiles = (s.m + tt - 1) / tt;
-        uint32_t u = 0;
-        if (tiles <= 4)
-            for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
-        // many row tiles: the warp counts them together
-        uint32_t many = __ballot_sync(0xffffffffu, tiles > 4);
-        while (many) {
-            const int l = __ffs(many) - 1;
-            many &= many - 1;
-            SeqView o;
-            o.m = __shfl_sync(0xffffffffu, s.m, l);
-            o.len = __shfl_sync(0xffffffffu, s.len, l);
-            const int ot = (o.m + tt - 1) / tt;
-            uint32_t x = 0;
-            for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
-            x = __reduce_add_sync(0xffffffffu, x);
-            if (lane == l) u = x;
+    if (p.b.n <= 2 * nwarps) {  // few sequences: a warp each, its lanes over the row tiles
+        for (int i = warp; i < p.b.n; i += nwarps) {
+            const SeqView s = seq_view(p.c, p.b, i);
+            const int tiles = (s.m + tt - 1) / tt;
+            uint32_t u = 0;
+            for (int t = lane; t < tiles; t += 32) u += tile_units<KT>(p, s, t, tt);
+            u = __reduce_add_sync(0xffffffffu, u);
+            if (lane == 0) units[i] = u * p.c.kv_heads;
         }
-        if (i < p.b.n) units[i] = u * p.c.kv_heads;
+    } else {  // a thread each
+        for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
+            const int i = i0 + lane;
+            SeqView s{0, 0, 0, 0};
+            if (i < p.b.n) s = seq_view(p.c, p.b, i);
+            const int tiles = (s.m + tt - 1) / tt;
+            uint32_t u = 0;
+            if (tiles <= 4)
+                for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
+            // many row tiles: the warp counts them together
+            uint32_t many = __ballot_sync(0xffffffffu, tiles > 4);
+            while (many) {
+                const int l = __ffs(many) - 1;
+                many &= many - 1;
+                SeqView o;
+                o.m = __shfl_sync(0xffffffffu, s.m, l);
+                o.len = __shfl_sync(0xffffffffu, s.len, l);
+                const int ot = (o.m + tt - 1) / tt;
+                uint32_t x = 0;
+                for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
+                x = __reduce_add_sync(0xffffffffu, x);
+                if (lane == l) u = x;
+            }
+            if (i < p.b.n) units[i] = u * p.c.kv_heads;
+        }
     }
     __syncthreads();
     // warp 0 finds where the range begins, warp 1 where it ends
