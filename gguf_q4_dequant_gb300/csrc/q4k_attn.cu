@@ -424,12 +424,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             if (!(seen >> e & 1u)) sv[c][e] = 0xFF800000u;
                     }
                 }
-                float mx = -INFINITY;
+                float part_max[4];  // four chains: one would be 64 steps long
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    part_max[c] = __uint_as_float(sv[c][0]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sv[c][e]));
-                mx *= p.scale_log2;
+                    for (int e = 1; e < 32; ++e) part_max[c] = fmaxf(part_max[c], __uint_as_float(sv[c][e]));
+                }
+                const float mx = fmaxf(fmaxf(part_max[0], part_max[1]), fmaxf(part_max[2], part_max[3])) * p.scale_log2;
                 const bool grow = mx > ref + 8.f || (ref == -INFINITY && mx > ref);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2(ref - mx) : 1.f;
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                 }
                 const float base = ref == -INFINITY ? 0.f : ref;
-                uint64_t acc = pack2(0.f, 0.f);
+                uint64_t acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
                 const uint64_t k2 = pack2(p.scale_log2, p.scale_log2), b2 = pack2(-base, -base);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         const float2 x = unpack2(fma2(
                             pack2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])), k2, b2));
                         const float a0 = ex2(x.x), a1 = ex2(x.y);
-                        acc = add2(acc, pack2(a0, a1));
+                        acc[e & 1] = add2(acc[e & 1], pack2(a0, a1));
                         const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);
                         pw[e] = *reinterpret_cast<const uint32_t*>(&pr);
                     }
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(b_pfull + 8 * hf);
-                const float2 a = unpack2(acc);
+                const float2 a = unpack2(add2(acc[0], acc[1]));
                 sum += a.x + a.y;
             }
             if (!ok) break;
@@ -578,39 +580,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             if (!(ok = wg_sync())) break;
             if (!last_s[hf]) continue;
-            // two parts' loads at a time (two parts are what there mostly are)
-            float top = -INFINITY;
-            for (int cta = first; cta <= last; cta += 2) {
-                const float a0 = __ldcg(part(cta) + D * 128 + r), a1 = __ldcg(part(min(cta + 1, last)) + D * 128 + r);
-                top = fmaxf(top, fmaxf(a0, a1));
-            }
-            const float zero_ref = top == -INFINITY ? 0.f : top;
-            float all = 0.f;
-            constexpr int kCols = 32;
+            // the first two parts' loads together (two are what there mostly are)
+            const float *f0 = part(first), *f1 = part(first + 1);
+            const float r0 = __ldcg(f0 + D * 128 + r), r1 = __ldcg(f1 + D * 128 + r);
+            const float s0 = __ldcg(f0 + (D + 1) * 128 + r), s1 = __ldcg(f1 + (D + 1) * 128 + r);
+            float top = fmaxf(r0, r1);
+            for (int cta = first + 2; cta <= last; ++cta) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
+            const float base = top == -INFINITY ? 0.f : top;
+            const float w0 = ex2(r0 - base), w1 = ex2(r1 - base);
+            float all = s0 * w0 + s1 * w1;
+            for (int cta = first + 2; cta <= last; ++cta)
+                all = fmaf(__ldcg(part(cta) + (D + 1) * 128 + r), ex2(__ldcg(part(cta) + D * 128 + r) - base), all);
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {
-                float o[64];
-                all = 0.f;
+                float o[64], x[64];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) o[e] = 0.f;
-                for (int cta = first; cta <= last; cta += 2) {
-                    const bool pair = cta < last;
-                    const float *f0 = part(cta), *f1 = part(pair ? cta + 1 : cta);
-                    const float w0 = ex2(__ldcg(f0 + D * 128 + r) - zero_ref);
-                    const float w1 = pair ? ex2(__ldcg(f1 + D * 128 + r) - zero_ref) : 0.f;
-                    const float s0 = __ldcg(f0 + (D + 1) * 128 + r), s1 = __ldcg(f1 + (D + 1) * 128 + r);
+                for (int e = 0; e < 64; ++e) o[e] = __ldcg(f0 + (c0 + e) * 128 + r);
 #pragma unroll
-                    for (int c = 0; c < 64; c += kCols) {
-                        float x0[kCols], x1[kCols];
+                for (int e = 0; e < 64; ++e) x[e] = __ldcg(f1 + (c0 + e) * 128 + r);
 #pragma unroll
-                        for (int e = 0; e < kCols; ++e) x0[e] = __ldcg(f0 + (c0 + c + e) * 128 + r);
+                for (int e = 0; e < 64; ++e) o[e] = fmaf(x[e], w1, o[e] * w0);
+                for (int cta = first + 2; cta <= last; ++cta) {
+                    const float* from = part(cta);
 #pragma unroll
-                        for (int e = 0; e < kCols; ++e) x1[e] = pair ? __ldcg(f1 + (c0 + c + e) * 128 + r) : 0.f;
+                    for (int e = 0; e < 64; ++e) x[e] = __ldcg(from + (c0 + e) * 128 + r);
+                    const float w = ex2(__ldcg(from + D * 128 + r) - base);
 #pragma unroll
-                        for (int e = 0; e < kCols; ++e) o[c + e] = fmaf(x1[e], w1, fmaf(x0[e], w0, o[c + e]));
-                    }
-                    all = fmaf(s0, w0, all);
-                    if (pair) all = fmaf(s1, w1, all);
+                    for (int e = 0; e < 64; ++e) o[e] = fmaf(x[e], w, o[e]);
                 }
                 store(o, c0, all == 0.f ? 0.f : 1.f / all);
             }
