@@ -37,12 +37,11 @@ namespace q4k {
 constexpr int kChunkKeys = 128;
 constexpr int kChunkThreads = 384;
 constexpr int kScanWarps = 2;
-#ifndef Q4K_CHUNK_SNAP
-#define Q4K_CHUNK_SNAP 2
-#endif
-#define Q4K_REGS_DEC 88
+// Registers: the block starts with 168 a thread; the last warpgroup gives some to the softmax.
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "registers");
 constexpr int kChunkMinUnits = 1;
-constexpr int kChunkSnap = Q4K_CHUNK_SNAP;
+constexpr int kChunkSnap = 2;
 
 template <int D>
 struct ChunkCfg {
@@ -140,9 +139,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     pdl_wait();
     const int tph = 128 / p.group, tt = 2 * tph;  // tokens per half and per item
-    plan_units<KT>(p, tt, kChunkMinUnits, kChunkSnap, reinterpret_cast<uint32_t*>(smem + Cfg::kOffRing), walk_s);
-    // the plan's scratch (generic accesses) becomes the ring (TMA writes)
-    fence_proxy_async_smem();
+    if (p.b.n > 32) {
+        plan_block<KT>(p, tt, kChunkMinUnits, kChunkSnap, reinterpret_cast<uint32_t*>(smem + Cfg::kOffRing), walk_s);
+        fence_proxy_async_smem();  // the plan's scratch (generic accesses) becomes the ring (TMA writes)
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -150,10 +150,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (threadIdx.x == 0) pdl_launch_dependents();
 
     if (warp >= 8) {
-        regs_dec<Q4K_REGS_DEC>();
+        regs_dec<kOtherRegs>();
         if (warp == 8) {
             // ------------------------------------------------ TMA producer ---
-            AttnWalk w = *walk_s;
+            AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kChunkMinUnits, kChunkSnap);
             AttnItem it{};
             PageIds ids;
             int slot = 0, n_items = 0, issued = 0;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax ---
-        regs_inc<(504 - Q4K_REGS_DEC) / 2 / 8 * 8>();
+        regs_inc<kSoftRegs>();
         const int hf = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lane_base + Cfg::kColS + hf * 128;

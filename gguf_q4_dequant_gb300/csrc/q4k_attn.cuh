@@ -141,46 +141,35 @@ struct AttnCut {
     SeqView s;
 };
 
-// Found by one warp: the row tile that holds unit u < total, from the units of
-// the sequences.
+// Inclusive sum over the lanes of a warp.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, x, k);
+        if (lane >= k) x += v;
+    }
+    return x;
+}
+
+// By one warp: where unit u of the step lies in sequence b, which has per_head
+// units per kv head from unit `at` on.
 template <int KT>
-__device__ __forceinline__ AttnCut find_cut(const AttnParams& p, int tt, const uint32_t* units, uint32_t u, int snap) {
+__device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, const SeqView& s, uint32_t per_head,
+                                          uint32_t at, uint32_t u, int snap) {
     const int lane = threadIdx.x & 31;
     AttnCut c;
-    c.b = c.h = c.tile = c.off = 0;
-    uint32_t at = 0;
-    for (int i0 = 0; p.b.n > 1 && i0 < p.b.n; i0 += 32) {
-        const uint32_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0;
-        uint32_t incl = mine;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, k);
-            if (lane >= k) incl += v;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, at + incl > u);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            c.b = i0 + l;
-            at += __shfl_sync(0xffffffffu, incl - mine, l);
-            break;
-        }
-        at += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    c.s = seq_view(p.c, p.b, c.b);
-    const uint32_t per_head = units[c.b] / p.c.kv_heads;
+    c.b = b;
+    c.s = s;
+    c.tile = 0;
     c.h = static_cast<int>((u - at) / per_head);
     uint32_t rest = (u - at) - c.h * per_head;
     int n = per_head;
-    if (c.s.m > tt) {
-        for (int t0 = 0; t0 < (c.s.m + tt - 1) / tt; t0 += 32) {
+    if (s.m > tt) {
+        for (int t0 = 0; t0 < (s.m + tt - 1) / tt; t0 += 32) {
             const int t = t0 + lane;
-            const uint32_t mine = static_cast<int64_t>(t) * tt < c.s.m ? tile_units<KT>(p, c.s, t, tt) : 0;
-            uint32_t incl = mine;
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, k);
-                if (lane >= k) incl += v;
-            }
+            const uint32_t mine = static_cast<int64_t>(t) * tt < s.m ? tile_units<KT>(p, s, t, tt) : 0;
+            const uint32_t incl = warp_scan(mine);
             const uint32_t past = __ballot_sync(0xffffffffu, incl > rest);
             if (past) {
                 const int l = __ffs(past) - 1;
@@ -205,47 +194,81 @@ __device__ __forceinline__ AttnCut find_cut(const AttnParams& p, int tt, const u
     return c;
 }
 
-// The CTA's range, found by all threads of the block: `units` holds n words of
-// shared memory, `found` takes the result. Ends with __syncthreads(). `q_min`:
-// units that a range has at least.
+// By one warp: units per kv head of the lanes' sequences.
 template <int KT>
-__device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int q_min, int snap, uint32_t* units,
+__device__ __forceinline__ uint32_t lane_units(const AttnParams& p, int tt, const SeqView& s) {
+    const int lane = threadIdx.x & 31, tiles = (s.m + tt - 1) / tt;
+    uint32_t u = 0;
+    if (tiles <= 4)
+        for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
+    // many row tiles: the warp counts them together
+    uint32_t many = __ballot_sync(0xffffffffu, tiles > 4);
+    while (many) {
+        const int l = __ffs(many) - 1;
+        many &= many - 1;
+        SeqView o;
+        o.m = __shfl_sync(0xffffffffu, s.m, l);
+        o.len = __shfl_sync(0xffffffffu, s.len, l);
+        const int ot = (o.m + tt - 1) / tt;
+        uint32_t x = 0;
+        for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
+        x = __reduce_add_sync(0xffffffffu, x);
+        if (lane == l) u = x;
+    }
+    return u;
+}
+
+// The CTA's range by one warp, for at most 32 sequences. `q_min`: units that a
+// range has at least.
+template <int KT>
+__device__ __forceinline__ AttnWalk plan_warp(const AttnParams& p, int tt, int q_min, int snap) {
+    const int lane = threadIdx.x & 31;
+    SeqView s{0, 0, 0, 0};
+    if (lane < p.b.n) s = seq_view(p.c, p.b, lane);
+    const uint32_t per_head = lane_units<KT>(p, tt, s), mine = per_head * p.c.kv_heads;
+    const uint32_t incl = p.b.n > 1 ? warp_scan(mine) : __shfl_sync(0xffffffffu, mine, 0);
+    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
+    AttnWalk w;
+    w.q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(q_min));
+    w.u = w.u_end = total;
+    w.b = w.h = w.tile = w.off = 0;
+    w.s = SeqView{0, 0, 0, 0};
+    auto cut = [&](uint32_t u) {
+        const int l = __ffs(__ballot_sync(0xffffffffu, incl > u)) - 1;
+        SeqView o;
+        o.t0 = __shfl_sync(0xffffffffu, s.t0, l);
+        o.m = __shfl_sync(0xffffffffu, s.m, l);
+        o.len = __shfl_sync(0xffffffffu, s.len, l);
+        o.row = __shfl_sync(0xffffffffu, s.row, l);
+        return cut_in<KT>(p, tt, l, o, __shfl_sync(0xffffffffu, per_head, l), __shfl_sync(0xffffffffu, incl - mine, l), u, snap);
+    };
+    const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * w.q, u1 = u0 + w.q;
+    if (u0 < total) {
+        const AttnCut c = cut(static_cast<uint32_t>(u0));
+        w.u = c.u;
+        w.b = c.b;
+        w.h = c.h;
+        w.tile = c.tile;
+        w.off = c.off;
+        w.s = c.s;
+        if (u1 < total) w.u_end = cut(static_cast<uint32_t>(u1)).u;
+    }
+    return w;
+}
+
+// The same by all threads of the block, for any number of sequences: `units`
+// holds n words of shared memory, `found` takes the result. Ends with
+// __syncthreads().
+template <int KT>
+__device__ __forceinline__ void plan_block(const AttnParams& p, int tt, int q_min, int snap, uint32_t* units,
                                            AttnWalk* found) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    if (p.b.n <= 2 * nwarps) {  // few sequences: a warp each, its lanes over the row tiles
-        for (int i = warp; i < p.b.n; i += nwarps) {
-            const SeqView s = seq_view(p.c, p.b, i);
-            const int tiles = (s.m + tt - 1) / tt;
-            uint32_t u = 0;
-            for (int t = lane; t < tiles; t += 32) u += tile_units<KT>(p, s, t, tt);
-            u = __reduce_add_sync(0xffffffffu, u);
-            if (lane == 0) units[i] = u * p.c.kv_heads;
-        }
-    } else {  // a thread each
-        for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
-            const int i = i0 + lane;
-            SeqView s{0, 0, 0, 0};
-            if (i < p.b.n) s = seq_view(p.c, p.b, i);
-            const int tiles = (s.m + tt - 1) / tt;
-            uint32_t u = 0;
-            if (tiles <= 4)
-                for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
-            // many row tiles: the warp counts them together
-            uint32_t many = __ballot_sync(0xffffffffu, tiles > 4);
-            while (many) {
-                const int l = __ffs(many) - 1;
-                many &= many - 1;
-                SeqView o;
-                o.m = __shfl_sync(0xffffffffu, s.m, l);
-                o.len = __shfl_sync(0xffffffffu, s.len, l);
-                const int ot = (o.m + tt - 1) / tt;
-                uint32_t x = 0;
-                for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
-                x = __reduce_add_sync(0xffffffffu, x);
-                if (lane == l) u = x;
-            }
-            if (i < p.b.n) units[i] = u * p.c.kv_heads;
-        }
+    for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
+        const int i = i0 + lane;
+        SeqView s{0, 0, 0, 0};
+        if (i < p.b.n) s = seq_view(p.c, p.b, i);
+        const uint32_t u = lane_units<KT>(p, tt, s);
+        if (i < p.b.n) units[i] = u * p.c.kv_heads;
     }
     __syncthreads();
     // warp 0 finds where the range begins, warp 1 where it ends
@@ -254,12 +277,28 @@ __device__ __forceinline__ void plan_units(const AttnParams& p, int tt, int q_mi
         for (int i = lane; i < p.b.n; i += 32) total += units[i];
         total = __reduce_add_sync(0xffffffffu, total);
         const uint32_t q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(q_min));
-        const uint64_t u = static_cast<uint64_t>(blockIdx.x + warp) * q;
+        const uint64_t u64 = static_cast<uint64_t>(blockIdx.x + warp) * q;
         AttnCut c;
         c.u = total;
         c.b = c.h = c.tile = c.off = 0;
         c.s = SeqView{0, 0, 0, 0};
-        if (u < total) c = find_cut<KT>(p, tt, units, static_cast<uint32_t>(u), snap);
+        if (u64 < total) {
+            const uint32_t u = static_cast<uint32_t>(u64);
+            uint32_t at = 0;
+            int b = 0;
+            for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+                const uint32_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0, incl = warp_scan(mine);
+                const uint32_t past = __ballot_sync(0xffffffffu, at + incl > u);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    b = i0 + l;
+                    at += __shfl_sync(0xffffffffu, incl - mine, l);
+                    break;
+                }
+                at += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            c = cut_in<KT>(p, tt, b, seq_view(p.c, p.b, b), units[b] / p.c.kv_heads, at, u, snap);
+        }
         if (lane == 0) {
             if (warp == 0) {
                 found->u = c.u;

@@ -23,14 +23,8 @@ namespace q4k {
 constexpr int kDecKeys = 128;
 constexpr int kDecWarps = 8;                    // consumers; one more warp produces
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
-#ifndef Q4K_DEC_SNAP
-#define Q4K_DEC_SNAP 4
-#endif
-#ifndef Q4K_DEC_MIN
-#define Q4K_DEC_MIN 4
-#endif
-constexpr int kDecMinUnits = Q4K_DEC_MIN;
-constexpr int kDecSnap = Q4K_DEC_SNAP;
+constexpr int kDecMinUnits = 4;
+constexpr int kDecSnap = 4;
 
 template <int D>
 struct DecodeCfg {
@@ -115,15 +109,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     pdl_wait();
     const int tt = 8 * NB / p.group;  // tokens of a row tile
-    plan_units<KT>(p, tt, kDecMinUnits, kDecSnap, reinterpret_cast<uint32_t*>(smem), walk_s);
-    fence_proxy_async_smem();  // the plan's scratch becomes the ring
+    if (p.b.n > 32) {
+        plan_block<KT>(p, tt, kDecMinUnits, kDecSnap, reinterpret_cast<uint32_t*>(smem), walk_s);
+        fence_proxy_async_smem();  // the plan's scratch becomes the ring
+    }
     __syncthreads();
     if (threadIdx.x == 0) pdl_launch_dependents();
     const int page = 1 << p.c.page_shift;
 
     if (warp == kDecWarps) {
         // ---------------------------------------------------- TMA producer ---
-        AttnWalk w = *walk_s;
+        AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kDecMinUnits, kDecSnap);
         AttnItem it{};
         PageIds ids;
         int slot = 0, issued = 0;
