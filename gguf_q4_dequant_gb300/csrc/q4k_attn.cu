@@ -40,8 +40,7 @@ constexpr int kScanWarps = 2;
 // Registers: the block starts with 168 a thread; the last warpgroup gives some to the softmax.
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "registers");
-constexpr int kChunkMinUnits = 1;
-constexpr int kChunkSnap = 2;
+constexpr AttnCost kChunkCost{2, 1, 1};  // item, snap, q_min
 
 template <int D>
 struct ChunkCfg {
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     pdl_wait();
     const int tph = 128 / p.group, tt = 2 * tph;  // tokens per half and per item
     if (p.b.n > 32) {
-        plan_block<KT>(p, tt, kChunkMinUnits, kChunkSnap, reinterpret_cast<uint32_t*>(smem + Cfg::kOffRing), walk_s);
+        plan_block<KT>(p, tt, kChunkCost, reinterpret_cast<uint32_t*>(smem + Cfg::kOffRing), walk_s);
         fence_proxy_async_smem();  // the plan's scratch (generic accesses) becomes the ring (TMA writes)
     }
     tc_fence_before();
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         regs_dec<kOtherRegs>();
         if (warp == 8) {
             // ------------------------------------------------ TMA producer ---
-            AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kChunkMinUnits, kChunkSnap);
+            AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kChunkCost);
             AttnItem it{};
             PageIds ids;
             int slot = 0, n_items = 0, issued = 0;
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 return true;
             };
             for (;;) {
-                const bool more = next_item<KT>(p, w, tt, kChunkSnap, it);
+                const bool more = next_item<KT>(p, w, tt, kChunkCost, it);
                 const int k = n_items % kItemRing;
                 ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
                 if (!ok) break;

@@ -64,6 +64,16 @@ __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
     return j <= p && (window == 0 || j > p - window || j < sinks);
 }
 
+// How a range's units are counted: a row tile counts as `item` units more than
+// it has key tiles (its start and its end take about that long), and a range's
+// end that falls into a row tile within `snap` key tiles of one of its ends
+// moves there, since putting two parts together costs about as much. So
+// boundary c, at first c * q, lies inside a row tile of units [a, b) only if
+// a + item + snap < c * q < b - snap. A range has q_min units at least.
+struct AttnCost {
+    int item, snap, q_min;
+};
+
 // What one CTA does, item by item.
 struct AttnItem {
     int t_first, tokens;  // rows of the step's arrays
@@ -93,7 +103,7 @@ struct AttnWalk {
 
 // The next item, or false. `tt`: tokens of a row tile.
 template <int KT>
-__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, int snap, AttnItem& it) {
+__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, AttnCost cost, AttnItem& it) {
     it.i0 = it.i1 = 0;
     if (w.u >= w.u_end) return false;
     while (w.tile * tt >= w.s.m) {  // the sequence's row tiles are done for this head
@@ -110,31 +120,27 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int 
     it.row = w.s.row;
     it.len = w.s.len;
     it.keys = key_tiles<KT>(it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
-    it.i0 = w.off;
-    it.i1 = static_cast<int>(min(static_cast<uint32_t>(it.keys.n), it.i0 + (w.u_end - w.u)));
+    const uint32_t u0 = w.u - w.off, u1 = u0 + cost.item + it.keys.n;  // the row tile's units
+    it.i0 = w.off > 0 ? w.off - cost.item : 0;
+    it.i1 = w.u_end < u1 ? static_cast<int>(w.u_end - u0) - cost.item : it.keys.n;
     it.first = it.last = blockIdx.x;
     if (it.i0 > 0 || it.i1 < it.keys.n) {
-        const uint32_t u0 = w.u - it.i0, u1 = u0 + it.keys.n;  // the row tile's units
-        it.first = static_cast<int>((u0 + snap) / w.q);        // one before the first boundary inside
-        it.last = static_cast<int>((u1 - snap - 1) / w.q);     // the last boundary inside
+        it.first = static_cast<int>((u0 + cost.item + cost.snap) / w.q);  // one before the first boundary inside
+        it.last = static_cast<int>((u1 - cost.snap - 1) / w.q);           // the last boundary inside
     }
-    w.u += it.i1 - it.i0;
+    w.u = min(u1, w.u_end);
     w.off = 0;
     ++w.tile;
     return true;
 }
 
-// Units of the row tiles of one sequence and kv head.
+// Units of a row tile of a sequence.
 template <int KT>
-__device__ __forceinline__ int tile_units(const AttnParams& p, const SeqView& s, int tile, int tt) {
+__device__ __forceinline__ int tile_units(const AttnParams& p, const SeqView& s, int tile, int tt, AttnCost cost) {
     const int p0 = s.len - s.m + tile * tt;
-    return key_tiles<KT>(p0, p0 + min(tt, s.m - tile * tt) - 1, p.window, p.sinks).n;
+    return cost.item + key_tiles<KT>(p0, p0 + min(tt, s.m - tile * tt) - 1, p.window, p.sinks).n;
 }
 
-// A row tile that a range's end falls into near one of its own ends is not cut
-// there: the end moves by up to `snap` key tiles, since putting two parts
-// together costs about as much time. So boundary c, at first c * q, lies inside
-// a row tile of units [a, b) only if a + snap < c * q < b - snap.
 struct AttnCut {
     uint32_t u;        // the boundary, moved
     int b, h, tile, off;  // where it lies (off > 0: inside the row tile)
@@ -156,7 +162,7 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
 // units per kv head from unit `at` on.
 template <int KT>
 __device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, const SeqView& s, uint32_t per_head,
-                                          uint32_t at, uint32_t u, int snap) {
+                                          uint32_t at, uint32_t u, AttnCost cost) {
     const int lane = threadIdx.x & 31;
     AttnCut c;
     c.b = b;
@@ -168,7 +174,7 @@ __device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, co
     if (s.m > tt) {
         for (int t0 = 0; t0 < (s.m + tt - 1) / tt; t0 += 32) {
             const int t = t0 + lane;
-            const uint32_t mine = static_cast<int64_t>(t) * tt < s.m ? tile_units<KT>(p, s, t, tt) : 0;
+            const uint32_t mine = static_cast<int64_t>(t) * tt < s.m ? tile_units<KT>(p, s, t, tt, cost) : 0;
             const uint32_t incl = warp_scan(mine);
             const uint32_t past = __ballot_sync(0xffffffffu, incl > rest);
             if (past) {
@@ -183,10 +189,10 @@ __device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, co
     }
     c.u = u;
     c.off = static_cast<int>(rest);
-    if (c.off <= snap) {
+    if (c.off <= cost.item + cost.snap) {
         c.u -= c.off;
         c.off = 0;
-    } else if (n - c.off <= snap) {
+    } else if (n - c.off <= cost.snap) {
         c.u += n - c.off;
         c.off = 0;
         ++c.tile;  // (one past the last: the walk goes on to the next head or sequence)
@@ -196,11 +202,11 @@ __device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, co
 
 // By one warp: units per kv head of the lanes' sequences.
 template <int KT>
-__device__ __forceinline__ uint32_t lane_units(const AttnParams& p, int tt, const SeqView& s) {
+__device__ __forceinline__ uint32_t lane_units(const AttnParams& p, int tt, const SeqView& s, AttnCost cost) {
     const int lane = threadIdx.x & 31, tiles = (s.m + tt - 1) / tt;
     uint32_t u = 0;
     if (tiles <= 4)
-        for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt);
+        for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt, cost);
     // many row tiles: the warp counts them together
     uint32_t many = __ballot_sync(0xffffffffu, tiles > 4);
     while (many) {
@@ -211,25 +217,24 @@ __device__ __forceinline__ uint32_t lane_units(const AttnParams& p, int tt, cons
         o.len = __shfl_sync(0xffffffffu, s.len, l);
         const int ot = (o.m + tt - 1) / tt;
         uint32_t x = 0;
-        for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt);
+        for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt, cost);
         x = __reduce_add_sync(0xffffffffu, x);
         if (lane == l) u = x;
     }
     return u;
 }
 
-// The CTA's range by one warp, for at most 32 sequences. `q_min`: units that a
-// range has at least.
+// The CTA's range by one warp, for at most 32 sequences.
 template <int KT>
-__device__ __forceinline__ AttnWalk plan_warp(const AttnParams& p, int tt, int q_min, int snap) {
+__device__ __forceinline__ AttnWalk plan_warp(const AttnParams& p, int tt, AttnCost cost) {
     const int lane = threadIdx.x & 31;
     SeqView s{0, 0, 0, 0};
     if (lane < p.b.n) s = seq_view(p.c, p.b, lane);
-    const uint32_t per_head = lane_units<KT>(p, tt, s), mine = per_head * p.c.kv_heads;
+    const uint32_t per_head = lane_units<KT>(p, tt, s, cost), mine = per_head * p.c.kv_heads;
     const uint32_t incl = p.b.n > 1 ? warp_scan(mine) : __shfl_sync(0xffffffffu, mine, 0);
     const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
     AttnWalk w;
-    w.q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(q_min));
+    w.q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(cost.q_min));
     w.u = w.u_end = total;
     w.b = w.h = w.tile = w.off = 0;
     w.s = SeqView{0, 0, 0, 0};
@@ -240,7 +245,7 @@ __device__ __forceinline__ AttnWalk plan_warp(const AttnParams& p, int tt, int q
         o.m = __shfl_sync(0xffffffffu, s.m, l);
         o.len = __shfl_sync(0xffffffffu, s.len, l);
         o.row = __shfl_sync(0xffffffffu, s.row, l);
-        return cut_in<KT>(p, tt, l, o, __shfl_sync(0xffffffffu, per_head, l), __shfl_sync(0xffffffffu, incl - mine, l), u, snap);
+        return cut_in<KT>(p, tt, l, o, __shfl_sync(0xffffffffu, per_head, l), __shfl_sync(0xffffffffu, incl - mine, l), u, cost);
     };
     const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * w.q, u1 = u0 + w.q;
     if (u0 < total) {
@@ -260,14 +265,14 @@ __device__ __forceinline__ AttnWalk plan_warp(const AttnParams& p, int tt, int q
 // holds n words of shared memory, `found` takes the result. Ends with
 // __syncthreads().
 template <int KT>
-__device__ __forceinline__ void plan_block(const AttnParams& p, int tt, int q_min, int snap, uint32_t* units,
+__device__ __forceinline__ void plan_block(const AttnParams& p, int tt, AttnCost cost, uint32_t* units,
                                            AttnWalk* found) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
         const int i = i0 + lane;
         SeqView s{0, 0, 0, 0};
         if (i < p.b.n) s = seq_view(p.c, p.b, i);
-        const uint32_t u = lane_units<KT>(p, tt, s);
+        const uint32_t u = lane_units<KT>(p, tt, s, cost);
         if (i < p.b.n) units[i] = u * p.c.kv_heads;
     }
     __syncthreads();
@@ -276,7 +281,7 @@ __device__ __forceinline__ void plan_block(const AttnParams& p, int tt, int q_mi
         uint32_t total = 0;
         for (int i = lane; i < p.b.n; i += 32) total += units[i];
         total = __reduce_add_sync(0xffffffffu, total);
-        const uint32_t q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(q_min));
+        const uint32_t q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(cost.q_min));
         const uint64_t u64 = static_cast<uint64_t>(blockIdx.x + warp) * q;
         AttnCut c;
         c.u = total;
@@ -297,7 +302,7 @@ __device__ __forceinline__ void plan_block(const AttnParams& p, int tt, int q_mi
                 }
                 at += __shfl_sync(0xffffffffu, incl, 31);
             }
-            c = cut_in<KT>(p, tt, b, seq_view(p.c, p.b, b), units[b] / p.c.kv_heads, at, u, snap);
+            c = cut_in<KT>(p, tt, b, seq_view(p.c, p.b, b), units[b] / p.c.kv_heads, at, u, cost);
         }
         if (lane == 0) {
             if (warp == 0) {

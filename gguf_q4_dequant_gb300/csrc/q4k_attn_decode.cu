@@ -23,8 +23,7 @@ namespace q4k {
 constexpr int kDecKeys = 128;
 constexpr int kDecWarps = 8;                    // consumers; one more warp produces
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
-constexpr int kDecMinUnits = 4;
-constexpr int kDecSnap = 4;
+constexpr AttnCost kDecCost{2, 3, 4};  // item, snap, q_min
 
 template <int D>
 struct DecodeCfg {
@@ -110,7 +109,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     pdl_wait();
     const int tt = 8 * NB / p.group;  // tokens of a row tile
     if (p.b.n > 32) {
-        plan_block<KT>(p, tt, kDecMinUnits, kDecSnap, reinterpret_cast<uint32_t*>(smem), walk_s);
+        plan_block<KT>(p, tt, kDecCost, reinterpret_cast<uint32_t*>(smem), walk_s);
         fence_proxy_async_smem();  // the plan's scratch becomes the ring
     }
     __syncthreads();
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     if (warp == kDecWarps) {
         // ---------------------------------------------------- TMA producer ---
-        AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kDecMinUnits, kDecSnap);
+        AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kDecCost);
         AttnItem it{};
         PageIds ids;
         int slot = 0, issued = 0;
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int pages = KT >> p.c.page_shift;
         const uint32_t page_bytes = static_cast<uint32_t>(page) * D * 2;
         for (int n_items = 0; ok; ++n_items) {
-            const bool more = next_item<KT>(p, w, tt, kDecSnap, it);
+            const bool more = next_item<KT>(p, w, tt, kDecCost, it);
             const int k = n_items % kItemRing;
             ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
             if (!ok) break;
