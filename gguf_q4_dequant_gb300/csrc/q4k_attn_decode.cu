@@ -13,7 +13,14 @@
 // S^T = K Q^T and O^T = V^T P^T), the rows their N of 8 or 16: few rows waste
 // little, and P^T comes from S^T by one 8x8 transpose in registers. (128 rows
 // per tcgen05 MMA, with a round trip through TMEM and barriers per tile, would
-// be idle for the most part.)
+// be idle for the most part: the chunk kernel takes 468 us where this one takes
+// 156.)
+//
+// 64 tokens of 40 heads over 1.02 GB of keys and values: 156 us, 6.6 TB/s (with
+// rows as the M of 16-row products, twice the products and registers: 197 us);
+// 2 tokens over 217 k positions, 64 wide, 445 MB: 77 us, 5.8 TB/s -- the rest is
+// the plan at the start and the joining of ten parts per row tile; one token over
+// 517 positions: 8.9 us, five tiles through one SM per kv head.
 #include <cuda_bf16.h>
 
 #include "q4k_attn.cuh"
@@ -207,8 +214,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         return true;
     };
+    // (one block of rows: the next item's queries are fetched while this one's
+    // parts are put together; two leave no registers for that)
     bool more = fetch();
-    while (more) {
+    for (; more; more = NB == 1 ? more : fetch()) {
         const AttnItem cur = it;
         const int rows = cur.tokens * p.group, p1 = cur.p0 + cur.tokens - 1;
         int pos[NB][2];  // of this lane's rows 8 b + r2, 8 b + r2 + 1
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const uint32_t ks = sbase + slot * Cfg::kStageBytes + slice, vs = ks + Cfg::kTileBytes;
             const bool none = j0 > p1 || (p.window > 0 && j0 + 15 <= cur.p0 - p.window && j0 >= p.sinks);
             if (!none) {
-                // scores: two chains of products each, added at the end
+                // scores: one block of rows in two chains of products, added at the end
                 float s[NB][4], s1[NB][4];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
@@ -247,12 +256,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     const int chunk = 2 * k + k_chunk;
                     ldmatrix_x4(ks + (chunk >> 3) * block_stride + k_key * 128 + (((chunk & 7) ^ (k_key & 7)) << 4), kf);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) mma_16816(k & 1 ? s1[b] : s[b], kf, q[b][k][0], q[b][k][1]);
+                    for (int b = 0; b < NB; ++b) mma_16816(NB == 1 && (k & 1) ? s1[b] : s[b], kf, q[b][k][0], q[b][k][1]);
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[b][e] += s1[b][e];
+                    for (int e = 0; e < 4 && NB == 1; ++e) s[b][e] += s1[b][e];
                 const bool full = tile_is_full<16>(j0 >> 4, cur.p0, p1, p.window, p.sinks);
                 if (!full) {
 #pragma unroll
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
             }
         }
-        more = fetch();  // the next item's queries are on their way while this one's parts are put together
+        if (NB == 1) more = fetch();
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
