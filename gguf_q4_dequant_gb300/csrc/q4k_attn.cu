@@ -16,16 +16,20 @@
 // While the tensor core works for one half, the other half's 128 threads (one
 // row each) turn S into P: the two halves take turns.
 //
-// 4096 tokens of 32 heads over 16384 positions, 128 wide: 0.61-0.63 ms, 1.52 to
-// 1.58 PFLOP/s. A key tile takes 3000 cycles for both halves, 2048 of them
+// 4096 tokens of 32 heads over 16384 positions, 128 wide: 0.59-0.61 ms, 1.57 to
+// 1.63 PFLOP/s. A key tile takes 3000 cycles for both halves, 2048 of them
 // products (tensor pipe 65 %); with the softmax reduced to a copy the whole
 // still takes 0.58 ms: the products are held up by shared memory, of which Q and K are read at
 // 64 KB and V at 32 KB per half while the next tiles come in at 64 KB, together
 // 2048 cycles at 128 bytes. Sharing K between two SMs (cta_group::2) is what
 // would lift that. Two threads per row, P handed over in parts, a pipeline over
 // TMEM loads and hand-ordered exponentials were no faster (0.60 to 0.88 ms).
-// 2017 tokens in 8 sequences with a window of 1024: 51 us; 14 key tiles a CTA
+// 2017 tokens in 8 sequences with a window of 1024: 48 us; 14 key tiles a CTA
 // are 22 us of it, the first loads, row tiles' ends and the joining the rest.
+// Joining: the half that comes last keeps its own part in TMEM, and does not
+// write it out if it sees that the others have come; parts are read and written 16 bytes a
+// thread (2048 tokens of one sequence 42 us; all parts written and read back, 4
+// bytes a thread: 48).
 //
 // Warp roles: 0-3 softmax of half 0, 4-7 of half 1, 8 TMA producer (pages of
 // K and V tiles, Q), 9 MMA issuer, 10-11 scan (below). K and V tiles go through one ring of
@@ -51,10 +55,10 @@ constexpr int kScanWarps = 2;
 // Registers: the block starts with 168 a thread; the last warpgroup gives some to the softmax.
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "registers");
-// item, snap, q_min. With a range of 1, 3 or 4 units at least: a prompt of 512
-// tokens 18.5, 15.4, 18.1 us; 64 tokens over 4000 positions 38.8, 32.4, 29.9 us
+// item, snap, q_min. With a range of 3, 4 or 5 units at least: a prompt of 512
+// tokens 17.9, 15.0, 17.7 us; 64 tokens over 4000 positions 31.5, 30.4, 28.4 us
 // (every part more costs the joining CTA 128 KB); steps that fill the GPU alike.
-constexpr AttnCost kChunkCost{2, 1, 3};
+constexpr AttnCost kChunkCost{3, 1, 4};
 
 template <int D>
 struct ChunkCfg {
@@ -487,6 +491,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 sum += a.x + a.y;
             }
             if (!ok) break;
+            const bool whole = it.i0 == 0 && it.i1 == it.keys.n;
+            const int first = it.first, last = it.last, me = blockIdx.x;
+            uint32_t* count = p.counters + 2 * first + hf;
+            uint32_t arrived = 0;
+            if (!whole && r == 0) arrived = ld_acquire(count);
             if (!__all_sync(0xffffffffu, mbar_wait(b_ofull + 8 * hf, o_phase, p.err))) {
                 ok = false;
                 break;
@@ -494,7 +503,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             o_phase ^= 1;
             tc_fence_after();
             const bool fix = poison[n_items & 3] == n_items;
-            const bool whole = it.i0 == 0 && it.i1 == it.keys.n;
             // the non-finite values that were zeroed, back into 64 columns of the rows that see them
             auto add_back = [&](float (&o)[64], int c0) {
                 for (int j = 0; j < n; ++j) {
@@ -561,63 +569,74 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 continue;
             }
             // part of a row tile: the partial sums go to the scratch, the last
-            // CTA to arrive adds them up in the CTAs' order
-            const int first = it.first, last = it.last;
+            // CTA to arrive adds them up in the CTAs' order, its own from TMEM
             auto part = [&](int cta) {
                 return p.scratch + (static_cast<int64_t>(it.slot(cta)) * 2 + hf) * Cfg::kPartFloats;
             };
-            float* out_part = part(blockIdx.x);
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 64) {
-                float o[64];
-                accumulators(o, c0);
-#pragma unroll
-                for (int e = 0; e < 64; ++e) __stcg(out_part + (c0 + e) * 128 + r, o[e]);
-            }
-            __stcg(out_part + D * 128 + r, ref);
-            __stcg(out_part + (D + 1) * 128 + r, sum);
-            __threadfence();
             auto wg_sync = [&] {
                 mbar_arrive(b_wg + 8 * hf);
                 const bool done = __all_sync(0xffffffffu, mbar_wait(b_wg + 8 * hf, wg_phase, p.err));
                 wg_phase ^= 1;
                 return done;
             };
+            // (all threads of the half have read last_s of the item before: their P has been used)
+            if (r == 0) last_s[hf] = arrived == static_cast<uint32_t>(last - first);
             if (!(ok = wg_sync())) break;
-            if (r == 0) {
-                uint32_t* count = p.counters + 2 * first + hf;
-                const bool here = atomicAdd(count, 1u) == static_cast<uint32_t>(last - first);
-                if (here) *count = 0u;  // as the next call expects it
+            if (!last_s[hf]) {
+                float* out_part = part(me);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    float o[64];
+                    accumulators(o, c0);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4)
+                        __stcg(reinterpret_cast<float4*>(out_part + (c0 + e) * 128) + r,
+                               make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                }
+                __stcg(out_part + D * 128 + r, ref);
+                __stcg(out_part + (D + 1) * 128 + r, sum);
                 __threadfence();
-                last_s[hf] = here;
+                if (!(ok = wg_sync())) break;
+                if (r == 0) {
+                    last_s[hf] = atomicAdd(count, 1u) == static_cast<uint32_t>(last - first);
+                    __threadfence();
+                }
+                if (!(ok = wg_sync())) break;
+                if (!last_s[hf]) continue;
             }
-            if (!(ok = wg_sync())) break;
-            if (!last_s[hf]) continue;
-            // the first two parts' loads together (two are what there mostly are)
-            const float *f0 = part(first), *f1 = part(first + 1);
-            const float r0 = __ldcg(f0 + D * 128 + r), r1 = __ldcg(f1 + D * 128 + r);
-            const float s0 = __ldcg(f0 + (D + 1) * 128 + r), s1 = __ldcg(f1 + (D + 1) * 128 + r);
-            float top = fmaxf(r0, r1);
-            for (int cta = first + 2; cta <= last; ++cta) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
+            if (r == 0) *count = 0u;  // as the next call expects it
+            float top = ref;
+            for (int cta = first; cta <= last; ++cta)
+                if (cta != me) top = fmaxf(top, __ldcg(part(cta) + D * 128 + r));
             const float base = top == -INFINITY ? 0.f : top;
-            const float w0 = ex2(r0 - base), w1 = ex2(r1 - base);
-            float all = s0 * w0 + s1 * w1;
-            for (int cta = first + 2; cta <= last; ++cta)
-                all = fmaf(__ldcg(part(cta) + (D + 1) * 128 + r), ex2(__ldcg(part(cta) + D * 128 + r) - base), all);
+            float all = 0.f;
+            for (int cta = first; cta <= last; ++cta) {
+                const bool own = cta == me;
+                const float its_ref = own ? ref : __ldcg(part(cta) + D * 128 + r);
+                const float its_sum = own ? sum : __ldcg(part(cta) + (D + 1) * 128 + r);
+                all = fmaf(its_sum, ex2(its_ref - base), all);
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {
-                float o[64], x[64];
-#pragma unroll
-                for (int e = 0; e < 64; ++e) o[e] = __ldcg(f0 + (c0 + e) * 128 + r);
-#pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] = __ldcg(f1 + (c0 + e) * 128 + r);
-#pragma unroll
-                for (int e = 0; e < 64; ++e) o[e] = fmaf(x[e], w1, o[e] * w0);
-                for (int cta = first + 2; cta <= last; ++cta) {
+                float o[64] = {};
+#pragma unroll 1
+                for (int cta = first; cta <= last; ++cta) {
                     const float* from = part(cta);
+                    float x[64], its_ref = ref;
+                    if (cta == me) {
+                        accumulators(x, c0);
+                    } else {
+                        its_ref = __ldcg(from + D * 128 + r);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) x[e] = __ldcg(from + (c0 + e) * 128 + r);
-                    const float w = ex2(__ldcg(from + D * 128 + r) - base);
+                        for (int e = 0; e < 64; e += 4) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4*>(from + (c0 + e) * 128) + r);
+                            x[e] = y.x;
+                            x[e + 1] = y.y;
+                            x[e + 2] = y.z;
+                            x[e + 3] = y.w;
+                        }
+                    }
+                    const float w = ex2(its_ref - base);
 #pragma unroll
                     for (int e = 0; e < 64; ++e) o[e] = fmaf(x[e], w, o[e]);
                 }

@@ -74,6 +74,13 @@ struct AttnCost {
     int item, snap, q_min;
 };
 
+// A counter that other CTAs add to after they have written their parts.
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t x;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+
 // What one CTA does, item by item.
 struct AttnItem {
     int t_first, tokens;  // rows of the step's arrays
