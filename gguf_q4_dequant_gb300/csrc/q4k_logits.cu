@@ -11,18 +11,22 @@
 // mask at a few instructions each, four at a time, with one comparison per four.
 // The four warps count the history into a table of the CTA's part of the row in
 // shared memory (integer atomics: their order does not matter; 16 bits per logit
-// unless the history is long enough to overflow them); whoever counts a token
-// first puts it on a list, and the tokens of the list are adjusted one by one
+// unless the history is long enough to overflow them); tokens counted for the
+// first time go on a list, and the tokens of the list are adjusted one by one
 // and go over the streamed logits at the end. A thread whose largest logit turns
 // out to be one of them has its logits looked through again, by a warp, without
 // the ones on the list.
 // (Penalties applied where the logits stream by took 68 instructions per logit,
 // half of the warps dividing for one lane's token: 43 us for 64 rows of 151936,
-// issue-bound. The same steps before or after the stream, by all warps, left the
-// memory idle through four dependent loads: 33 and 35 us. Now 26 us, 3.0 TB/s;
-// 200 rows of 50257, not kept: 15 us, 2.8 TB/s; one row of 128256: 5.9 us. What
-// is left is the chain before and after the stream: starts, history, list, the
-// look again, the cluster's exchange.)
+// issue-bound. The same steps before or after the stream, by all warps: 33 and 35
+// us, 27 with the row asked for into L2 before. Beside the stream an access of
+// shared memory takes about half a microsecond, as it queues behind the stream's:
+// with the tables cleared by all warps first, one atomic operation per
+// history entry, eight of them in flight, and one per warp and batch for the
+// list's places, 22 us, 3.6 TB/s; one entry after another, three atomics each:
+// 26 us. 200 rows of 50257, not kept: 13.4 us, 3.1 TB/s; one row of 128256: 5.6 us.
+// Of the 22 us the stream is 13; the rest is the chain before and after
+// it: starts, the list, the look again, the cluster's exchange.)
 //
 // Rows start at any multiple of 4 bytes (V may be odd), so a row is cut into
 // the 16-byte groups of the memory, the first and last of them partly used.
@@ -37,16 +41,16 @@ namespace {
 
 constexpr int kPickThreads = 512;
 constexpr int kPickApart = 128;          // threads that see to the penalised and biased tokens
-constexpr int kPickBatch = 4;            // groups of 4 logits that a thread has in flight
+constexpr int kPickBatch = 3;            // groups of 4 logits that a thread has in flight
 constexpr int kPickTableGroups = 7168;   // groups that the tables cover at most
 constexpr int kPickList = 1024;          // adjusted tokens that wait for the end of the stream
 constexpr int kPickMaxCluster = 8;
 
-// Bytes of the tables of `groups` groups (a multiple of 32): two bits per logit
-// (seen to apart; not on the list for want of room), 16-bit counts; the list.
-__host__ __device__ constexpr int pick_marks_bytes(int groups) { return groups / 2; }
+// Bytes of the tables of `groups` groups (a multiple of 32): a 16-bit count per
+// logit, a bit per logit that is not on the list for want of room; the list.
+__host__ __device__ constexpr int pick_late_bytes(int groups) { return groups / 2; }
 __host__ __device__ constexpr int pick_tables_bytes(int groups) {
-    return 2 * pick_marks_bytes(groups) + 8 * groups + 8 * kPickList;
+    return pick_late_bytes(groups) + 8 * groups + 8 * kPickList;
 }
 
 // The largest number met and its token: by value, then by lower token.
@@ -131,11 +135,17 @@ __global__ void __launch_bounds__(kPickThreads, 3)
     extern __shared__ __align__(16) uint8_t tables[];
     __shared__ unsigned long long best_s[kPickThreads / 32];
     __shared__ unsigned long long cluster_best[kPickMaxCluster];
-    __shared__ int ids_s[kApart ? kPickApart : 1], again_s[kApart ? kPickThreads : 1], listed, again;
-    if (C > 1) cluster_arrive_relaxed();
-    pdl_wait();
-    if (threadIdx.x == 0) pdl_launch_dependents();
+    __shared__ int again_s[kApart ? kPickThreads : 1], listed, again;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto clear = [&] {
+        for (int i = tid; i < (pick_late_bytes(table_groups) + 8 * table_groups) / 16; i += kPickThreads)
+            reinterpret_cast<uint4*>(tables)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid == 0) listed = again = 0;
+    };
+    if (C > 1) cluster_arrive_relaxed();
+    if (kApart) clear();
+    pdl_wait();
+    if (tid == 0) pdl_launch_dependents();
     const int rank = blockIdx.x % C;
     const int64_t m = blockIdx.x / C;
     const int64_t V = a.V, row = m * V;
@@ -155,16 +165,17 @@ __global__ void __launch_bounds__(kPickThreads, 3)
         rules.b0 = a.bias_starts[m];
         rules.b1 = a.bias_starts[m + 1];
     }
-    const bool wide = rules.h1 - rules.h0 > 65535;
-    uint32_t* marks = reinterpret_cast<uint32_t*>(tables);
-    uint32_t* late = marks + pick_marks_bytes(table_groups) / 4;
-    uint32_t* counts = late + pick_marks_bytes(table_groups) / 4;
+    // A token's entry: how often the history has it, and the highest bit if it has a bias.
+    const bool wide = rules.h1 - rules.h0 > 32767;
+    uint32_t* late = reinterpret_cast<uint32_t*>(tables);
+    uint32_t* counts = late + pick_late_bytes(table_groups) / 4;
     int2* list = reinterpret_cast<int2*>(counts + 2 * table_groups);  // token, its bias entry or -1; then its value's bits
     const int step = kApart ? (wide ? table_groups / 2 : table_groups) : groups;  // groups that the tables cover at a time
 
     Best best{-INFINITY, 0xFFFFFFFFu};
     uint32_t any = rules.mask == nullptr;  // bits 0..3: some token is allowed
     for (int g_tab = g_begin; g_tab < g_end; g_tab += step) {
+        if (kApart) __syncthreads();  // the tables are clear
         const int n = min(step, g_end - g_tab);
         const int64_t first = s - 4 * static_cast<int64_t>(g_tab);  // logit v is entry v + first of the tables
         // a token's place in the tables, or -1
@@ -172,11 +183,14 @@ __global__ void __launch_bounds__(kPickThreads, 3)
             const int64_t at = v + first;
             return v >= 0 && v < V && at >= 0 && at < 4 * n ? static_cast<int>(at) : -1;
         };
+        auto entry = [&](int at) { return counts + (wide ? at : at >> 1); };
+        auto shift = [&](int at) { return wide ? 0 : 16 * (at & 1); };
+        const uint32_t field = wide ? 0xFFFFFFFFu : 0xFFFFu, flag = field ^ (field >> 1);
         auto adjusted = [&](int at, int v, float bias, bool has_bias) {
             float y = a.logits[row + v];
             const bool ok = rules.allowed(v);
             if (rules.h1 > rules.h0) {
-                const uint32_t c = wide ? counts[at] : counts[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
+                const uint32_t c = *entry(at) >> shift(at) & (field ^ flag);
                 if (c) y = rules.penalise(y, c);
             }
             if (has_bias) y = __fadd_rn(y, bias);
@@ -248,49 +262,56 @@ __global__ void __launch_bounds__(kPickThreads, 3)
             const int t = tid - T;
             auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kPickApart) : "memory"); };
             const int h0 = rules.h0, h1 = rules.h1, b0 = rules.b0, b1 = rules.b1;
-            if (t == 0) listed = again = 0;
-            for (int i = t; i < (n + 7) / 8; i += kPickApart) marks[i] = late[i] = 0u;
-            if (h1 > h0)
-                for (int i = t; i < (n + 1) / 2 * (wide ? 2 : 1); i += kPickApart)
-                    reinterpret_cast<uint4*>(counts)[i] = make_uint4(0u, 0u, 0u, 0u);
-            sync();
-            auto enlist = [&](int at, int v, int bias_at) {
-                const int k = atomicAdd(&listed, 1);
-                if (k < kPickList)
-                    list[k] = make_int2(v, bias_at);
+            // (by whole warps) puts tokens on the list, at places from `to` on
+            auto put = [&](int to, int at, int v, int bias_at) {
+                if (to < kPickList)
+                    list[to] = make_int2(v, bias_at);
                 else
                     atomicOr(late + (at >> 5), 1u << (at & 31));
             };
-            // biases: the last entry of a token counts, so the entries go by from
-            // the end, a block at a time, and yield to a later one of their block
-            for (int i1 = b1; i1 > b0; i1 -= kPickApart) {
-                const int i0 = max(b0, i1 - kPickApart), k = i1 - i0;
-                const int v = t < k ? a.bias_ids[i0 + t] : -1;
-                ids_s[t] = v;
-                sync();
-                bool later = false;
-                for (int j = t + 1; j < k; ++j) later |= ids_s[j] == v;
-                const int at = place(v);
-                if (at >= 0 && !later) {
-                    const uint32_t bit = 1u << (at & 31);
-                    if (!(atomicOr(marks + (at >> 5), bit) & bit)) enlist(at, v, i0 + t);
-                }
-                sync();
-            }
+            auto places = [&](int k) { return __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(&listed, k) : 0, 0); };
+            const uint32_t below = (1u << lane) - 1;
             constexpr int kUnroll = 8;  // history entries in flight
-            for (int i0 = h0 + t; i0 < h1; i0 += kUnroll * kPickApart) {
-                int v[kUnroll];
+            auto history = [&](int i) { return i < h1 ? a.history[i] : -1; };
+            int v[kUnroll];
 #pragma unroll
-                for (int e = 0; e < kUnroll; ++e) v[e] = i0 + e * kPickApart < h1 ? a.history[i0 + e * kPickApart] : -1;
+            for (int e = 0; e < kUnroll; ++e) v[e] = history(h0 + t + e * kPickApart);
+            // biases, by one warp: the last entry of a token counts, so the entries go by from the end
+            if (t < 32) {
+                for (int i1 = b1; i1 > b0; i1 -= 32) {
+                    const int i = i1 - 1 - lane, w = i >= b0 ? a.bias_ids[i] : -1, at = place(w);
+                    const bool last = (__match_any_sync(0xffffffffu, w) & below) == 0u;
+                    bool is = false;
+                    if (at >= 0 && last) is = !(atomicOr(entry(at), flag << shift(at)) >> shift(at) & flag);
+                    const uint32_t m = __ballot_sync(0xffffffffu, is);
+                    if (m == 0u) continue;
+                    const int to = places(__popc(m));
+                    if (is) put(to + __popc(m & below), at, w, i);
+                }
+            }
+            sync();
+            for (int i0 = h0; i0 < h1; i0 += kUnroll * kPickApart) {
+                uint32_t first[kUnroll];
+                if (i0 != h0)
+#pragma unroll
+                    for (int e = 0; e < kUnroll; ++e) v[e] = history(i0 + t + e * kPickApart);
+#pragma unroll
+                for (int e = 0; e < kUnroll; ++e) {  // (a bias has its token on the list already)
+                    const int at = place(v[e]);
+                    first[e] = at >= 0 ? atomicAdd(entry(at), 1u << shift(at)) >> shift(at) & field : 1u;
+                }
+                int news = 0;
 #pragma unroll
                 for (int e = 0; e < kUnroll; ++e) {
-                    const int at = place(v[e]);
-                    if (at < 0) continue;
-                    const int sh = wide ? 0 : 16 * (at & 1);
-                    const uint32_t old = atomicAdd(counts + (wide ? at : at >> 1), 1u << sh);
-                    if (wide ? old != 0u : (old >> sh & 0xFFFFu) != 0u) continue;
-                    const uint32_t bit = 1u << (at & 31);
-                    if (!(atomicOr(marks + (at >> 5), bit) & bit)) enlist(at, v[e], -1);  // (else a bias has it)
+                    first[e] = __ballot_sync(0xffffffffu, first[e] == 0u);
+                    news += __popc(first[e]);
+                }
+                if (news == 0) continue;
+                int to = places(news);
+#pragma unroll
+                for (int e = 0; e < kUnroll; ++e) {
+                    if (first[e] >> lane & 1u) put(to + __popc(first[e] & below), place(v[e]), v[e], -1);
+                    to += __popc(first[e]);
                 }
             }
             sync();
@@ -300,7 +321,10 @@ __global__ void __launch_bounds__(kPickThreads, 3)
                 list[i].y = __float_as_int(adjusted(place(e.x), e.x, bias, e.y >= 0));
             }
         }
-        auto marked = [&](int64_t v) { return kApart && (marks[(v + first) >> 5] >> ((v + first) & 31) & 1u); };
+        auto marked = [&](int64_t v) {
+            const int at = static_cast<int>(v + first);
+            return kApart && (*entry(at) >> shift(at) & field) != 0u;
+        };
         if (kApart) {
             __syncthreads();  // all is listed, and the logits are written
             if (a.out != nullptr)
@@ -359,7 +383,10 @@ __global__ void __launch_bounds__(kPickThreads, 3)
                 best.take(y, static_cast<uint32_t>(v));
             }
         }
-        if (kApart && g_tab + step < g_end) __syncthreads();  // the tables are read
+        if (kApart && g_tab + step < g_end) {
+            __syncthreads();  // the tables are read
+            clear();
+        }
     }
 
     if (a.pick == nullptr) {

@@ -742,3 +742,51 @@ def test_pick_long_rows_and_histories(q4k, R, V):
     y, best, _ = pick_ref(x, hist, pen, bias, None)
     out, got = pick_run(q4k, x, hist, pen, bias)
     assert np.array_equal(got, best) and np.array_equal(out, y.astype(np.float32))
+
+
+@pytest.mark.parametrize("total", [32766, 32767, 32768, 32769, 65535, 65536])
+def test_pick_counts_of_neighbours(q4k, total):
+    """Histories about as long as a 15-bit and a 16-bit count, of two tokens side by side, with and without biases."""
+    V = 23
+    x = (np.random.default_rng(total).integers(-40, 41, (4, V)) / 8).astype(np.float32)
+    split = [total, 0, total // 2, total - 1]
+    hist = [[8] * k + [9] * (total - k) for k in split]
+    pen = [[2.0, 0.5, 1.0 / 4096]] * 4
+    bias = [[(8, 2.0), (9, -1.0), (8, 40.0)], [(9, 40.0)], [], [(8, 16.0)]]
+    for b in (bias, None):
+        y, best, _ = pick_ref(x, hist, pen, b, None)
+        out, got = pick_run(q4k, x, hist, pen, b)
+        assert np.array_equal(got, best) and np.array_equal(out, y.astype(np.float32))
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 700])
+def test_pick_last_bias_counts(q4k, n):
+    """Biases of few tokens over and over, more than one at a time is looked at."""
+    rng = np.random.default_rng(n)
+    V = 37
+    x = (rng.integers(-40, 41, (5, V)) / 8).astype(np.float32)
+    bias = [[(int(v), float(rng.integers(-64, 65)) / 4) for v in rng.integers(-2, V + 2, n)] for _ in range(5)]
+    hist = [rng.integers(0, V, 12).tolist() for _ in range(5)]
+    pen = [[2.0, 0.25, 0.125]] * 5
+    for h in (hist, None):
+        y, best, _ = pick_ref(x, h, pen, bias, None)
+        out, got = pick_run(q4k, x, h, pen, bias)
+        assert np.array_equal(got, best) and np.array_equal(out, y.astype(np.float32))
+
+
+@pytest.mark.parametrize("V,seen,biased", [(5000, 3000, 0), (5003, 900, 1500), (4097, 4097, 4097), (40001, 0, 30000)])
+def test_pick_many_adjusted_tokens(q4k, V, seen, biased):
+    """More penalised and biased tokens than wait for the end of the row on their own."""
+    rng = np.random.default_rng(V)
+    R = 2
+    x = (rng.integers(-40, 41, (R, V)) / 8).astype(np.float32)
+    hist = [np.r_[rng.choice(V, seen, replace=False), rng.integers(0, V, seen // 3)].tolist() for _ in range(R)]
+    pen = [[2.0, 0.25, 0.125]] * R
+    bias = [[(int(v), float(rng.integers(-64, 65)) / 4) for v in np.r_[rng.choice(V, biased, replace=False), rng.integers(0, V, 9)]]
+            for _ in range(R)]
+    allowed = rng.random((R, V)) < 0.7
+    for ok in (None, allowed):
+        y, best, _ = pick_ref(x, hist, pen, bias, ok)
+        for alias in (False, True):
+            out, got = pick_run(q4k, x, hist, pen, bias, ok, alias=alias)
+            assert np.array_equal(got, best) and np.array_equal(out, y.astype(np.float32))
