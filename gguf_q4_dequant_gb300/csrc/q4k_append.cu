@@ -12,7 +12,7 @@
 // are on their way: that takes four loads, each from the result of the one
 // before. 2894 tokens of 48 rows, 108 MB: 21 us, 5.2 TB/s (26 us when the rows
 // were loaded after the place was known and the norm's and rotation's steps were
-// taken whether wanted or not); 64 tokens of 56 rows: 5.3 us, the launch and the
+// taken whether wanted or not); 64 tokens of 56 rows: 3.9 us, the launch and the
 // four loads.
 #include <cuda_bf16.h>
 
@@ -21,21 +21,25 @@
 
 namespace q4k {
 
-constexpr int kAppThreads = 256;
-
 __device__ __forceinline__ uint2 bf16x4(float4 x) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-constexpr int kAppRows = 6;  // rows that a thread has in flight
+// A token is one block's, of one of two widths: wide, with all rows on their way
+// at once, for up to one token per SM (64 tokens of 56 rows 3.9 us, 5.4 in the other
+// width; 152 tokens 4.3, 5.9), else so that blocks in different phases share an
+// SM (200 tokens 6.2 us, 6.6 wide; 2894 tokens of 48 rows 21 us, 43 wide).
+__host__ __device__ constexpr int app_threads(bool wide) { return wide ? 1024 : 256; }
+__host__ __device__ constexpr int app_rows(bool wide) { return wide ? 2 : 6; }  // rows that a thread has in flight
 
-template <int D, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kAppThreads, 4)
+template <int D, int kPairs, bool kNorm, bool kWide>
+__global__ void __launch_bounds__(app_threads(kWide), kWide ? 1 : 4)
     q4k_append_kernel(const CacheLayer c, const Batch b, const float* __restrict__ Yq,
                       const float* __restrict__ Yk, const float* __restrict__ Yv,
                       uint16_t* __restrict__ q_out, int heads, const float* __restrict__ rope,
                       const float* __restrict__ q_norm, const float* __restrict__ k_norm, float eps) {
+    constexpr int kAppThreads = app_threads(kWide), kAppRows = app_rows(kWide);
     constexpr int L = D / 4;                // lanes per row
     constexpr int kStep = kAppThreads / L;  // rows that the block holds at a time
     pdl_wait();
@@ -55,10 +59,14 @@ __global__ void __launch_bounds__(kAppThreads, 4)
         }
     };
     load(r);
-    // the sequence: as many of starts[1 ..] as are not above t
-    int i = 0;
-    for (int j = 0; j < b.n; j += kAppThreads)
-        i += __syncthreads_count(j + threadIdx.x < b.n && b.starts[j + threadIdx.x + 1] <= t);
+    // the sequence: as many of starts[1 ..] as are not above t; of more than the
+    // block has threads, every `every`-th first, then those between two of them
+    const int every = (b.n + kAppThreads - 1) / kAppThreads, last = min((static_cast<int>(threadIdx.x) + 1) * every, b.n);
+    int i = every * __syncthreads_count(static_cast<int>(threadIdx.x) * every < b.n && b.starts[last] <= t);
+    if (every > 1) {
+        const int j = i + static_cast<int>(threadIdx.x);
+        i += __syncthreads_count(static_cast<int>(threadIdx.x) < every && j < b.n && b.starts[j + 1] <= t);
+    }
     int64_t pos = -1, off = -1;
     if (i < b.n) {
         const SeqView s = seq_view(c, b, i);
@@ -132,24 +140,26 @@ __global__ void __launch_bounds__(kAppThreads, 4)
     }
 }
 
-template <int D>
+template <int D, bool kWide>
 static cudaError_t launch_d(const CacheLayer& c, const Batch& b, const float* Yq, const float* Yk, const float* Yv,
                             uint16_t* q_out, int heads, const float* rope, int pairs, const float* q_norm,
                             const float* k_norm, float eps, cudaStream_t stream, int pdl) {
     const bool norm = q_norm != nullptr || k_norm != nullptr;
-    auto kernel = pairs == 0   ? (norm ? q4k_append_kernel<D, 0, true> : q4k_append_kernel<D, 0, false>)
-                  : pairs == 1 ? (norm ? q4k_append_kernel<D, 1, true> : q4k_append_kernel<D, 1, false>)
-                               : (norm ? q4k_append_kernel<D, 2, true> : q4k_append_kernel<D, 2, false>);
-    return launch_serve(kernel, dim3(b.tokens), dim3(kAppThreads), 0, stream, pdl, 1, c, b, Yq, Yk, Yv, q_out,
+    auto kernel = pairs == 0   ? (norm ? q4k_append_kernel<D, 0, true, kWide> : q4k_append_kernel<D, 0, false, kWide>)
+                  : pairs == 1 ? (norm ? q4k_append_kernel<D, 1, true, kWide> : q4k_append_kernel<D, 1, false, kWide>)
+                               : (norm ? q4k_append_kernel<D, 2, true, kWide> : q4k_append_kernel<D, 2, false, kWide>);
+    return launch_serve(kernel, dim3(b.tokens), dim3(app_threads(kWide)), 0, stream, pdl, 1, c, b, Yq, Yk, Yv, q_out,
                         heads, rope, q_norm, k_norm, eps);
 }
 
 cudaError_t launch_append(const CacheLayer& c, const Batch& b, const float* Yq, const float* Yk,
                           const float* Yv, uint16_t* q_out, int heads, int head_dim, const float* rope,
                           int pairs, const float* q_norm, const float* k_norm, float eps,
-                          cudaStream_t stream, int pdl) {
-    return (head_dim == 64 ? launch_d<64> : launch_d<128>)(c, b, Yq, Yk, Yv, q_out, heads, rope, pairs, q_norm,
-                                                           k_norm, eps, stream, pdl);
+                          cudaStream_t stream, const DeviceInfo& dev, int pdl) {
+    const bool wide = b.tokens <= dev.num_sms;
+    auto launch = head_dim == 64 ? (wide ? launch_d<64, true> : launch_d<64, false>)
+                                 : (wide ? launch_d<128, true> : launch_d<128, false>);
+    return launch(c, b, Yq, Yk, Yv, q_out, heads, rope, pairs, q_norm, k_norm, eps, stream, pdl);
 }
 
 }  // namespace q4k

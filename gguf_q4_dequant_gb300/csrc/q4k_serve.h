@@ -56,7 +56,7 @@ __device__ __forceinline__ SeqView seq_view(const CacheLayer& c, const Batch& b,
 cudaError_t launch_append(const CacheLayer& c, const Batch& b, const float* Yq, const float* Yk,
                           const float* Yv, uint16_t* q_out, int heads, int head_dim, const float* rope,
                           int pairs, const float* q_norm, const float* k_norm, float eps,
-                          cudaStream_t stream, int pdl);
+                          cudaStream_t stream, const DeviceInfo& dev, int pdl);
 
 struct AttnArgs {
     const uint16_t* Q;

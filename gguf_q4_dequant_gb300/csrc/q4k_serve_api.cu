@@ -124,7 +124,7 @@ int q4k_cache_append(const q4k_cache* c, int layer, const int32_t* seqs, int n, 
     if ((rc = device_info(&dev)) != Q4K_OK) return rc;
     const Batch b{seqs, starts, n, static_cast<int32_t>(tokens)};
     return launch_append(layer_view(*c, layer), b, Yq, Yk, Yv, q_out, heads, c->head_dim, rope, pairs,
-                         q_norm, k_norm, eps, static_cast<cudaStream_t>(stream), pdl_mode()) == cudaSuccess
+                         q_norm, k_norm, eps, static_cast<cudaStream_t>(stream), *dev, pdl_mode()) == cudaSuccess
                ? Q4K_OK
                : Q4K_ERR_CUDA;
 }

@@ -402,6 +402,62 @@ def test_append(q4k, dim, pairs, norm, heads, kv, page):
     assert torch.equal(got_k, kc) and torch.equal(got_v, vc), "rows beside the new tokens' changed"
 
 
+@pytest.mark.parametrize("n,most", [(7, 120), (300, 3), (1100, 1), (1100, 2), (4096, 2)])
+def test_append_finds_every_token(q4k, n, most):
+    """Many sequences, some without new tokens, and steps of few and many tokens: plain rounding, exact."""
+    rng = np.random.default_rng(n + most)
+    news = rng.integers(0, most + 1, n)
+    news[rng.random(n) < 0.3] = 0
+    if n == 1100 and most == 1:
+        news[rng.random(n) < 0.9] = 0  # few tokens of many sequences
+    lens = news + rng.integers(0, 9, n)
+    page, kv, dim, heads = 16, 2, 64, 4
+    cache = make_cache(q4k, lens.tolist(), page, kv, dim, width=9)
+    cache.k.zero_()
+    cache.v.zero_()
+    T = int(news.sum())
+    Y = [torch.randn(T, h * dim, device=DEV) for h in (heads, kv, kv)]
+    q_out = torch.zeros(T, heads, dim, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_cache_append(cache, 0, ints(range(n)), ints(np.concatenate([[0], np.cumsum(news)])), *Y, q_out, heads)
+    torch.cuda.synchronize()
+    assert torch.equal(q_out, Y[0].view(T, heads, dim).to(torch.bfloat16))
+    seq = np.repeat(np.arange(n), news)
+    at = np.concatenate([np.arange(m - k, m) for m, k in zip(lens, news)])
+    ids = cache.table.cpu().numpy()[seq, at // page]
+    for got, y in ((cache.k, Y[1]), (cache.v, Y[2])):
+        want = torch.zeros_like(got)
+        want[0, torch.tensor(ids, device=DEV).long(), :, torch.tensor(at % page, device=DEV).long()] = \
+            y.view(T, kv, dim).to(torch.bfloat16)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dim,pairs,norm,heads,kv", [(128, 2, True, 40, 8), (128, 1, False, 5, 1), (64, 2, False, 32, 8),
+                                                     (64, 1, True, 3, 3)])
+def test_append_same_bits_in_steps_of_any_size(q4k, dim, pairs, norm, heads, kv):
+    T, page = 700, 32
+    cache, other = (make_cache(q4k, [T + 5], page, kv, dim) for _ in range(2))
+    other.table.copy_(cache.table)
+    for c in (cache, other):
+        c.k.zero_()
+        c.v.zero_()
+    Y = [torch.randn(T, h * dim, device=DEV) for h in (heads, kv, kv)]
+    rows = cache.table.shape[1] * page
+    ang = torch.arange(rows, device=DEV)[:, None] * 0.37 ** (torch.arange(dim // 2, device=DEV) / 9.0)
+    rope = torch.cat([ang.cos(), ang.sin()], 1).float()
+    qn, kn = (torch.rand(dim, device=DEV) + 0.5, torch.rand(dim, device=DEV) + 0.5) if norm else (None, None)
+    q_out = torch.zeros(T, heads, dim, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_cache_append(cache, 0, ints([0]), ints([0, T]), *Y, q_out, heads, rope, pairs, qn, kn)
+    part, t = torch.zeros_like(q_out), 0
+    while t < T:  # the same tokens a few at a time
+        m = min(37, T - t)
+        other.lens.fill_(5 + t + m)
+        q4k.q4k_cache_append(other, 0, ints([0]), ints([0, m]), *(y[t:t + m] for y in Y), part[t:t + m], heads, rope,
+                             pairs, qn, kn)
+        t += m
+    torch.cuda.synchronize()
+    assert torch.equal(part, q_out) and torch.equal(cache.k, other.k) and torch.equal(cache.v, other.v)
+
+
 def test_append_out_of_range(q4k):
     """Ids, positions and pages out of range store nothing; the queries are still written, unrotated."""
     cache = make_cache(q4k, [5, 20], 16, 1, 64)
