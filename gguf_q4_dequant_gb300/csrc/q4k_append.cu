@@ -12,8 +12,9 @@
 // are on their way: that takes four loads, each from the result of the one
 // before. 2894 tokens of 48 rows, 108 MB: 21 us, 5.2 TB/s (26 us when the rows
 // were loaded after the place was known and the norm's and rotation's steps were
-// taken whether wanted or not); 64 tokens of 56 rows: 3.9 us, the launch and the
-// four loads.
+// taken whether wanted or not); with a norm 2894 tokens of 56 rows take 28 us for 23,
+// with rotation 33: five shuffles per row, and registers for 4 blocks per SM only.
+// 64 tokens of 56 rows: 3.7 us, the launch and the four loads.
 #include <cuda_bf16.h>
 
 #include "q4k_device.cuh"
@@ -27,7 +28,7 @@ __device__ __forceinline__ uint2 bf16x4(float4 x) {
 }
 
 // A token is one block's, of one of two widths: wide, with all rows on their way
-// at once, for up to one token per SM (64 tokens of 56 rows 3.9 us, 5.4 in the other
+// at once, for up to one token per SM (64 tokens of 56 rows 3.7 us, 5.4 in the other
 // width; 152 tokens 4.3, 5.9), else so that blocks in different phases share an
 // SM (200 tokens 6.2 us, 6.6 wide; 2894 tokens of 48 rows 21 us, 43 wide).
 __host__ __device__ constexpr int app_threads(bool wide) { return wide ? 1024 : 256; }
@@ -95,6 +96,11 @@ __global__ void __launch_bounds__(app_threads(kWide), kWide ? 1 : 4)
         }
     }
     const bool turn = kPairs != 0 && pos >= 0;
+    float4 wq = make_float4(0.f, 0.f, 0.f, 0.f), wk = wq;
+    if (kNorm) {
+        if (q_norm != nullptr) wq = *(reinterpret_cast<const float4*>(q_norm) + lane);
+        if (k_norm != nullptr) wk = *(reinterpret_cast<const float4*>(k_norm) + lane);
+    }
     // whole warps keep together: the shuffles need every lane of a row
     for (int h0 = r; h0 - r < rows; h0 += kAppRows * kStep) {
         if (h0 != r) load(h0);
@@ -105,14 +111,14 @@ __global__ void __launch_bounds__(app_threads(kWide), kWide ? 1 : 4)
             const bool in = h < rows, is_q = h < heads, is_v = h >= heads + G;
             float4 y = in ? x[e] : make_float4(0.f, 0.f, 0.f, 0.f);
             if (kNorm) {
-                const float* w = is_q ? q_norm : is_v ? nullptr : k_norm;
+                const bool scaled = is_q ? q_norm != nullptr : !is_v && k_norm != nullptr;
                 float ss = y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (w != nullptr) {
-                    const float4 wv = *reinterpret_cast<const float4*>(w + 4 * lane);
-                    const float f = 1.f / sqrtf(ss * (1.f / D) + eps);
-                    y = make_float4(y.x * f * wv.x, y.y * f * wv.y, y.z * f * wv.z, y.w * f * wv.w);
+                if (scaled) {
+                    const float f = rsqrtf(ss * (1.f / D) + eps);  // (within 2 ulp, before a rounding to 8 bits)
+                    const float4 w = is_q ? wq : wk;
+                    y = make_float4(y.x * f * w.x, y.y * f * w.y, y.z * f * w.z, y.w * f * w.w);
                 }
             }
             if (kPairs != 0) {
@@ -131,10 +137,22 @@ __global__ void __launch_bounds__(app_threads(kWide), kWide ? 1 : 4)
             }
             if (is_q) {
                 *(reinterpret_cast<uint2*>(q_out + (static_cast<int64_t>(t) * heads + h) * D) + lane) = bf16x4(y);
-            } else if (in && off >= 0) {
+            } else if (in && off >= 0 && !(kWide && is_v)) {
                 const int g = is_v ? h - heads - G : h - heads;
                 uint16_t* dst = (is_v ? c.v : c.k) + off + (static_cast<int64_t>(g) << c.page_shift) * D;
                 *(reinterpret_cast<uint2*>(dst) + lane) = bf16x4(y);
+            }
+        }
+        if (kWide) {
+            // values after keys, as the other width's threads write them one after
+            // the other: what a cache of one tensor for both holds is then the values
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kAppRows; ++e) {
+                const int h = h0 + e * kStep;
+                if (h < heads + G || h >= rows || off < 0) continue;
+                uint16_t* dst = c.v + off + (static_cast<int64_t>(h - heads - G) << c.page_shift) * D;
+                *(reinterpret_cast<uint2*>(dst) + lane) = bf16x4(x[e]);
             }
         }
     }
