@@ -131,13 +131,24 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+_current_stream = None  # a function that gives the address of the current stream
+
+
+def _find_current_stream():
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is not None:  # the same address without building a Stream object (2.9 us of a call's host time)
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:  # the same address without building a Stream object (2.9 us of a call's host time)
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -366,11 +377,11 @@ def q4k_cache_workspace(cache: Cache) -> int:
 
 def _tensor(t, dtype, need, name):
     """Device address of a contiguous tensor of at least `need` elements (an int is passed through)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.numel() >= need and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype != dtype:  # (what is wrong with it)
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() < need:
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs {need}")
