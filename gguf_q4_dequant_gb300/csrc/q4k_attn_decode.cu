@@ -315,7 +315,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                             }
                         }
                 }
-                uint32_t pt[NB][2];
+                // A weight is the sum of two bf16, 16 bits: one would add as much error
+                // as the output's own rounding, and here the tensor core has time for
+                // both. The upper is cut off, not rounded, and the lower is not 0 unless
+                // the weight is, so that both parts of an infinite value's product have its sign.
+                uint32_t pt[NB][2], pt_lo[NB][2];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const float z0 = ref[b][0] == -INFINITY ? 0.f : ref[b][0], z1 = ref[b][1] == -INFINITY ? 0.f : ref[b][1];
@@ -324,8 +328,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         const float x0 = ex2(fmaf(s[b][2 * e], p.scale_log2, -z0)), x1 = ex2(fmaf(s[b][2 * e + 1], p.scale_log2, -z1));
                         sum[b][0] += x0;
                         sum[b][1] += x1;
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(x0, x1);
-                        pt[b][e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&x));
+                        const uint32_t u0 = __float_as_uint(x0) & 0xFFFF0000u, u1 = __float_as_uint(x1) & 0xFFFF0000u;
+                        constexpr float kLeast = 1.17549435e-38f;  // 2^-126
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(
+                            fmaxf(x0 - __uint_as_float(u0), fminf(x0, kLeast)), fmaxf(x1 - __uint_as_float(u1), fminf(x1, kLeast)));
+                        pt[b][e] = transpose_8x8(u0 >> 16 | u1);
+                        pt_lo[b][e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
                     }
                 }
 #pragma unroll
@@ -334,7 +342,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     const int chunk = 2 * n + v_chunk;
                     ldmatrix_x4_trans(vs + (chunk >> 3) * block_stride + v_key * 128 + (((chunk & 7) ^ (v_key & 7)) << 4), vf);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) mma_16816(o[n][b], vf, pt[b][0], pt[b][1]);
+                    for (int b = 0; b < NB; ++b) {
+                        mma_16816(o[n][b], vf, pt[b][0], pt[b][1]);
+                        mma_16816(o[n][b], vf, pt_lo[b][0], pt_lo[b][1]);
+                    }
                 }
             }
             __syncwarp();

@@ -286,8 +286,9 @@ int q4k_cache_append(const q4k_cache* c, int layer, const int32_t* seqs, int n, 
  *   scale   > 0, finite; window, sinks >= 0 (sinks is ignored with window 0)
  *   ws      see q4k_cache_workspace; ws_bytes its size
  * heads/kv_heads <= 128; 1 <= n <= 4096; 1 <= tokens < 2^31 / heads.
- * Accumulates in fp32; the weights a_j are rounded to bf16 for the product
- * with V, as V is bf16 itself. The result does not depend on timing.
+ * Accumulates in fp32; for the product with V the weights a_j are rounded to
+ * bf16, or, with max_new * heads/kv_heads <= 16, to the sum of two bf16. The
+ * result does not depend on timing.
  */
 int q4k_cache_attention(const q4k_cache* c, int layer, const int32_t* seqs, int n,
                         const int32_t* starts, int64_t tokens, const uint16_t* Q, uint16_t* out,
