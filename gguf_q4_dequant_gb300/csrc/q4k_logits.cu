@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kPickThreads, 3)
             }
             if (has_bias) y = __fadd_rn(y, bias);
             if (!ok) y = -INFINITY;
+            any |= ok;  // (a token in a group that the row fills in part is seen as allowed only here)
             best.take(y, v);
             return y;
         };

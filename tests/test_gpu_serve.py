@@ -846,3 +846,35 @@ def test_pick_many_adjusted_tokens(q4k, V, seen, biased):
         for alias in (False, True):
             out, got = pick_run(q4k, x, hist, pen, bias, ok, alias=alias)
             assert np.array_equal(got, best) and np.array_equal(out, y.astype(np.float32))
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 6, 7, 8, 23, 41, 42, 4097, 9003])
+def test_pick_of_a_sole_allowed_token_at_the_ends_of_a_row(q4k, V):
+    """One allowed token among the row's first or last four (in a group of four that the row fills in part, for most V
+    and rows), in the history, biased or both, adjusted to -infinity or NaN: it is the pick, as no other is allowed."""
+    inf = float("inf")
+    # (the logit, in the history, presence penalty, bias): -inf, -inf, NaN, NaN, NaN, -inf, and a number
+    forms = [(1.0, False, 0.0, -inf), (1.0, True, inf, None), (inf, False, 0.0, -inf), (inf, True, inf, None),
+             (-inf, True, 0.0, inf), (-inf, True, 0.5, 2.0), (1.0, True, 0.5, 3.0)]
+    ends = sorted({v for v in (*range(4), *range(V - 4, V)) if 0 <= v < V})
+    rows = [(v, *f) for f in forms for v in ends]
+    rows = [r for r in rows for _ in range(2)]  # (an even number of each, so that V = 2 has both offsets)
+    x = np.random.default_rng(V).integers(-40, 41, (len(rows), V)).astype(np.float32)
+    allowed = np.zeros(x.shape, bool)
+    hist, pen, bias = [], [], []
+    for m, (v, logit, listed, presence, b) in enumerate(rows):
+        x[m, v] = logit
+        allowed[m, v] = True
+        hist.append([v] if listed else [])
+        pen.append([1.0, presence, 0.0])
+        bias.append([] if b is None else [(v, b)])
+    sole = [r[0] for r in rows]
+    for keep, alias in ((True, False), (False, False), (True, True)):
+        out, got = pick_run(q4k, x, hist, pen, bias, allowed, keep=keep, alias=alias)
+        assert got.tolist() == sole
+        if out is not None:
+            with np.errstate(invalid="ignore"):
+                y, _, _ = pick_ref(x, hist, pen, bias, allowed)
+            assert np.array_equal(out, y.astype(np.float32), equal_nan=True)
+    none = np.zeros(x.shape, bool)
+    assert set(pick_run(q4k, x, hist, pen, bias, none)[1].tolist()) == {-1}
