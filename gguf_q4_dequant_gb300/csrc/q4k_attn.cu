@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!tile_is_full<KT>(tile, h0, h1, p.window, p.sinks)) {
                     // columns of this tile that the row sees: [0, sink) and (low, high], as 32 bits per block
                     const int j0 = tile * KT, high = pos - j0;
-                    const int low = p.window > 0 ? max(pos - p.window, -1) - j0 : -1;
+                    const int low = p.window > 0 ? max(max(pos, 0) - p.window, -1) - j0 : -1;
                     const int sink = p.window > 0 ? p.sinks - j0 : 0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {

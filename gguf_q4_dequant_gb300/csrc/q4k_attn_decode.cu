@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const int j0 = cur.keys.tile(i) * KT + 16 * warp;
             if (!__all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, phase, p.err))) return;
             const uint32_t ks = sbase + slot * Cfg::kStageBytes + slice, vs = ks + Cfg::kTileBytes;
-            const bool none = j0 > p1 || (p.window > 0 && j0 + 15 <= cur.p0 - p.window && j0 >= p.sinks);
+            // (positions below 0 see nothing; less a large window they would pass -2^31)
+            const bool none = j0 > p1 || (p.window > 0 && j0 + 15 <= max(cur.p0, 0) - p.window && j0 >= p.sinks);
             if (!none) {
                 // scores: one block of rows in two chains of products, added at the end
                 float s[NB][4], s1[NB][4];

@@ -878,3 +878,13 @@ def test_pick_of_a_sole_allowed_token_at_the_ends_of_a_row(q4k, V):
             assert np.array_equal(out, y.astype(np.float32), equal_nan=True)
     none = np.zeros(x.shape, bool)
     assert set(pick_run(q4k, x, hist, pen, bias, none)[1].tolist()) == {-1}
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 4, (1 << 31) - 40])
+@pytest.mark.parametrize("max_new", [8, 100])
+def test_largest_windows_with_more_new_tokens_than_positions(q4k, window, max_new):
+    """Positions below 0 less a window near 2^31 lie below -2^31."""
+    lens, news = [5, 40, 1, 129], [8, 3, 8, 60]
+    cache = make_cache(q4k, lens, 16, 2, 128, fill=float("nan"))
+    check_attention(q4k, cache, [0, 1, 2, 3], news, 4, window=window, max_new=max_new)
+    check_attention(q4k, cache, [0, 1, 2, 3], news, 4, window=window, sinks=2, max_new=max_new)
