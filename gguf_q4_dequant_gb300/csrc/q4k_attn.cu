@@ -79,7 +79,7 @@ struct ChunkCfg {
     static constexpr int kMiscBytes = 144 + kItemRing * sizeof(AttnItem);
     static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;  // + alignment slack
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(kMaxBatch * 4 <= kRing * kTileBytes, "the plan's scratch is the ring");
+    static_assert(kMaxBatch * 8 <= kRing * kTileBytes, "the plan's scratch is the ring");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kColS = 0, kColO = 256;        // S (and P) 2 x 128, O 2 x D
     static constexpr int kPartFloats = (D + 2) * 128;        // a partial result of one half
@@ -94,7 +94,8 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <int D>
+// U: what units of work are counted in.
+template <int D, typename U>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     q4k_attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_q,
                           const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -119,12 +120,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t b_ifull = b_fin + 8;
     const uint32_t b_iempty = b_ifull + 8 * kItemRing;
     const uint32_t b_vclean = b_iempty + 8 * kItemRing;
-    AttnWalk* walk_s = reinterpret_cast<AttnWalk*>(smem + Cfg::kOffMisc);
+    AttnWalk<U>* walk_s = reinterpret_cast<AttnWalk<U>*>(smem + Cfg::kOffMisc);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 96);
     volatile int* poison = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 112);  // [4] item tags
     volatile int* last_s = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 128);  // [2]
     AttnItem* items = reinterpret_cast<AttnItem*>(smem + Cfg::kOffMisc + 144);
-    static_assert(sizeof(AttnWalk) <= 96 && sizeof(AttnItem) % 8 == 0, "layout");
+    static_assert(sizeof(AttnWalk<U>) <= 96 && Cfg::kOffMisc % 8 == 0 && sizeof(AttnItem) % 8 == 0, "layout");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     pdl_wait();
     const int tph = 128 / p.group, tt = 2 * tph;  // tokens per half and per item
     if (p.b.n > 32) {
-        plan_block<KT>(p, tt, kChunkCost, reinterpret_cast<uint32_t*>(smem + Cfg::kOffRing), walk_s);
+        plan_block<KT, U>(p, tt, kChunkCost, reinterpret_cast<U*>(smem + Cfg::kOffRing), walk_s);
         fence_proxy_async_smem();  // the plan's scratch (generic accesses) becomes the ring (TMA writes)
     }
     tc_fence_before();
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         regs_dec<kOtherRegs>();
         if (warp == 8) {
             // ------------------------------------------------ TMA producer ---
-            AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kChunkCost);
+            AttnWalk<U> w = p.b.n > 32 ? *walk_s : plan_warp<KT, U>(p, tt, kChunkCost);
             AttnItem it{};
             PageIds ids;
             int slot = 0, n_items = 0, issued = 0;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 return true;
             };
             for (;;) {
-                const bool more = next_item<KT>(p, w, tt, kChunkCost, it);
+                const bool more = next_item<KT, U>(p, w, tt, kChunkCost, it);
                 const int k = n_items % kItemRing;
                 ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
                 if (!ok) break;
@@ -675,7 +676,9 @@ static cudaError_t launch_chunk(const AttnParams& p, const AttnArgs& a, cudaStre
     if (!encode_q(&mq, a, p.b.tokens, p.group) || !encode_pages(&mk, p.c.k, p.c, D, 1) ||
         !encode_pages(&mv, p.c.v, p.c, D, 1))
         return cudaErrorInvalidValue;
-    return launch_serve(q4k_attn_chunk_kernel<D>, dim3(dev.num_sms), dim3(kChunkThreads), ChunkCfg<D>::kSmem, stream,
+    auto kernel = count_wide(p, 2 * (128 / p.group), kChunkKeys, kChunkCost) ? q4k_attn_chunk_kernel<D, uint64_t>
+                                                                             : q4k_attn_chunk_kernel<D, uint32_t>;
+    return launch_serve(kernel, dim3(dev.num_sms), dim3(kChunkThreads), ChunkCfg<D>::kSmem, stream,
                         pdl, 1, p, mq, mk, mv);
 }
 
@@ -710,11 +713,14 @@ cudaError_t attn_setup(DeviceInfo& dev) {
     if (2 * dev.num_sms > kPageTicket) return cudaErrorInvalidValue;  // counters of the workspace
     cudaError_t e = attn_decode_setup();
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(q4k_attn_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         ChunkCfg<64>::kSmem);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(q4k_attn_chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                ChunkCfg<128>::kSmem);
+    cudaError_t r;
+#define Q4K_SET(D, U)                                                                                     \
+    if ((r = cudaFuncSetAttribute(q4k_attn_chunk_kernel<D, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+                                  ChunkCfg<D>::kSmem)) != cudaSuccess)                                    \
+        e = r;
+    Q4K_SET(64, uint32_t) Q4K_SET(64, uint64_t) Q4K_SET(128, uint32_t) Q4K_SET(128, uint64_t)
+#undef Q4K_SET
+    return e;
 }
 
 }  // namespace q4k

@@ -6,8 +6,11 @@
 // sequences, kv heads and row tiles are numbered in that order, and CTA c of
 // the grid takes about units [c*q, (c+1)*q) with q = ceil(total / grid). So every
 // CTA has about the same number of key tiles whatever the sequences' lengths
-// are, on the device's own numbers. (Units are counted in 32 bits: a step of
-// more than 2^32 key tiles of at least 16 x 128 x 64 products would take hours.)
+// are, on the device's own numbers. Units are counted in 32 bits (U) unless the
+// step may have 2^32 of them, as a prompt of two million tokens with 8 query heads
+// for each of 8 kv heads has (some 40 s of work): then in 64. Counting in 64 always
+// cost 0.7 us at one token (11.0 for 10.3 in a stream) and 2 % of a prompt chunk.
+// Those of one row tile fit 24 bits.
 // A row tile that lies in several CTAs' ranges is put
 // together from their partial results by whichever of them finishes last, in
 // the order of the CTAs: the result does not depend on which one that is.
@@ -101,16 +104,17 @@ struct AttnItem {
 // through a small ring in shared memory; an item without key tiles is the end.
 constexpr int kItemRing = 4;
 
+template <typename U>
 struct AttnWalk {
-    uint32_t u, u_end;  // units left to do
-    uint32_t q;
+    U u, u_end;  // units left to do
+    U q;
     int b, h, tile, off;
     SeqView s;
 };
 
 // The next item, or false. `tt`: tokens of a row tile.
-template <int KT>
-__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int tt, AttnCost cost, AttnItem& it) {
+template <int KT, typename U>
+__device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk<U>& w, int tt, AttnCost cost, AttnItem& it) {
     it.i0 = it.i1 = 0;
     if (w.u >= w.u_end) return false;
     while (w.tile * tt >= w.s.m) {  // the sequence's row tiles are done for this head
@@ -127,7 +131,7 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, AttnWalk& w, int 
     it.row = w.s.row;
     it.len = w.s.len;
     it.keys = key_tiles<KT>(it.p0, it.p0 + it.tokens - 1, p.window, p.sinks);
-    const uint32_t u0 = w.u - w.off, u1 = u0 + cost.item + it.keys.n;  // the row tile's units
+    const U u0 = w.u - w.off, u1 = u0 + cost.item + it.keys.n;  // the row tile's units
     it.i0 = w.off > 0 ? w.off - cost.item : 0;
     it.i1 = w.u_end < u1 ? static_cast<int>(w.u_end - u0) - cost.item : it.keys.n;
     it.first = it.last = blockIdx.x;
@@ -148,36 +152,46 @@ __device__ __forceinline__ int tile_units(const AttnParams& p, const SeqView& s,
     return cost.item + key_tiles<KT>(p0, p0 + min(tt, s.m - tile * tt) - 1, p.window, p.sinks).n;
 }
 
+template <typename U>
 struct AttnCut {
-    uint32_t u;        // the boundary, moved
+    U u;               // the boundary, moved
     int b, h, tile, off;  // where it lies (off > 0: inside the row tile)
     SeqView s;
 };
 
 // Inclusive sum over the lanes of a warp.
-__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
+template <typename U>
+__device__ __forceinline__ U warp_scan(U x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, x, k);
+        const U v = __shfl_up_sync(0xffffffffu, x, k);
         if (lane >= k) x += v;
     }
     return x;
 }
 
+// Sum over the lanes of a warp.
+__device__ __forceinline__ uint32_t warp_sum(uint32_t x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+    return x;
+}
+
 // By one warp: where unit u of the step lies in sequence b, which has per_head
 // units per kv head from unit `at` on.
-template <int KT>
-__device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, const SeqView& s, uint32_t per_head,
-                                          uint32_t at, uint32_t u, AttnCost cost) {
+template <int KT, typename U>
+__device__ __forceinline__ AttnCut<U> cut_in(const AttnParams& p, int tt, int b, const SeqView& s, U per_head, U at, U u,
+                                             AttnCost cost) {
     const int lane = threadIdx.x & 31;
-    AttnCut c;
+    AttnCut<U> c;
     c.b = b;
     c.s = s;
     c.tile = 0;
     c.h = static_cast<int>((u - at) / per_head);
-    uint32_t rest = (u - at) - c.h * per_head;
-    int n = per_head;
+    U rest = (u - at) - c.h * per_head;
+    int n = static_cast<int>(per_head);  // (of the row tile that is cut, if the sequence has only one)
     if (s.m > tt) {
         for (int t0 = 0; t0 < (s.m + tt - 1) / tt; t0 += 32) {
             const int t = t0 + lane;
@@ -208,10 +222,10 @@ __device__ __forceinline__ AttnCut cut_in(const AttnParams& p, int tt, int b, co
 }
 
 // By one warp: units per kv head of the lanes' sequences.
-template <int KT>
-__device__ __forceinline__ uint32_t lane_units(const AttnParams& p, int tt, const SeqView& s, AttnCost cost) {
+template <int KT, typename U>
+__device__ __forceinline__ U lane_units(const AttnParams& p, int tt, const SeqView& s, AttnCost cost) {
     const int lane = threadIdx.x & 31, tiles = (s.m + tt - 1) / tt;
-    uint32_t u = 0;
+    U u = 0;
     if (tiles <= 4)
         for (int t = 0; t < tiles; ++t) u += tile_units<KT>(p, s, t, tt, cost);
     // many row tiles: the warp counts them together
@@ -223,83 +237,83 @@ __device__ __forceinline__ uint32_t lane_units(const AttnParams& p, int tt, cons
         o.m = __shfl_sync(0xffffffffu, s.m, l);
         o.len = __shfl_sync(0xffffffffu, s.len, l);
         const int ot = (o.m + tt - 1) / tt;
-        uint32_t x = 0;
+        U x = 0;
         for (int t = lane; t < ot; t += 32) x += tile_units<KT>(p, o, t, tt, cost);
-        x = __reduce_add_sync(0xffffffffu, x);
+        x = warp_sum(x);
         if (lane == l) u = x;
     }
     return u;
 }
 
 // The CTA's range by one warp, for at most 32 sequences.
-template <int KT>
-__device__ __forceinline__ AttnWalk plan_warp(const AttnParams& p, int tt, AttnCost cost) {
+template <int KT, typename U>
+__device__ __forceinline__ AttnWalk<U> plan_warp(const AttnParams& p, int tt, AttnCost cost) {
     const int lane = threadIdx.x & 31;
     SeqView s{0, 0, 0, 0};
     if (lane < p.b.n) s = seq_view(p.c, p.b, lane);
-    const uint32_t per_head = lane_units<KT>(p, tt, s, cost), mine = per_head * p.c.kv_heads;
-    const uint32_t incl = p.b.n > 1 ? warp_scan(mine) : __shfl_sync(0xffffffffu, mine, 0);
-    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
-    AttnWalk w;
-    w.q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(cost.q_min));
+    const U per_head = lane_units<KT, U>(p, tt, s, cost), mine = per_head * p.c.kv_heads;
+    const U incl = p.b.n > 1 ? warp_scan(mine) : __shfl_sync(0xffffffffu, mine, 0);
+    const U total = __shfl_sync(0xffffffffu, incl, 31);
+    AttnWalk<U> w;
+    w.q = max((total + gridDim.x - 1) / gridDim.x, static_cast<U>(cost.q_min));
     w.u = w.u_end = total;
     w.b = w.h = w.tile = w.off = 0;
     w.s = SeqView{0, 0, 0, 0};
-    auto cut = [&](uint32_t u) {
+    auto cut = [&](U u) {
         const int l = __ffs(__ballot_sync(0xffffffffu, incl > u)) - 1;
         SeqView o;
         o.t0 = __shfl_sync(0xffffffffu, s.t0, l);
         o.m = __shfl_sync(0xffffffffu, s.m, l);
         o.len = __shfl_sync(0xffffffffu, s.len, l);
         o.row = __shfl_sync(0xffffffffu, s.row, l);
-        return cut_in<KT>(p, tt, l, o, __shfl_sync(0xffffffffu, per_head, l), __shfl_sync(0xffffffffu, incl - mine, l), u, cost);
+        return cut_in<KT, U>(p, tt, l, o, __shfl_sync(0xffffffffu, per_head, l), __shfl_sync(0xffffffffu, incl - mine, l), u, cost);
     };
     const uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * w.q, u1 = u0 + w.q;
     if (u0 < total) {
-        const AttnCut c = cut(static_cast<uint32_t>(u0));
+        const AttnCut<U> c = cut(static_cast<U>(u0));
         w.u = c.u;
         w.b = c.b;
         w.h = c.h;
         w.tile = c.tile;
         w.off = c.off;
         w.s = c.s;
-        if (u1 < total) w.u_end = cut(static_cast<uint32_t>(u1)).u;
+        if (u1 < total) w.u_end = cut(static_cast<U>(u1)).u;
     }
     return w;
 }
 
 // The same by all threads of the block, for any number of sequences: `units`
-// holds n words of shared memory, `found` takes the result. Ends with
+// holds n counts in shared memory, `found` takes the result. Ends with
 // __syncthreads().
-template <int KT>
-__device__ __forceinline__ void plan_block(const AttnParams& p, int tt, AttnCost cost, uint32_t* units,
-                                           AttnWalk* found) {
+template <int KT, typename U>
+__device__ __forceinline__ void plan_block(const AttnParams& p, int tt, AttnCost cost, U* units,
+                                           AttnWalk<U>* found) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     for (int i0 = warp * 32; i0 < p.b.n; i0 += nwarps * 32) {
         const int i = i0 + lane;
         SeqView s{0, 0, 0, 0};
         if (i < p.b.n) s = seq_view(p.c, p.b, i);
-        const uint32_t u = lane_units<KT>(p, tt, s, cost);
+        const U u = lane_units<KT, U>(p, tt, s, cost);
         if (i < p.b.n) units[i] = u * p.c.kv_heads;
     }
     __syncthreads();
     // warp 0 finds where the range begins, warp 1 where it ends
     if (warp < 2) {
-        uint32_t total = 0;
+        U total = 0;
         for (int i = lane; i < p.b.n; i += 32) total += units[i];
-        total = __reduce_add_sync(0xffffffffu, total);
-        const uint32_t q = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(cost.q_min));
+        total = warp_sum(total);
+        const U q = max((total + gridDim.x - 1) / gridDim.x, static_cast<U>(cost.q_min));
         const uint64_t u64 = static_cast<uint64_t>(blockIdx.x + warp) * q;
-        AttnCut c;
+        AttnCut<U> c;
         c.u = total;
         c.b = c.h = c.tile = c.off = 0;
         c.s = SeqView{0, 0, 0, 0};
         if (u64 < total) {
-            const uint32_t u = static_cast<uint32_t>(u64);
-            uint32_t at = 0;
+            const U u = static_cast<U>(u64);
+            U at = 0;
             int b = 0;
             for (int i0 = 0; i0 < p.b.n; i0 += 32) {
-                const uint32_t mine = i0 + lane < p.b.n ? units[i0 + lane] : 0, incl = warp_scan(mine);
+                const U mine = i0 + lane < p.b.n ? units[i0 + lane] : 0, incl = warp_scan(mine);
                 const uint32_t past = __ballot_sync(0xffffffffu, at + incl > u);
                 if (past) {
                     const int l = __ffs(past) - 1;
@@ -309,7 +323,7 @@ __device__ __forceinline__ void plan_block(const AttnParams& p, int tt, AttnCost
                 }
                 at += __shfl_sync(0xffffffffu, incl, 31);
             }
-            c = cut_in<KT>(p, tt, b, seq_view(p.c, p.b, b), units[b] / p.c.kv_heads, at, u, cost);
+            c = cut_in<KT, U>(p, tt, b, seq_view(p.c, p.b, b), units[b] / p.c.kv_heads, at, u, cost);
         }
         if (lane == 0) {
             if (warp == 0) {
@@ -339,6 +353,16 @@ inline bool encode_pages(CUtensorMap* map, const uint16_t* base, const CacheLaye
                                  static_cast<uint64_t>(c.page_stride) * 2};
     const uint32_t box[5] = {64, static_cast<uint32_t>(page), static_cast<uint32_t>(blocks), 1, 1};
     return encode_bf16_sw128(map, base, 5, dims, strides, box);
+}
+
+// Whether units are to be counted in 64 bits: the step has fewer than 2^32 (and the
+// grid's rounding) if every sequence may have all the tokens, as offsets that make no
+// sense may say, and every row tile (of tt tokens) all the key tiles that the
+// table has room for.
+inline bool count_wide(const AttnParams& p, int tt, int keys, AttnCost cost) {
+    const double row_tiles = static_cast<double>(p.b.n) * (p.b.tokens / tt + 1) * p.c.kv_heads;
+    const int key_tiles = ((p.c.width << p.c.page_shift) + keys - 1) / keys;
+    return row_tiles * (key_tiles + cost.item) > 4.2e9;
 }
 
 // The kernel for few rows per kv head: `rows` <= 16 of them in a row tile (group <= rows).

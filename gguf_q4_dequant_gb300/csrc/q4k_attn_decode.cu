@@ -45,7 +45,7 @@ struct DecodeCfg {
     static constexpr int kOffMisc = kOffBar + 8 * (2 * kRing + 2 + 2 * kItemRing);
     static constexpr int kSmem = kOffMisc + 112 + kItemRing * sizeof(AttnItem) + 1024;
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(kMaxBatch * 4 <= kRing * kStageBytes, "the plan's scratch is the ring");
+    static_assert(kMaxBatch * 8 <= kRing * kStageBytes, "the plan's scratch is the ring");
     static constexpr int kPartFloats = 16 * (D + 2);
 };
 
@@ -76,8 +76,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
-// NB: blocks of 8 rows in a row tile.
-template <int D, int NB>
+// NB: blocks of 8 rows in a row tile. U: what units of work are counted in.
+template <int D, int NB, typename U>
 __global__ void __launch_bounds__(kDecThreads, 1)
     q4k_attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_v) {
@@ -95,10 +95,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint32_t b_join = b_empty + 8 * R;
     const uint32_t b_ifull = b_join + 8;
     const uint32_t b_iempty = b_ifull + 8 * kItemRing;
-    AttnWalk* walk_s = reinterpret_cast<AttnWalk*>(smem + Cfg::kOffMisc);
+    AttnWalk<U>* walk_s = reinterpret_cast<AttnWalk<U>*>(smem + Cfg::kOffMisc);
     volatile int* last_s = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 96);
     AttnItem* items = reinterpret_cast<AttnItem*>(smem + Cfg::kOffMisc + 112);
-    static_assert(sizeof(AttnWalk) <= 96 && sizeof(AttnItem) % 8 == 0, "layout");
+    static_assert(sizeof(AttnWalk<U>) <= 96 && Cfg::kOffMisc % 8 == 0 && sizeof(AttnItem) % 8 == 0, "layout");
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(b_full + 8 * i, 1);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     pdl_wait();
     const int tt = 8 * NB / p.group;  // tokens of a row tile
     if (p.b.n > 32) {
-        plan_block<KT>(p, tt, kDecCost, reinterpret_cast<uint32_t*>(smem), walk_s);
+        plan_block<KT, U>(p, tt, kDecCost, reinterpret_cast<U*>(smem), walk_s);
         fence_proxy_async_smem();  // the plan's scratch becomes the ring
     }
     __syncthreads();
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     if (warp == kDecWarps) {
         // ---------------------------------------------------- TMA producer ---
-        AttnWalk w = p.b.n > 32 ? *walk_s : plan_warp<KT>(p, tt, kDecCost);
+        AttnWalk<U> w = p.b.n > 32 ? *walk_s : plan_warp<KT, U>(p, tt, kDecCost);
         AttnItem it{};
         PageIds ids;
         int slot = 0, issued = 0;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int pages = KT >> p.c.page_shift;
         const uint32_t page_bytes = static_cast<uint32_t>(page) * D * 2;
         for (int n_items = 0; ok; ++n_items) {
-            const bool more = next_item<KT>(p, w, tt, kDecCost, it);
+            const bool more = next_item<KT, U>(p, w, tt, kDecCost, it);
             const int k = n_items % kItemRing;
             ok = __all_sync(0xffffffffu, mbar_wait(b_iempty + 8 * k, ((n_items / kItemRing) & 1) ^ 1, p.err));
             if (!ok) break;
@@ -494,7 +494,11 @@ static cudaError_t launch_d(const AttnParams& p, int rows, cudaStream_t stream, 
     CUtensorMap mk, mv;
     if (!encode_pages(&mk, p.c.k, p.c, D, D / 64) || !encode_pages(&mv, p.c.v, p.c, D, D / 64))
         return cudaErrorInvalidValue;
-    return launch_serve(rows <= 8 ? q4k_attn_decode_kernel<D, 1> : q4k_attn_decode_kernel<D, 2>, dim3(dev.num_sms),
+    const int blocks = rows <= 8 ? 1 : 2;
+    const bool wide = count_wide(p, 8 * blocks / p.group, kDecKeys, kDecCost);
+    auto kernel = blocks == 1 ? (wide ? q4k_attn_decode_kernel<D, 1, uint64_t> : q4k_attn_decode_kernel<D, 1, uint32_t>)
+                              : (wide ? q4k_attn_decode_kernel<D, 2, uint64_t> : q4k_attn_decode_kernel<D, 2, uint32_t>);
+    return launch_serve(kernel, dim3(dev.num_sms),
                         dim3(kDecThreads), DecodeCfg<D>::kSmem, stream, pdl, 1, p, mk, mv);
 }
 
@@ -505,11 +509,12 @@ cudaError_t launch_attn_decode(const AttnParams& p, int rows, int head_dim, cuda
 
 cudaError_t attn_decode_setup() {
     cudaError_t e = cudaSuccess, r;
-#define Q4K_SET(D, NB)                                                                                      \
-    if ((r = cudaFuncSetAttribute(q4k_attn_decode_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                                  DecodeCfg<D>::kSmem)) != cudaSuccess)                                     \
+#define Q4K_SET(D, NB, U)                                                                                      \
+    if ((r = cudaFuncSetAttribute(q4k_attn_decode_kernel<D, NB, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+                                  DecodeCfg<D>::kSmem)) != cudaSuccess)                                        \
         e = r;
-    Q4K_SET(64, 1) Q4K_SET(64, 2) Q4K_SET(128, 1) Q4K_SET(128, 2)
+    Q4K_SET(64, 1, uint32_t) Q4K_SET(64, 2, uint32_t) Q4K_SET(128, 1, uint32_t) Q4K_SET(128, 2, uint32_t)
+    Q4K_SET(64, 1, uint64_t) Q4K_SET(64, 2, uint64_t) Q4K_SET(128, 1, uint64_t) Q4K_SET(128, 2, uint64_t)
 #undef Q4K_SET
     return e;
 }
