@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(app_threads(kWide), kWide ? 1 : 4)
             }
         }
         if (kWide) {
-            // values after keys, as the other width's threads write them one after
-            // the other: what a cache of one tensor for both holds is then the values
+            // values after keys: what a cache of one tensor for both holds is then the
+            // values (in the other width no order holds between a key and its value)
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < kAppRows; ++e) {
@@ -174,7 +174,10 @@ cudaError_t launch_append(const CacheLayer& c, const Batch& b, const float* Yq, 
                           const float* Yv, uint16_t* q_out, int heads, int head_dim, const float* rope,
                           int pairs, const float* q_norm, const float* k_norm, float eps,
                           cudaStream_t stream, const DeviceInfo& dev, int pdl) {
-    const bool wide = b.tokens <= dev.num_sms;
+    // A cache of one tensor for K and V takes the width that writes the values last.
+    // (To leave its keys unwritten instead costs the others: 2894 tokens of 56 rows
+    // with norm 28.1 us for 27.6.)
+    const bool wide = b.tokens <= dev.num_sms || c.k == c.v;
     auto launch = head_dim == 64 ? (wide ? launch_d<64, true> : launch_d<64, false>)
                                  : (wide ? launch_d<128, true> : launch_d<128, false>);
     return launch(c, b, Yq, Yk, Yv, q_out, heads, rope, pairs, q_norm, k_norm, eps, stream, pdl);

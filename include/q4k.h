@@ -219,8 +219,8 @@ int q4k_selftest_timeout(int64_t limit_ns, void* stream);
  * lens - m + r.
  */
 typedef struct q4k_cache {
-    uint16_t* k;           /* device, bf16 bit patterns, 16-byte aligned */
-    uint16_t* v;
+    uint16_t* k;           /* device, bf16 bit patterns, 16-byte aligned; K and V must not */
+    uint16_t* v;           /* overlap, unless k == v: what is stored then is the values */
     int64_t layer_stride;  /* elements; multiples of 8; layers and pages must not overlap */
     int64_t page_stride;
     int32_t* refs;         /* device, [n_pages] */

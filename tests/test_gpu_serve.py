@@ -888,3 +888,27 @@ def test_largest_windows_with_more_new_tokens_than_positions(q4k, window, max_ne
     cache = make_cache(q4k, lens, 16, 2, 128, fill=float("nan"))
     check_attention(q4k, cache, [0, 1, 2, 3], news, 4, window=window, max_new=max_new)
     check_attention(q4k, cache, [0, 1, 2, 3], news, 4, window=window, sinks=2, max_new=max_new)
+
+
+@pytest.mark.parametrize("T", [1, 37, 700])
+@pytest.mark.parametrize("dim,kv,pairs,norm", [(64, 8, 0, False), (64, 1, 2, True), (64, 16, 1, False), (128, 4, 0, True),
+                                               (128, 8, 2, False), (128, 3, 1, True)])
+def test_append_to_a_cache_of_one_tensor(q4k, T, dim, kv, pairs, norm):
+    """K and V the same tensor, in steps of few and of many tokens: the values remain, in every row."""
+    page, heads = 32, 2 * kv
+    c = make_cache(q4k, [T + 5], page, kv, dim)
+    cache = q4k.Cache(c.k, c.k, c.refs, c.table, c.lens)
+    Y = [torch.randn(T, h * dim, device=DEV) for h in (heads, kv, kv)]
+    rope = torch.rand(c.table.shape[1] * page, dim, device=DEV)
+    w = torch.rand(dim, device=DEV) + 0.5 if norm else None
+    q_out = torch.empty(T, heads, dim, dtype=torch.bfloat16, device=DEV)
+    at = torch.arange(5, T + 5, device=DEV)
+    want = c.k.clone()
+    want[0, c.table[0, at // page].long(), :, at % page] = Y[2].view(T, kv, dim).to(torch.bfloat16)
+    for _ in range(3):
+        cache.k.fill_(7.0)
+        q4k.q4k_cache_append(cache, 0, None, ints([0, T]), *Y, q_out, heads, rope, pairs, w, w)
+        torch.cuda.synchronize()
+        rows = c.table[0, at // page].long(), at % page
+        assert torch.equal(cache.k[0][rows[0], :, rows[1]], want[0][rows[0], :, rows[1]])
+        assert int((cache.k != 7.0).flatten(2).any(2).sum()) <= c.table.shape[1]
