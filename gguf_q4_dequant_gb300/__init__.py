@@ -487,10 +487,11 @@ def q4k_logits_pick(logits, M: int, V: int, out=None, pick=None, history=None, h
     f32, i32 = torch.float32, torch.int32
     if not isinstance(mask, (int, type(None))) and mask.dtype == torch.uint32:
         mask = mask.view(i32)
+    biases = 0 if isinstance(bias_ids, (int, type(None))) else bias_ids.numel()  # a value is read for each
     _check(lib().q4k_logits_pick(
         _tensor(logits, f32, M * V, "logits"), M, V, _tensor(out, f32, M * V, "out"),
         _tensor(pick, torch.int64, M, "pick"), _tensor(history, i32, 0, "history") or None,
         _tensor(hist_starts, i32, M + 1, "hist_starts"), _tensor(penalties, f32, 3 * M, "penalties"),
-        _tensor(bias_ids, i32, 0, "bias_ids") or None, _tensor(bias, f32, 0, "bias"),
+        _tensor(bias_ids, i32, 0, "bias_ids") or None, _tensor(bias, f32, biases, "bias"),
         _tensor(bias_starts, i32, M + 1, "bias_starts"), _tensor(mask, i32, M * ((V + 31) // 32), "mask"),
         _stream(stream)), "q4k_logits_pick")

@@ -141,3 +141,40 @@ def test_binding_refusals(q4k):
         q4k.q4k_logits_pick(x, 3, 10, x)
     with pytest.raises(ValueError, match="must be torch.float32"):
         q4k.q4k_logits_pick(x.double(), 2, 10, x)
+
+
+class Tensor:
+    """Stands for a CUDA tensor: what the binding looks at."""
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape, self.is_cuda = dtype, shape, True
+
+    def numel(self):
+        n = 1
+        for d in self.shape:
+            n *= d
+        return n
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("ids,values,refused", [(5, 4, True), (5, 0, True), (1, 0, True), (5, 5, None), (5, 6, None)])
+def test_pick_refuses_fewer_biases_than_ids(q4k, ids, values, refused):
+    """Every id's value is read, so there must be one for each."""
+    torch = pytest.importorskip("torch")
+    i32, f32 = torch.int32, torch.float32
+    call = lambda: q4k.q4k_logits_pick(  # noqa: E731
+        A, 0, 10, A, A, bias_ids=Tensor(i32, ids), bias=Tensor(f32, values), bias_starts=A, stream=0)
+    if refused:
+        with pytest.raises(ValueError, match="bias holds"):
+            call()
+    else:
+        with pytest.raises(q4k.Q4KError, match="Q4K_ERR_BAD_DIM"):  # (M = 0: nothing is launched)
+            call()
