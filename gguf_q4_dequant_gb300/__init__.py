@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI declared in ``include/q4k.h``. The functions mirror
 the C names and take torch tensors (device memory, caller-owned) or raw device
-pointers (ints). There is no fallback: if ``libq4k.so`` has not been built, or
-a call fails, a ``Q4KError`` is raised.
+pointers (ints; an array that a count is taken from, as the step's ``starts`` or
+sequences to free, has to be a tensor). There is no fallback: if ``libq4k.so``
+has not been built, or a call fails, a ``Q4KError`` is raised.
 """
 from __future__ import annotations
 
@@ -397,6 +398,19 @@ def _step(seqs, starts):
     return _tensor(seqs, torch.int32, n, "seqs"), n, _tensor(starts, torch.int32, n + 1, "starts")
 
 
+def _count(t, name):
+    if isinstance(t, int):
+        raise ValueError(f"{name} must be a tensor, its entries are counted")
+    return t.numel()
+
+
+def _workspace(cache, ws, uint8):
+    """(address, bytes) of a workspace; an address is taken to have the bytes that the calls need."""
+    if ws is None or isinstance(ws, int):
+        return ws, q4k_cache_workspace(cache) if ws else 0
+    return _tensor(ws, uint8, 0, "workspace"), ws.numel()
+
+
 def q4k_cache_append(cache: Cache, layer: int, seqs, starts, Yq, Yk, Yv, q_out, heads: int, rope=None,
                      pairs: int = 0, q_norm=None, k_norm=None, eps: float = 1e-6, stream=None):
     """A step's keys and values into the pages of a layer, its queries to q_out [tokens, heads, head_dim]
@@ -408,7 +422,9 @@ def q4k_cache_append(cache: Cache, layer: int, seqs, starts, Yq, Yk, Yv, q_out, 
         raise ValueError("Yq must be a tensor of a row per token")
     tokens = Yq.shape[0]
     rows = 0
-    if rope is not None:
+    if isinstance(rope, int):  # taken to have a row for every position
+        rows = cache.table.shape[1] * cache.k.shape[3]
+    elif rope is not None:
         rows = rope.shape[0]
         if rope.numel() != rows * D:
             raise ValueError("rope must be [rows, head_dim]")
@@ -432,8 +448,7 @@ def q4k_cache_attention(cache: Cache, layer: int, seqs, starts, Q, out, heads: i
     _check(lib().q4k_cache_attention(
         cache._ref, layer, s, n, st, tokens, _tensor(Q, torch.bfloat16, need, "Q"),
         _tensor(out, torch.bfloat16, need, "out"), heads, max_new, scale, window, sinks,
-        _tensor(workspace, torch.uint8, 0, "workspace"), 0 if workspace is None else workspace.numel(),
-        _stream(stream)), "q4k_cache_attention")
+        *_workspace(cache, workspace, torch.uint8), _stream(stream)), "q4k_cache_attention")
 
 
 def q4k_pages_reserve(cache: Cache, seqs, starts, status, stream=None):
@@ -447,18 +462,17 @@ def q4k_pages_reserve(cache: Cache, seqs, starts, status, stream=None):
 def q4k_pages_fork(cache: Cache, parents, children, status, workspace=None, stream=None):
     """Sequence children[i] becomes a copy of parents[i] (shared pages; the last partial page copied)."""
     import torch
-    n = parents.numel()
+    n = _count(parents, "parents")
     i32 = torch.int32
     _check(lib().q4k_pages_fork(
         cache._ref, _tensor(parents, i32, n, "parents"), _tensor(children, i32, n, "children"), n,
-        _tensor(status, i32, n, "status"), _tensor(workspace, torch.uint8, 0, "workspace"),
-        0 if workspace is None else workspace.numel(), _stream(stream)), "q4k_pages_fork")
+        _tensor(status, i32, n, "status"), *_workspace(cache, workspace, torch.uint8), _stream(stream)), "q4k_pages_fork")
 
 
 def q4k_pages_free(cache: Cache, seqs, stream=None):
     """Ends the sequences: their pages lose a reference."""
     import torch
-    n = seqs.numel()
+    n = _count(seqs, "seqs")
     _check(lib().q4k_pages_free(cache._ref, _tensor(seqs, torch.int32, n, "seqs"), n, _stream(stream)),
            "q4k_pages_free")
 
@@ -466,7 +480,7 @@ def q4k_pages_free(cache: Cache, seqs, stream=None):
 def q4k_pages_copy(cache: Cache, src, dst, stream=None):
     """Copies page src[i] to page dst[i] in every layer."""
     import torch
-    n = src.numel()
+    n = _count(src, "src")
     _check(lib().q4k_pages_copy(cache._ref, _tensor(src, torch.int32, n, "src"),
                                 _tensor(dst, torch.int32, n, "dst"), n, _stream(stream)), "q4k_pages_copy")
 
@@ -474,8 +488,7 @@ def q4k_pages_copy(cache: Cache, src, dst, stream=None):
 def q4k_pages_compact(cache: Cache, workspace=None, stream=None):
     """Moves the pages in use to the lowest ids, in every layer; refs and table follow."""
     import torch
-    _check(lib().q4k_pages_compact(cache._ref, _tensor(workspace, torch.uint8, 0, "workspace"),
-                                   0 if workspace is None else workspace.numel(), _stream(stream)),
+    _check(lib().q4k_pages_compact(cache._ref, *_workspace(cache, workspace, torch.uint8), _stream(stream)),
            "q4k_pages_compact")
 
 

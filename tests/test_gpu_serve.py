@@ -912,3 +912,29 @@ def test_append_to_a_cache_of_one_tensor(q4k, T, dim, kv, pairs, norm):
         rows = c.table[0, at // page].long(), at % page
         assert torch.equal(cache.k[0][rows[0], :, rows[1]], want[0][rows[0], :, rows[1]])
         assert int((cache.k != 7.0).flatten(2).any(2).sum()) <= c.table.shape[1]
+
+
+def test_raw_addresses(q4k):
+    """Device addresses in the tensors' place, where no count is taken from the tensor: the same results."""
+    T, heads, kv, dim, page = 40, 4, 2, 64, 16
+    Y = [torch.randn(T, h * dim, device=DEV) for h in (heads, kv, kv)]
+    starts, seqs, w = ints([0, 40]), ints([0]), torch.rand(dim, device=DEV)
+    results = []
+    for raw in (False, True):
+        to = (lambda t: t.data_ptr()) if raw else (lambda t: t)
+        cache = make_cache(q4k, [100, 0], page, kv, dim, spare=5)
+        cache.k.nan_to_num_(0.0)
+        ws, status = cache.workspace(), ints([9])
+        rope = torch.arange(cache.table.shape[1] * page * dim, device=DEV).view(-1, dim).float().cos()
+        Q = torch.zeros(T, heads, dim, dtype=torch.bfloat16, device=DEV)
+        out = torch.zeros_like(Q)
+        q4k.q4k_cache_append(cache, 0, to(seqs), starts, Y[0], to(Y[1]), to(Y[2]), to(Q), heads, to(rope), 2, to(w), to(w))
+        q4k.q4k_cache_attention(cache, 0, to(seqs), starts, Q, to(out), heads, T, dim ** -0.5, workspace=to(ws))
+        q4k.q4k_pages_fork(cache, ints([0]), to(ints([1])), to(status), to(ws))
+        q4k.q4k_pages_free(cache, ints([0]))
+        q4k.q4k_pages_compact(cache, to(ws))
+        torch.cuda.synchronize()
+        assert int(status) == 0
+        results.append([t.clone() for t in (Q, out, cache.k, cache.v, cache.table, cache.lens, cache.refs)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

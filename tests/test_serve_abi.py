@@ -178,3 +178,11 @@ def test_pick_refuses_fewer_biases_than_ids(q4k, ids, values, refused):
     else:
         with pytest.raises(q4k.Q4KError, match="Q4K_ERR_BAD_DIM"):  # (M = 0: nothing is launched)
             call()
+
+
+def test_counts_come_from_tensors(q4k):
+    """An address says nothing of how many entries there are: refused where the call has no other argument for it."""
+    for call in (lambda: q4k.q4k_pages_fork(None, A, A, A, A), lambda: q4k.q4k_pages_free(None, A),
+                 lambda: q4k.q4k_pages_copy(None, A, A), lambda: q4k.q4k_pages_reserve(None, A, A, A)):
+        with pytest.raises(ValueError, match="must be a tensor"):
+            call()
