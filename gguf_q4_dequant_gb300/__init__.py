@@ -329,10 +329,12 @@ class Cache:
                 raise ValueError(f"{name} must have {dims} dimension{'s' if dims > 1 else ''}")
             _ptr(t)
         layers, n_pages, kv_heads, page_size, head_dim = k.shape
-        if v.shape != k.shape or v.stride()[:2] != k.stride()[:2]:
+        # a stride of a single layer, page or head is never used: any one will do
+        used = [i for i in range(5) if k.shape[i] > 1]
+        if v.shape != k.shape or any(v.stride(i) != k.stride(i) for i in used if i < 2):
             raise ValueError("k and v must have the same shape and strides")
         for t, name in ((k, "k"), (v, "v")):
-            if t.stride()[2:] != (page_size * head_dim, head_dim, 1):
+            if any(t.stride(i) != (page_size * head_dim, head_dim, 1)[i - 2] for i in used if i >= 2):
                 raise ValueError(f"a page of a layer of {name} must be contiguous")
             if not t.is_cuda:
                 raise ValueError("tensor must live in CUDA device memory")
@@ -342,7 +344,6 @@ class Cache:
             raise ValueError("the tensors of a cache must be on one device")
         self.k, self.v, self.refs, self.table, self.lens = k, v, refs, table, lens
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
-        # a stride of a single layer or page is never used: any valid one will do
         page = kv_heads * page_size * head_dim
         page_stride = k.stride(1) if n_pages > 1 else page
         layer_stride = k.stride(0) if layers > 1 else page_stride * n_pages

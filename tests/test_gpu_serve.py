@@ -938,3 +938,30 @@ def test_raw_addresses(q4k):
         results.append([t.clone() for t in (Q, out, cache.k, cache.v, cache.table, cache.lens, cache.refs)])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_strides_of_single_layers_pages_and_heads_do_not_matter(q4k):
+    """A dimension of one entry may have any stride, and another one in V than in K."""
+    def odd(shape, strides, seed):
+        base = torch.empty(1 << 16, dtype=torch.bfloat16, device=DEV)
+        base.copy_(torch.randn(1 << 16, generator=torch.Generator().manual_seed(seed)))
+        return base.as_strided(shape, strides)
+
+    for shape, page_stride, a, b in (((1, 4, 2, 16, 64), 4096, (99, 4096, 1024), (4096 * 7, 4096, 1024)),
+                                     ((1, 4, 1, 16, 64), 2048, (8, 2048, 5), (1, 2048, 1)),
+                                     ((3, 1, 2, 16, 64), 0, (4096, 17, 1024), (4096, 4096, 1024))):
+        k, v = odd(shape, (*a, 64, 1), 1), odd(shape, (*b, 64, 1), 2)
+        n_pages, kv = shape[1:3]
+        lens = [16 * n_pages - 5]
+        refs, table = ints([1] * n_pages), torch.arange(n_pages, dtype=torch.int32, device=DEV)[None]
+        cache = q4k.Cache(k, v, refs, table, ints(lens))
+        for layer in range(shape[0]):
+            check_attention(q4k, cache, [0], [1], 2 * kv, layer=layer)
+            check_attention(q4k, cache, [0], [11], 2 * kv, layer=layer)
+    k = odd((2, 4, 2, 16, 64), (8192, 2048, 1024, 64, 1), 1)
+    v = odd((2, 4, 2, 16, 64), (10240, 2048, 1024, 64, 1), 1)
+    with pytest.raises(ValueError, match="same shape and strides"):
+        q4k.Cache(k, v, ints([0] * 4), ints([0]).view(1, 1), ints([0]))
+    v = odd((2, 4, 2, 16, 64), (8192, 2048, 1024, 32, 1), 1)
+    with pytest.raises(ValueError, match="contiguous"):
+        q4k.Cache(k, v, ints([0] * 4), ints([0]).view(1, 1), ints([0]))
