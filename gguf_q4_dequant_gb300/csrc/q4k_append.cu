@@ -36,10 +36,10 @@ __host__ __device__ constexpr int app_rows(bool wide) { return wide ? 2 : 6; }  
 
 template <int D, int kPairs, bool kNorm, bool kWide>
 __global__ void __launch_bounds__(app_threads(kWide), kWide ? 1 : 4)
-    q4k_append_kernel(const CacheLayer c, const Batch b, const float* __restrict__ Yq,
-                      const float* __restrict__ Yk, const float* __restrict__ Yv,
-                      uint16_t* __restrict__ q_out, int heads, const float* __restrict__ rope,
-                      const float* __restrict__ q_norm, const float* __restrict__ k_norm, float eps) {
+    q4k_append_kernel(const CacheLayer c, const Batch b, const float* Yq,
+                      const float* Yk, const float* Yv,
+                      uint16_t* q_out, int heads, const float* rope,
+                      const float* q_norm, const float* k_norm, float eps) {
     constexpr int kAppThreads = app_threads(kWide), kAppRows = app_rows(kWide);
     constexpr int L = D / 4;                // lanes per row
     constexpr int kStep = kAppThreads / L;  // rows that the block holds at a time

@@ -81,7 +81,7 @@ int parts_per_page(const PageGeom& g) { return (g.page_vecs + kCopyThreads * kCo
 // Copies n pairs of pages in every layer (n from the device if n_dev is given);
 // blocks take parts of (pair, layer, K or V) in turn.
 __global__ void __launch_bounds__(kCopyThreads)
-    q4k_pages_copy_kernel(const PageGeom g, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+    q4k_pages_copy_kernel(const PageGeom g, const int32_t* src, const int32_t* dst,
                           int64_t n, int64_t n_pages, int parts) {
     pdl_wait();
     const int64_t per_pair = static_cast<int64_t>(g.layers) * 2 * parts, total = n * per_pair;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 __global__ void __launch_bounds__(256)
-    q4k_pages_free_kernel(const int32_t* __restrict__ seqs, int n_seqs, int width, int64_t n_pages,
+    q4k_pages_free_kernel(const int32_t* seqs, int n_seqs, int width, int64_t n_pages,
                           int32_t* refs, int32_t* table, int32_t* lens) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(256)
 // One block: needs of the sequences, their running total, then the free pages
 // in ascending order to the sequences in order.
 __global__ void __launch_bounds__(kPlanThreads)
-    q4k_pages_reserve_kernel(const int32_t* __restrict__ seqs, int n, const int32_t* __restrict__ starts,
-                             int32_t* __restrict__ status, int n_seqs, int width, int page_size,
+    q4k_pages_reserve_kernel(const int32_t* seqs, int n, const int32_t* starts,
+                             int32_t* status, int n_seqs, int width, int page_size,
                              int64_t n_pages, int32_t* refs, int32_t* table, int32_t* lens) {
     __shared__ int64_t upto[kMaxBatch + 1];  // pages that the sequences before i need
     __shared__ int warp_sums[32];
@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // changes, writes the new tables, lengths, references and the statuses; all copy
 // their share of the pages. (Parents' lengths and tables do not change.)
 __global__ void __launch_bounds__(kCopyThreads)
-    q4k_pages_fork_kernel(const PageGeom g, const int32_t* __restrict__ parents,
-                          const int32_t* __restrict__ children, int n, int32_t* __restrict__ status, int n_seqs,
+    q4k_pages_fork_kernel(const PageGeom g, const int32_t* parents,
+                          const int32_t* children, int n, int32_t* status, int n_seqs,
                           int width, int page_size, int64_t n_pages, int32_t* refs, int32_t* table,
                           int32_t* lens, int parts, uint32_t* ticket) {
     extern __shared__ int32_t plan_s[];
@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // Second kernel: the copies, and the tables' entries that moved.
 __global__ void __launch_bounds__(kCopyThreads)
-    q4k_pages_move_kernel(const PageGeom g, const int32_t* __restrict__ plan, const int32_t* __restrict__ src,
-                          const int32_t* __restrict__ dst, const int32_t* __restrict__ to, int64_t n_pages,
-                          int n_seqs, int width, int page_size, int32_t* table, const int32_t* __restrict__ lens,
+    q4k_pages_move_kernel(const PageGeom g, const int32_t* plan, const int32_t* src,
+                          const int32_t* dst, const int32_t* to, int64_t n_pages,
+                          int n_seqs, int width, int page_size, int32_t* table, const int32_t* lens,
                           int parts) {
     pdl_wait();
     const int used = plan[0], moves = plan[1];

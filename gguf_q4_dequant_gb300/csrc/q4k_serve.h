@@ -102,7 +102,9 @@ cudaError_t launch_pick(const PickArgs& a, cudaStream_t stream, const DeviceInfo
 
 // Launch with programmatic stream serialisation when the PDL mode asks for it
 // (every kernel launched this way begins with pdl_wait()), and with a cluster
-// of `cluster` CTAs along x when that is above 1.
+// of `cluster` CTAs along x when that is above 1. A kernel's arrays are not
+// declared __restrict__: the kernel before may write them after this one has
+// begun, so they may not be read as data that is constant while it runs.
 template <typename... P, typename... A>
 cudaError_t launch_serve(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                          int pdl, int cluster, A... args) {

@@ -965,3 +965,67 @@ def test_strides_of_single_layers_pages_and_heads_do_not_matter(q4k):
     v = odd((2, 4, 2, 16, 64), (8192, 2048, 1024, 32, 1), 1)
     with pytest.raises(ValueError, match="contiguous"):
         q4k.Cache(k, v, ints([0] * 4), ints([0]).view(1, 1), ints([0]))
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+def test_a_whole_step_in_every_launch_mode(q4k, mode):
+    """Reserve, append, attention, fork, free, compaction and pick, each on what the call before it wrote, captured
+    and replayed: the state and results of the same calls made one at a time."""
+    heads, kv, dim, page, n_pages, V = 8, 2, 64, 16, 700, 1001
+    table = torch.full((12, 60), -1, dtype=torch.int32, device=DEV)
+    k, v = (torch.randn(3, n_pages, kv, page, dim, device=DEV).to(torch.bfloat16) for _ in range(2))
+    cache = q4k.Cache(k, v, ints([0] * n_pages), table, ints([0] * 12))
+    ws, status = cache.workspace(), ints([9] * 6)
+    seqs, news = ints(range(6)), [300, 1, 77, 16, 31, 200]
+    starts, T = ints(np.concatenate([[0], np.cumsum(news)])), sum(news)
+    Y = [torch.randn(T, h * dim, device=DEV) for h in (heads, kv, kv)]
+    Q = torch.zeros(T, heads, dim, dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros_like(Q)
+    one, ones = ints(range(7)), [torch.randn(6, h * dim, device=DEV) for h in (heads, kv, kv)]
+    Q1 = torch.zeros(6, heads, dim, dtype=torch.bfloat16, device=DEV)
+    out1 = torch.zeros_like(Q1)
+    logits, pick = torch.randn(6, V, device=DEV), torch.zeros(6, dtype=torch.int64, device=DEV)
+    adjusted, pen = torch.zeros_like(logits), torch.rand(6, 3, device=DEV) + 0.5
+    scale = dim ** -0.5
+    state = (cache.k, cache.v, cache.refs, cache.table, cache.lens)
+    results = (Q, out, Q1, out1, status, adjusted, pick)
+    begin = [t.clone() for t in state]
+    calls = [
+        lambda: q4k.q4k_pages_reserve(cache, seqs, starts, status),
+        lambda: q4k.q4k_cache_append(cache, 1, seqs, starts, *Y, Q, heads),
+        lambda: q4k.q4k_cache_attention(cache, 1, seqs, starts, Q, out, heads, 300, scale, workspace=ws),
+        lambda: q4k.q4k_pages_fork(cache, seqs, ints_b, status, ws),
+        lambda: q4k.q4k_pages_free(cache, odd),
+        lambda: q4k.q4k_pages_compact(cache, ws),
+        lambda: q4k.q4k_pages_copy(cache, src, dst),
+        lambda: q4k.q4k_pages_reserve(cache, ints_b, one, status),
+        lambda: q4k.q4k_cache_append(cache, 1, ints_b, one, *ones, Q1, heads),
+        lambda: q4k.q4k_cache_attention(cache, 1, ints_b, one, Q1, out1, heads, 1, scale, workspace=ws),
+        lambda: q4k.q4k_logits_pick(logits, 6, V, adjusted, pick, status, one, pen),
+        lambda: q4k.q4k_pages_compact(cache, ws),
+    ]
+    ints_b, odd = ints(range(6, 12)), ints([0, 2, 4])
+    src, dst = ints([0, 3]), ints([n_pages - 1, n_pages - 2])
+    old = q4k.q4k_set_pdl(0)
+    try:
+        for call in calls:
+            call()
+            torch.cuda.synchronize()
+        want = [t.clone() for t in (*state, *results)]
+        assert int(status.sum()) == 0 and int((cache.refs > 0).sum()) > 40
+        q4k.q4k_set_pdl(mode)
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            for call in calls:
+                call()
+        for _ in range(20):
+            for t, b in zip(state, begin):
+                t.copy_(b)
+            for t in results:
+                t.fill_(5)
+            graph.replay()
+            torch.cuda.synchronize()
+            for t, w in zip((*state, *results), want):
+                assert torch.equal(t, w)
+    finally:
+        q4k.q4k_set_pdl(old)
