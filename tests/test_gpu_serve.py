@@ -1029,3 +1029,92 @@ def test_a_whole_step_in_every_launch_mode(q4k, mode):
                 assert torch.equal(t, w)
     finally:
         q4k.q4k_set_pdl(old)
+
+
+def attention_rows(cache, ids, news, Q, heads, window=0, sinks=0, p_bits=None):
+    """The definition on the GPU in float64, a sequence at a time, and the bound (each weight rounded to bf16: p_bits
+    None, or to the sum of two, 15 bits of it: p_bits 15). Ids out of range give zeros."""
+    page, dim = cache.k.shape[3], cache.head_dim
+    scale = dim ** -0.5
+    y = torch.zeros(Q.shape, dtype=torch.float64, device=DEV)
+    tol = torch.zeros_like(y)
+    lens, at = cache.lens.tolist(), 0
+    for b, m in zip(ids, news):
+        rows = slice(at, at + m)
+        at += m
+        n = lens[b] if 0 <= b < len(lens) else 0
+        if m == 0 or n == 0:
+            continue
+        pages = cache.table[b, :-(-n // page)].long()
+        k, v = (t[0][pages].transpose(0, 1).reshape(cache.kv_heads, -1, dim)[:, :n].double() for t in (cache.k, cache.v))
+        q = Q[rows].double().view(m, cache.kv_heads, -1, dim)
+        x = torch.einsum("mghd,gjd->mghj", q, k) * scale
+        size = torch.einsum("mghd,gjd->mghj", q.abs(), k.abs()).amax(-1, keepdim=True) * scale
+        p, j = torch.arange(n - m, n, device=DEV)[:, None], torch.arange(n, device=DEV)[None]
+        sees = (j <= p) & ((j > p - window) | (j < sinks) if window else j >= 0)
+        x = x.masked_fill(~sees[:, None, None], -float("inf"))
+        a = torch.exp(x - x.amax(-1, keepdim=True).nan_to_num(neginf=0.0))
+        total = a.sum(-1, keepdim=True)
+        a = torch.where(total > 0, a / total, 0.0)
+        want, mean = (torch.einsum("mghj,gjd->mghd", a, t) for t in (v, v.abs()))
+        bound = 2.0 ** -8 * want.abs() + (2.0 ** -(p_bits or 8) + 2.0 ** -13 + 2.0 ** -18 * size) * mean
+        y[rows], tol[rows] = want.reshape(m, heads, dim), bound.reshape(m, heads, dim)
+    return y, tol
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,group,most", [(33, 1, 1), (33, 16, 1), (64, 5, 1), (64, 8, 1), (64, 12, 1), (300, 4, 4), (300, 2, 3),
+                                          (4096, 4, 1), (4096, 9, 1), (40, 4, 30), (200, 2, 70)])
+def test_many_sequences(q4k, dim, n, group, most):
+    """Steps of more than 32 sequences, single tokens and chunks, every row: lengths from 0 on (some shared out over
+    several blocks), sequences without new tokens, more new tokens than positions, ids out of range."""
+    rng = np.random.default_rng(n + group + dim)
+    kv, page = 2, 32
+    lens = np.where(rng.random(n) < 0.1, rng.integers(0, 3, n), rng.integers(1, 900 if n < 1000 else 80, n))
+    lens[n // 3] = 30000 if n < 1000 else 9000  # one that is shared out
+    lens[n // 2] = 5000
+    news = rng.integers(0, most + 1, n) if most > 1 else (rng.random(n) < 0.9).astype(int)
+    news[n // 3] = most
+    ids = np.arange(n)
+    ids[[5, n - 2]] = [n + 3, -1]
+    counts = -(-lens // page)
+    cache = make_cache(q4k, [0], page, kv, dim, spare=int(counts.sum()) + 2)  # (the pool; its table is made here)
+    order = torch.randperm(cache.k.shape[1], generator=torch.Generator().manual_seed(n)).tolist()
+    table = np.full((n, int(counts.max())), -1, dtype=np.int32)
+    for i, c in enumerate(counts):
+        table[i, :c] = [order.pop() for _ in range(c)]
+    k, v = cache.k.clone(), cache.v.clone()
+    for i, length in enumerate(lens):  # what lies past a sequence's end must not matter
+        if length % page:
+            k[0, table[i, length // page], :, length % page:] = float("nan")
+            v[0, table[i, length // page], :, length % page:] = float("nan")
+    cache = q4k.Cache(k, v, cache.refs, torch.tensor(table, device=DEV), ints(lens))
+    heads = kv * group
+    Q = (torch.randn(int(news.sum()), heads, dim, generator=torch.Generator().manual_seed(3)) * 1.5).to(torch.bfloat16).to(DEV)
+    for window, sinks in ((0, 0), (300, 3))[:2 if n < 1000 else 1]:
+        out = attend(q4k, cache, 0, ids, news, Q, heads, window=window, sinks=sinks, max_new=most)
+        y, tol = attention_rows(cache, ids, news.tolist(), Q, heads, window, sinks, 15 if most * group <= 16 else None)
+        worst = float(((out.double() - y).abs() / (tol + 1e-30)).max())
+        assert worst <= 1.0, f"error {worst:.3f} of the bound"
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 8, 16])
+def test_weights_of_single_tokens_have_more_bits_than_one_bf16(q4k, dim, group):
+    """Values that are unit vectors give the weights themselves: within the output's own rounding, 2^-8, and 2^-15
+    for the sum of two bf16 (the upper cut off, at most 2^-7 away, the lower rounded to 8 bits)."""
+    n, kv = dim, 2
+    cache = make_cache(q4k, [n], 64, kv, dim)
+    cache.k.mul_(0.5)  # (scores, and so the fp32 part of the bound, small)
+    for j in range(n):
+        cache.v[0, cache.table[0, j // 64].long(), :, j % 64] = 0.0
+        cache.v[0, cache.table[0, j // 64].long(), :, j % 64, j] = 1.0
+    Q = torch.randn(1, kv * group, dim, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    out = attend(q4k, cache, 0, [0], [1], Q, kv * group).double()
+    y, tol = attention_rows(cache, [0], [1], Q, kv * group, p_bits=15)
+    assert bool(((out - y).abs() <= tol).all())
+    # the bound tells the two apart: weights rounded to one bf16 pass it
+    once = y.float().to(torch.bfloat16).double()
+    low = (y / y.amax(-1, keepdim=True)).float().to(torch.bfloat16).double()  # as the kernel has them, 1 at the largest
+    low = (low * y.amax(-1, keepdim=True)).float().to(torch.bfloat16).double()
+    assert bool(((once - y).abs() <= tol).all()) and not bool(((low - y).abs() <= tol).all())
