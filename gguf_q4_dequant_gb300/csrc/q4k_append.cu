@@ -14,7 +14,7 @@
 // were loaded after the place was known and the norm's and rotation's steps were
 // taken whether wanted or not); with a norm 2894 tokens of 56 rows take 28 us for 23,
 // with rotation 33: five shuffles per row, and registers for 4 blocks per SM only.
-// 64 tokens of 56 rows: 3.7 us, the launch and the four loads.
+// 64 tokens of 56 rows: 3.8 us, the launch and the four loads.
 #include <cuda_bf16.h>
 
 #include "q4k_device.cuh"
@@ -28,7 +28,7 @@ __device__ __forceinline__ uint2 bf16x4(float4 x) {
 }
 
 // A token is one block's, of one of two widths: wide, with all rows on their way
-// at once, for up to one token per SM (64 tokens of 56 rows 3.7 us, 5.4 in the other
+// at once, for up to one token per SM (64 tokens of 56 rows 3.8 us, 5.4 in the other
 // width; 152 tokens 4.3, 5.9), else so that blocks in different phases share an
 // SM (200 tokens 6.2 us, 6.6 wide; 2894 tokens of 48 rows 21 us, 43 wide).
 __host__ __device__ constexpr int app_threads(bool wide) { return wide ? 1024 : 256; }

@@ -19,15 +19,16 @@
 // While the tensor core works for one half, the other half's 128 threads (one
 // row each) turn S into P: the two halves take turns.
 //
-// 4096 tokens of 32 heads over 16384 positions, 128 wide: 0.59-0.61 ms, 1.57 to
-// 1.63 PFLOP/s. A key tile takes 3000 cycles for both halves, 2048 of them
+// 4096 tokens of 32 heads over 16384 positions, 128 wide: 0.59-0.60 ms for a dozen
+// calls, 1.59 to 1.63 PFLOP/s; 0.62-0.64, 1.52, call after call (1380 W, power
+// capped, 1.93 GHz). A key tile takes 3000 cycles for both halves, 2048 of them
 // products (tensor pipe 65 %); with the softmax reduced to a copy the whole
 // still takes 0.58 ms: the products are held up by shared memory, of which Q and K are read at
 // 64 KB and V at 32 KB per half while the next tiles come in at 64 KB, together
 // 2048 cycles at 128 bytes. Sharing K between two SMs (cta_group::2) is what
 // would lift that. Two threads per row, P handed over in parts, a pipeline over
 // TMEM loads and hand-ordered exponentials were no faster (0.60 to 0.88 ms).
-// 2017 tokens in 8 sequences with a window of 1024: 48 us; 14 key tiles a CTA
+// 2017 tokens in 8 sequences with a window of 1024: 49-52 us; 14 key tiles a CTA
 // are 22 us of it, the first loads, row tiles' ends and the joining the rest.
 // Joining: the half that comes last keeps its own part in TMEM, and does not
 // write it out if it sees that the others have come; parts are read and written 16 bytes a

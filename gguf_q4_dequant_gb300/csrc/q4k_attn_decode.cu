@@ -20,7 +20,7 @@
 // rows as the M of 16-row products, twice the products and registers: 197 us);
 // 2 tokens over 217 k positions, 64 wide, 445 MB: 77 us, 5.8 TB/s -- the rest is
 // the plan at the start and the joining of ten parts per row tile; one token over
-// 517 positions: 8.9 us, five tiles through one SM per kv head.
+// 517 positions: 9.1 us, five tiles through one SM per kv head.
 #include <cuda_bf16.h>
 
 #include "q4k_attn.cuh"

@@ -24,7 +24,7 @@
 // with the tables cleared by all warps first, one atomic operation per
 // history entry, eight of them in flight, and one per warp and batch for the
 // list's places, 22 us, 3.6 TB/s; one entry after another, three atomics each:
-// 26 us. 200 rows of 50257, not kept: 13.4 us, 3.1 TB/s; one row of 128256: 5.6 us.
+// 26 us. 200 rows of 50257, not kept: 13.4 us, 3.1 TB/s; one row of 128256: 5.8 us.
 // Of the 22 us the stream is 13; the rest is the chain before and after
 // it: starts, the list, the look again, the cluster's exchange.)
 //

@@ -209,7 +209,8 @@ int q4k_selftest_timeout(int64_t limit_ns, void* stream);
  *   page table[s*width + p/page_size].
  * refs[page] counts the sequences that hold the page; 0: the page is free.
  * lens[s] is the number of positions of sequence s, 0: not in use. Entries of
- * table past a sequence's pages are -1 (they are never followed).
+ * table past a sequence's pages must be -1: q4k_pages_free gives back every page
+ * that a row names, the other calls follow a sequence's own pages only.
  *
  * A step's batch is n sequences with new tokens: seqs[i] (device, distinct;
  * NULL: 0..n-1) names the i-th one, and its new tokens are rows starts[i] to
@@ -240,6 +241,7 @@ typedef struct q4k_cache {
  * or a negative status. It must be zero-filled before its first use; every
  * call leaves what later calls rely on, so one workspace serves any sequence
  * of calls on one stream. Calls that may run at the same time need one each.
+ * A call that ended in Q4K_ERR_TIMEOUT leaves it undefined: zero it again.
  * The size depends on n_pages, head_dim and the device only.
  */
 int64_t q4k_cache_workspace(const q4k_cache* c);
@@ -282,7 +284,9 @@ int q4k_cache_append(const q4k_cache* c, int layer, const int32_t* seqs, int n, 
  *   Q, out  device, [tokens][heads][head_dim] bf16, 16-byte aligned; rows of
  *           out that belong to no sequence of the batch are left as they are
  *   max_new the largest number of new tokens of a sequence, as far as the
- *           caller knows it: it only selects between kernels
+ *           caller knows it: it selects between kernels, and with that the
+ *           rounding of the weights (below), for all tokens of the call; any
+ *           value is right for any step
  *   scale   > 0, finite; window, sinks >= 0 (sinks is ignored with window 0)
  *   ws      see q4k_cache_workspace; ws_bytes its size
  * heads/kv_heads <= 128; 1 <= n <= 4096; 1 <= tokens < 2^31 / heads.
@@ -301,7 +305,10 @@ int q4k_cache_attention(const q4k_cache* c, int layer, const int32_t* seqs, int 
  * order of i. status[i] (device): 0, or 1 where the pages left over (or width)
  * do not suffice, or the id is out of range; such a sequence keeps its length
  * and pages. (Pages are given while the running total of the batch's needs
- * fits the free pages; a sequence that needs none always succeeds.)
+ * fits the free pages; a sequence that needs none always succeeds.) Give a
+ * sequence with status 1 no new tokens in the step's other calls: its length does
+ * not count them, so they would be stored over its last positions, in pages
+ * that other sequences may hold too.
  * 1 <= n <= 4096.
  */
 int q4k_pages_reserve(const q4k_cache* c, const int32_t* seqs, int n, const int32_t* starts,
