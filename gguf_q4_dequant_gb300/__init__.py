@@ -30,8 +30,13 @@ EXPORTS = ("q4k_status_string", "q4k_init", "q4k_dequant", "q4k_matmul", "q4k_ma
            "q4k_matmul_multi", "q4k_matmul_multi_bf16", "q4k_matmul_argmax",
            "q4k_matmul_argmax_bf16", "q4k_set_pdl", "q4k_device_error", "q4k_selftest_timeout",
            "q4k_cache_workspace", "q4k_cache_append", "q4k_cache_attention", "q4k_pages_reserve",
-           "q4k_pages_fork", "q4k_pages_free", "q4k_pages_copy", "q4k_pages_compact", "q4k_logits_pick")
+           "q4k_pages_fork", "q4k_pages_free", "q4k_pages_copy", "q4k_pages_compact", "q4k_logits_pick",
+           "q4k_add_norm", "q4k_route_workspace", "q4k_route", "q4k_experts_gather", "q4k_experts_matmul",
+           "q4k_experts_gated", "q4k_experts_combine")
 MAX_GROUP = 8
+
+#: weightings of q4k_route
+ROUTE_SOFTMAX, ROUTE_SOFTMAX_TOP, ROUTE_SIGMOID, ROUTE_SIGMOID_TOP = range(4)
 
 
 _STATUS_NAMES = {Q4K_OK: "Q4K_OK", Q4K_ERR_NULL: "Q4K_ERR_NULL", Q4K_ERR_BAD_DIM: "Q4K_ERR_BAD_DIM",
@@ -98,6 +103,8 @@ def lib() -> ctypes.CDLL:
             L.q4k_selftest_timeout.argtypes = [i64, vp]
             L.q4k_selftest_timeout.restype = ctypes.c_int
             ci, cf, cp = ctypes.c_int, ctypes.c_float, ctypes.POINTER(_CacheStruct)
+            L.q4k_route_workspace.argtypes = [i64, i64]
+            L.q4k_route_workspace.restype = i64
             L.q4k_cache_workspace.argtypes = [cp]
             L.q4k_cache_workspace.restype = i64
             for name, args in (
@@ -108,7 +115,13 @@ def lib() -> ctypes.CDLL:
                     ("q4k_pages_free", [cp, vp, ci, vp]),
                     ("q4k_pages_copy", [cp, vp, vp, i64, vp]),
                     ("q4k_pages_compact", [cp, vp, i64, vp]),
-                    ("q4k_logits_pick", [vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp])):
+                    ("q4k_logits_pick", [vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+                    ("q4k_add_norm", [vp, ci, vp, vp, cf, i64, i64, vp, vp, ci, vp, vp, vp]),
+                    ("q4k_route", [vp, i64, i64, ci, ci, cf, vp, vp, vp, vp, vp, vp, i64, vp]),
+                    ("q4k_experts_gather", [vp, vp, vp, i64, ci, i64, vp, vp]),
+                    ("q4k_experts_matmul", [vp, i64, i64, i64, vp, vp, i64, vp, vp]),
+                    ("q4k_experts_gated", [vp, vp, i64, i64, i64, vp, vp, i64, vp, vp]),
+                    ("q4k_experts_combine", [vp, i64, vp, vp, vp, i64, ci, i64, vp, vp])):
                 fn = getattr(L, name)
                 fn.argtypes = args
                 fn.restype = ci
@@ -509,3 +522,116 @@ def q4k_logits_pick(logits, M: int, V: int, out=None, pick=None, history=None, h
         _tensor(bias_ids, i32, 0, "bias_ids") or None, _tensor(bias, f32, biases, "bias"),
         _tensor(bias_starts, i32, M + 1, "bias_starts"), _tensor(mask, i32, M * ((V + 31) // 32), "mask"),
         _stream(stream)), "q4k_logits_pick")
+
+
+# ------------------------------------------------------- the expert layer ---
+
+def _rows(t, name):
+    """(rows, columns) of a tensor of a row per token or pair."""
+    if isinstance(t, int) or t.dim() != 2:
+        raise ValueError(f"{name} must be a tensor of two dimensions")
+    return t.shape
+
+
+def _float_type(t, name):
+    """q4k_type of a tensor."""
+    import torch
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be {torch.float32} or {torch.bfloat16}, got {t.dtype}")
+    return int(t.dtype == torch.bfloat16)
+
+
+def _bytes(t, need, name):
+    """Address of a tensor of 8-bit codes (uint8, or torch's e4m3)."""
+    import torch
+    if t is not None and not isinstance(t, int) and t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    return _tensor(t, torch.uint8, need, name)
+
+
+def q4k_add_norm(x, delta, weight, eps: float = 1e-6, sum=None, out=None, codes=None, scales=None, stream=None):
+    """sum = x + delta [T, C] (x and sum fp32 or bf16; delta fp32 or None), and its RMS norm times weight as out
+    (fp32 or bf16) and as e4m3 codes with scales [T, C/32] (uint8 exponents); each output may be None."""
+    import torch
+    T, C = _rows(x, "x")
+    kind = _float_type(x, "x")
+    if isinstance(out, int):
+        raise ValueError("out must be a tensor, its type is taken from it")
+    out_kind = 0 if out is None else _float_type(out, "out")
+    _check(lib().q4k_add_norm(
+        _ptr(x), kind, _tensor(delta, torch.float32, T * C, "delta"), _tensor(weight, torch.float32, C, "weight"), eps, T, C,
+        _tensor(sum, x.dtype, T * C, "sum"), _tensor(out, None if out is None else out.dtype, T * C, "out"), out_kind,
+        _bytes(codes, T * C, "codes"), _tensor(scales, torch.uint8, T * (C // 32), "scales"), _stream(stream)), "q4k_add_norm")
+
+
+def q4k_route_workspace(T: int, E: int) -> int:
+    """Bytes of the workspace of q4k_route."""
+    n = lib().q4k_route_workspace(T, E)
+    if n < 0:
+        raise Q4KError(n, "q4k_route_workspace")
+    return n
+
+
+def q4k_route(logits, k: int, weighting: int, scale: float, ids, weights, order, slots, starts, workspace, stream=None):
+    """The k largest of the router's logits [T, E] of each token: ids, weights, slots [T, k], and the pairs by expert:
+    order [T*k], starts [E + 1] (see include/q4k.h)."""
+    import torch
+    T, E = _rows(logits, "logits")
+    i32 = torch.int32
+    ws_bytes = q4k_route_workspace(T, E) if isinstance(workspace, int) else workspace.numel() if workspace is not None else 0
+    _check(lib().q4k_route(
+        _tensor(logits, torch.float32, T * E, "logits"), T, E, k, weighting, scale, _tensor(ids, i32, T * k, "ids"),
+        _tensor(weights, torch.float32, T * k, "weights"), _tensor(order, i32, T * k, "order"),
+        _tensor(slots, i32, T * k, "slots"), _tensor(starts, i32, E + 1, "starts"),
+        _tensor(workspace, torch.uint8, 0, "workspace"), ws_bytes, _stream(stream)), "q4k_route")
+
+
+def q4k_experts_gather(X, order, k: int, out, scales=None, stream=None):
+    """out[p] = X[order[p] // k] (bf16 [T*k, C]) from rows X [T, C] in bf16, or in e4m3 codes with their scales."""
+    import torch
+    T, C = _rows(X, "X")
+    x = _tensor(X, torch.bfloat16, T * C, "X") if scales is None else _bytes(X, T * C, "X")
+    _check(lib().q4k_experts_gather(
+        x, _tensor(scales, torch.uint8, T * (C // 32), "scales"), _tensor(order, torch.int32, T * k, "order"), T, k, C,
+        _tensor(out, torch.bfloat16, T * k * C, "out"), _stream(stream)), "q4k_experts_gather")
+
+
+def _experts(N, K, X, starts, Y):
+    """(E, X, starts, pairs, Y) of an experts' product, checked."""
+    import torch
+    pairs, cols = _rows(X, "X")
+    if cols != K:
+        raise ValueError(f"X has {cols} columns, K is {K}")
+    E = _count(starts, "starts") - 1
+    return (E, _tensor(X, torch.bfloat16, pairs * K, "X"), _tensor(starts, torch.int32, E + 1, "starts"), pairs,
+            _tensor(Y, torch.bfloat16, pairs * max(N, 0), "Y"))
+
+
+def q4k_experts_matmul(W, N: int, K: int, X, starts, Y, stream=None):
+    """Y[p] = X[p] W_e^T (bf16) for the rows p of each expert e: starts [E + 1], W the E packed matrices [N, K]."""
+    import torch
+    E, x, st, pairs, y = _experts(N, K, X, starts, Y)
+    need = E * _w_bytes(N, K) if _dims_valid(N, K) else 0
+    _check(lib().q4k_experts_matmul(_tensor(W, torch.uint8, need, "W"), E, N, K, x, st, pairs, y, _stream(stream)),
+           "q4k_experts_matmul")
+
+
+def q4k_experts_gated(gate, up, N: int, K: int, X, starts, Y, stream=None):
+    """Y[p] = silu(X[p] gate_e^T) * (X[p] up_e^T) (bf16) for the rows p of each expert e."""
+    import torch
+    E, x, st, pairs, y = _experts(N, K, X, starts, Y)
+    need = E * _w_bytes(N, K) if _dims_valid(N, K) else 0
+    _check(lib().q4k_experts_gated(_tensor(gate, torch.uint8, need, "gate"), _tensor(up, torch.uint8, need, "up"), E, N, K, x,
+                                   st, pairs, y, _stream(stream)), "q4k_experts_gated")
+
+
+def q4k_experts_combine(Y, slots, weights, out, base=None, stream=None):
+    """out[t] = base[t] + sum_j weights[t, j] * Y[slots[t, j]] (fp32 [T, C]); slots below 0 add nothing."""
+    import torch
+    pairs, C = _rows(Y, "Y")
+    T, k = _rows(slots, "slots")
+    f32 = torch.float32
+    _check(lib().q4k_experts_combine(
+        _tensor(Y, torch.bfloat16, pairs * C, "Y"), pairs, _tensor(slots, torch.int32, T * k, "slots"),
+        _tensor(weights, f32, T * k, "weights"), _tensor(base, f32, T * C, "base"), T, k, C, _tensor(out, f32, T * C, "out"),
+        _stream(stream)), "q4k_experts_combine")

@@ -21,6 +21,7 @@
 
 #include "q4k.h"
 #include "q4k_device.cuh"
+#include "q4k_experts.h"
 #include "q4k_internal.h"
 #include "q4k_serve.h"
 
@@ -116,7 +117,7 @@ void init_device(int dev, DeviceState& st) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess || gemv_setup(st.info) != cudaSuccess || tcgemv_setup(st.info) != cudaSuccess ||
         gemm_setup(st.info) != cudaSuccess || attn_setup(st.info) != cudaSuccess || pick_setup(st.info) != cudaSuccess ||
-        pages_setup() != cudaSuccess ||
+        pages_setup() != cudaSuccess || experts_setup(st.info) != cudaSuccess ||
         encoder() == nullptr) {
         st.status = Q4K_ERR_CUDA;
         return;
@@ -342,6 +343,8 @@ int check_matmul(int count, const void* const* W, const int64_t* N, int64_t K, c
 
 int device_info(const DeviceInfo** info) { return current_device(info); }
 int pdl_mode() { return g_pdl.load(std::memory_order_relaxed); }
+
+int weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K, int rows) { return encode_w(map, W, N, K, rows); }
 
 bool encode_bf16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box) {

@@ -1,0 +1,87 @@
+// q4k_experts.h -- what the kernels of an expert layer share: the device view of
+// the rows sorted by expert, and the host-side launchers. Not part of the public
+// interface.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "q4k.h"
+#include "q4k_internal.h"
+
+namespace q4k {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTop = 32;
+
+// The rows of a step in the order of their experts: expert e has rows
+// starts[e] .. starts[e+1]-1 of `pairs` rows.
+struct ExpertRows {
+    const int32_t* starts;  // [experts + 1]
+    int experts, pairs;
+};
+
+struct NormArgs {
+    const void* x;
+    const float* delta;
+    const float* weight;
+    void* sum;
+    void* out;
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t T;
+    int C;
+    float eps;
+    bool x_bf16, out_bf16;
+};
+cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t stream, int pdl);
+
+struct RouteArgs {
+    const float* logits;
+    int T, E, k, weighting;
+    float scale;
+    int32_t* ids;
+    float* weights;
+    int32_t *order, *slots, *starts;
+    int32_t* ws;
+};
+int64_t route_scratch_bytes(int64_t T, int E);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int pdl);
+
+struct GatherArgs {
+    const void* x;
+    const uint8_t* scales;  // NULL: bf16 rows, else e4m3 codes and these exponents
+    const int32_t* order;
+    uint16_t* out;
+    int T, C, k, pairs;
+};
+cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream, int pdl);
+
+struct CombineArgs {
+    const uint16_t* y;
+    const int32_t* slots;
+    const float* weights;
+    const float* base;
+    float* out;
+    int64_t T;
+    int C, k, pairs;
+};
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream, int pdl);
+
+struct ExpertArgs {
+    const uint8_t* W;
+    const uint8_t* W2;  // the up matrices of a gated product, or NULL
+    int64_t N, K;
+    const uint16_t* X;
+    ExpertRows rows;
+    uint16_t* Y;
+};
+cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
+cudaError_t experts_setup(DeviceInfo& dev);
+
+// A 2-D byte map {K/256*144, N} of packed rows, box one super-block of `rows` rows
+// (a q4k_status; cached per host thread).
+int weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K, int rows);
+
+}  // namespace q4k

@@ -371,6 +371,118 @@ int q4k_logits_pick(const float* logits, int64_t M, int64_t V, float* out, int64
                     const int32_t* bias_ids, const float* bias, const int32_t* bias_starts,
                     const uint32_t* mask, void* stream);
 
+/* ======================================================================
+ * The expert layer of a mixture-of-experts model
+ * ======================================================================
+ * A layer whose feed-forward part is E experts with packed Q4_K matrices, k of
+ * them for each token: the norm before it (q4k_add_norm), the router's picks
+ * and the order of the rows by expert (q4k_route, from the logits of the
+ * router's product), the rows in that order (q4k_experts_gather), the experts'
+ * products (q4k_experts_gated for gate and up, q4k_experts_matmul for down),
+ * and the way back with the weights applied (q4k_experts_combine). The pages of
+ * the reference name the gathered product of quantised experts (mlx-rs #356:
+ * gather_qmm, QuantizedSwitchLinear) and the norms of every layer.
+ *
+ * The rules of the calls above hold: asynchronous on `stream`, no allocation,
+ * no host synchronisation, capturable, arguments checked before any launch,
+ * contents of device arrays never lead outside the arrays. Arrays that a call
+ * writes overlap no other array of the call unless it is said.
+ *
+ * A step has T tokens. Its pairs are (t, j), token t with its j-th pick, numbered
+ * t*k + j. Sorted by expert and within an expert by number they are the rows of
+ * the experts' products: row p is pair order[p], pair i is row slots[i], and
+ * expert e has rows starts[e] .. starts[e+1]-1.
+ */
+
+enum q4k_type { Q4K_F32 = 0, Q4K_BF16 = 1 };
+
+/*
+ * r = x + delta; sum = r; y = r / sqrt(mean(r^2) + eps) * weight, row by row, in
+ * fp32, and y as wanted: `out` in fp32 or bf16, and `codes` with `scales` in 8
+ * bits: of every 32 columns the scale is the smallest power of two s >= 2^-127
+ * with max|y| <= 448 s, held as the byte log2(s) + 127, and the codes are y / s
+ * rounded to e4m3 (4 significant bits, to nearest even). 32 columns with an
+ * infinity or a NaN have the scale byte 255 and codes of NaN.
+ *   x       device, [T][C], fp32 or bf16 by x_type
+ *   delta   device, [T][C] floats (what the layer before adds); NULL: 0
+ *   weight  device, [C] floats
+ *   sum     device, [T][C] of x's type (r rounded once; y is taken from r), may be x; NULL: not kept
+ *   out     device, [T][C] by out_type; NULL: not wanted
+ *   codes, scales  device, [T][C] and [T][C/32] bytes; NULL: not wanted
+ * At least one of out and codes is wanted; codes and scales go together.
+ * 1 <= T < 2^31; C a multiple of 32, 32 .. 32768; eps >= 0, finite. codes is 8-byte
+ * aligned, the others but scales 16.
+ */
+int q4k_add_norm(const void* x, int x_type, const float* delta, const float* weight, float eps, int64_t T, int64_t C,
+                 void* sum, void* out, int out_type, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* How the weights of a token's picks follow from its logits (each times `scale`): */
+enum q4k_weighting {
+    Q4K_ROUTE_SOFTMAX = 0,     /* softmax over all experts */
+    Q4K_ROUTE_SOFTMAX_TOP = 1, /* softmax over the picked ones */
+    Q4K_ROUTE_SIGMOID = 2,     /* 1 / (1 + exp(-logit)) */
+    Q4K_ROUTE_SIGMOID_TOP = 3  /* the same divided by their sum over the picked ones */
+};
+
+/*
+ * The k largest logits of each token, largest first (ties: the lowest expert
+ * first), their weights, and the order of the pairs by expert. A logit of -inf or
+ * NaN is never picked and counts for nothing in a softmax (a mask); where fewer
+ * than k are left, the last picks have id -1, weight 0 and slot -1, and are
+ * among no expert's rows. starts[E] is the number of rows; order is -1 from there on.
+ *   logits  device, [T][E] floats
+ *   ids, weights, slots  device, [T][k] int32, floats, int32
+ *   order   device, [T*k] int32;  starts  device, [E+1] int32
+ *   ws      device, ws_bytes >= q4k_route_workspace(T, E), 4-byte aligned; needs no
+ *           set-up, and holds nothing between calls
+ * 1 <= k <= 32, k <= E <= 1024; T >= 1, T*k < 2^31; scale finite.
+ */
+int64_t q4k_route_workspace(int64_t T, int64_t E); /* 4 E (ceil(T / 64) + 1) */
+int q4k_route(const float* logits, int64_t T, int64_t E, int k, int weighting, float scale, int32_t* ids, float* weights,
+              int32_t* order, int32_t* slots, int32_t* starts, void* ws, int64_t ws_bytes, void* stream);
+
+/*
+ * Rows in the order of their experts: out[p] = X[order[p] / k] for p < T*k; rows
+ * whose order is outside [0, T*k) are left as they are. X: bf16 (scales NULL), or
+ * e4m3 codes with scales as q4k_add_norm writes them; a code times its scale is
+ * exact in bf16 (down to 2^-126).
+ *   X    device, [T][C] bf16 or codes;  scales  device, [T][C/32] bytes or NULL
+ *   out  device, [T*k][C] bf16
+ * 1 <= k <= 32, T >= 1, T*k < 2^31; C a multiple of 8 (of 32 with scales), 8 .. 32768.
+ * X and out 16-byte aligned (codes 8).
+ */
+int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* order, int64_t T, int k, int64_t C,
+                       uint16_t* out, void* stream);
+
+/*
+ * The experts' products: Y[p] = X[p] W_e^T for the rows p of every expert e, W_e
+ * the e-th of E packed matrices [N][K] that follow one another; accumulated in
+ * fp32 and rounded once to bf16. q4k_experts_gated takes two of them and gives
+ * Y[p] = g / (1 + exp(-g)) * u with g = X[p] gate_e^T and u = X[p] up_e^T in fp32.
+ * Rows before starts[0] and from starts[E] on are left as they are; starts is
+ * taken as ascending and inside [0, pairs] (values are clamped to that).
+ *   W, gate, up  device, E*N*K/256*144 bytes, 16-byte aligned
+ *   X  device, [pairs][K] bf16, values below 2^64;  Y  device, [pairs][N] bf16
+ *   starts  device, [E+1] int32
+ * 1 <= E <= 1024, N >= 1, E*N < 2^31; K a multiple of 256, 256 .. 2^24; 1 <= pairs < 2^31.
+ */
+int q4k_experts_matmul(const void* W, int64_t E, int64_t N, int64_t K, const uint16_t* X, const int32_t* starts,
+                       int64_t pairs, uint16_t* Y, void* stream);
+int q4k_experts_gated(const void* gate, const void* up, int64_t E, int64_t N, int64_t K, const uint16_t* X,
+                      const int32_t* starts, int64_t pairs, uint16_t* Y, void* stream);
+
+/*
+ * Back to the tokens: out[t] = base[t] + sum_j weights[t][j] * Y[slots[t][j]], in
+ * fp32, added in the order of j. A slot outside [0, pairs) adds nothing.
+ *   Y      device, [pairs][C] bf16;  slots, weights  device, [T][k]
+ *   base   device, [T][C] floats (a shared expert's output, the residual stream); NULL: 0
+ *   out    device, [T][C] floats, may be base
+ * 1 <= k <= 32, T >= 1, T*k < 2^31, 1 <= pairs < 2^31; C a multiple of 8, 8 .. 32768. Y, base
+ * and out 16-byte aligned.
+ */
+int q4k_experts_combine(const uint16_t* Y, int64_t pairs, const int32_t* slots, const float* weights, const float* base,
+                        int64_t T, int k, int64_t C, float* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

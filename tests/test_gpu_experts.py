@@ -1,0 +1,435 @@
+"""The expert layer's calls on the GPU, against plain implementations in 64
+bits: norm with the residual's addition, routing, gathering, the experts'
+packed products, the weighted way back.
+
+Tolerances follow from the number formats, half a step for every rounding (bf16
+2^-8, fp32 2^-24, e4m3 2^-4, relative).
+* norm: a sum of squares in fp32 goes through a chain of at most 32 terms and two
+  trees of 5, half of which counts after the root; the residual's addition, the
+  mean, the root, the division and two products add a rounding each: 2^-19.
+* weights of the picks: exp and the division are good to 2 steps, sums of at most
+  32 terms and a tree of 5 to 37; exp of a difference x has its rounding |x| times.
+* combine: k + 1 roundings of the sums' magnitudes.
+* products: the output's rounding 2^-8 |y|; the weights' rounding to bf16 where
+  the rows are many, 2^-8 sum |w x|; fp32 sums over K / 16 products of 16 and what
+  is behind them, 2^-23 (K/16 + 64) sum (|d sc q x| + |dmin m x|).
+* a gated product has the errors of both factors: |silu'| <= 1.1, silu(g) <= |g|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gguf_q4_dequant_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda(q4k):
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    torch.cuda.set_device(0)
+    q4k.q4k_init()
+    yield
+    torch.cuda.synchronize()
+    assert q4k.q4k_device_error() == 0
+
+
+def ints(v):
+    return torch.tensor(list(v), dtype=torch.int32, device=DEV)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def bits(t):
+    return t.cpu().view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t.cpu().contiguous().view(torch.uint8)
+
+
+# -------------------------------------------------------------------- norm ---
+
+def norm_ref(x, delta, w, eps):
+    r = x.double() + (0 if delta is None else delta.double())
+    return r, r / torch.sqrt(r.square().mean(1, keepdim=True) + eps) * w.double()
+
+
+def scale_bytes(y):
+    """log2(s) + 127 of the smallest power of two s >= 2^-127 with max|y| <= 448 s, per 32 columns of float32 y."""
+    top = y.double().abs().view(y.shape[0], -1, 32).amax(2)
+    e = torch.full(top.shape, -127.0, dtype=F64)
+    while True:
+        more = top > 448 * torch.exp2(e)
+        if not more.any():
+            return (e + 127).to(torch.uint8)
+        e = torch.where(more, e + 1, e)
+
+
+@pytest.mark.parametrize("T,C", [(1, 32), (3, 64), (5, 256), (2, 288), (7, 512), (4, 1024), (3, 1056), (130, 2048),
+                                 (1, 4096), (2, 5120), (3, 8192), (2, 8224), (2, 16384), (2, 16416), (1, 32768)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_norm(q4k, T, C, kind):
+    g = gen(T * 7 + C)
+    dt = torch.float32 if kind == "f32" else torch.bfloat16
+    x = (torch.randn(T, C, generator=g) * torch.exp(torch.randn(C, generator=g))).to(dt)
+    delta = torch.randn(T, C, generator=g) if T != 3 else None
+    w = torch.randn(C, generator=g)
+    r, y = norm_ref(x, delta, w, 1e-5)
+    d = None if delta is None else delta.to(DEV)
+    guard = 64
+    out = torch.full((T * C + guard,), float("nan"), device=DEV)
+    sum_ = torch.full((T * C + guard,), 7.0, device=DEV, dtype=dt)
+    codes = torch.full((T * C + guard,), 0xA5, dtype=torch.uint8, device=DEV)
+    scales = torch.full((T * C // 32 + guard,), 0xA5, dtype=torch.uint8, device=DEV)
+    q4k.q4k_add_norm(x.to(DEV), d, w.to(DEV), 1e-5, sum=sum_, out=out, codes=codes, scales=scales)
+    got = out[:T * C].view(T, C).cpu()
+    assert bool(((got.double() - y).abs() <= 2.0 ** -19 * y.abs()).all())
+    half = 2.0 ** -24 if kind == "f32" else 2.0 ** -24 + 2.0 ** -8
+    assert bool(((sum_[:T * C].view(T, C).cpu().double() - r).abs() <= half * r.abs()).all())
+    # the codes are those of the fp32 rows, bit for bit
+    sb = scale_bytes(got)
+    assert torch.equal(scales[:T * C // 32].view(T, -1).cpu(), sb)
+    v = got.double().view(T, -1, 32) * torch.exp2(127 - sb.double()).unsqueeze(2)
+    want = v.float().view(T, C).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(codes[:T * C].view(T, C).cpu(), want)
+    assert bool(out[T * C:].isnan().all()) and bool((sum_[T * C:] == 7).all())
+    assert bool((codes[T * C:] == 0xA5).all()) and bool((scales[T * C // 32:] == 0xA5).all())
+    # bf16 rows, in place
+    xd, ob = x.to(DEV), torch.empty(T, C, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_add_norm(xd, d, w.to(DEV), 1e-5, sum=xd, out=ob)
+    assert torch.equal(ob.cpu(), got.to(torch.bfloat16))
+    assert torch.equal(bits(xd), bits(sum_[:T * C].view(T, C)))
+
+
+def test_norm_special_rows(q4k):
+    C = 96
+    x = torch.zeros(6, C)
+    x[1] = 1e-30
+    x[2, 5] = float("inf")
+    x[3, 40] = float("nan")
+    x[4] = 448.0 * 2.0 ** torch.arange(C).div(32, rounding_mode="floor")
+    x[5, 3] = 3e38
+    w = torch.ones(C)
+    out = torch.empty(6, C, device=DEV)
+    codes = torch.empty(6, C, device=DEV, dtype=torch.float8_e4m3fn)
+    scales = torch.empty(6, C // 32, device=DEV, dtype=torch.uint8)
+    q4k.q4k_add_norm(x.to(DEV), None, w.to(DEV), 1e-6, out=out, codes=codes, scales=scales)
+    out, s = out.cpu(), scales.cpu()
+    assert bool((out[0] == 0).all()) and bool((s[0] == 0).all()) and bool((codes[0].cpu().float() == 0).all())
+    assert bool(((out[1] / 1e-27 - 1).abs() < 1e-5).all())
+    # an infinite residual: the infinity times 0 is NaN, the rest 0; a NaN: all NaN
+    assert bool(out[2, 5].isnan()) and bool((out[2, 32:] == 0).all()) and s[2].tolist() == [255, 0, 0]
+    assert bool(codes[2, :32].cpu().float().isnan().all()) and bool((codes[2, 32:].cpu().float() == 0).all())
+    assert bool(out[3].isnan().all()) and s[3].tolist() == [255] * 3
+    # sums of squares beyond fp32: the root is infinite and the row 0
+    assert bool((out[5] == 0).all())
+    assert s[4].tolist() == scale_bytes(out[4:5])[0].tolist()
+
+
+# ------------------------------------------------------------------- route ---
+
+def route_ref(logits, k, weighting, scale):
+    T, E = logits.shape
+    z = logits.double()
+    z = torch.where(z.isnan(), float("-inf"), z)
+    key, ids = torch.sort(z, dim=1, descending=True, stable=True)
+    key, ids = key[:, :k], ids[:, :k]
+    live = key > float("-inf")
+    top = key[:, :1]
+    rel = lambda x: torch.where(x == top, 1.0, torch.where(x > float("-inf"), torch.exp(x - top), 0.0))  # noqa: E731
+    if weighting in (0, 1):
+        w = rel(key)
+        total = (rel(z) if weighting == 0 else w).sum(1, keepdim=True)
+    else:
+        w = torch.sigmoid(key)
+        total = w.sum(1, keepdim=True) if weighting == 3 else torch.ones(T, 1, dtype=F64)
+    w = torch.where(live, w / total.clamp(min=1e-300), 0.0) * scale
+    ids = torch.where(live, ids, -1)
+    flat = ids.reshape(-1).numpy()
+    used = np.nonzero(flat >= 0)[0]
+    order = np.full(T * k, -1)
+    order[:len(used)] = used[np.argsort(flat[used], kind="stable")]
+    slots = np.full(T * k, -1)
+    slots[order[:len(used)]] = np.arange(len(used))
+    starts = np.concatenate([[0], np.cumsum(np.bincount(flat[used], minlength=E))])
+    return ids, w, order, slots.reshape(T, k), starts, key - top
+
+
+def route(q4k, logits, k, weighting, scale=1.0, pad=5):
+    T, E = logits.shape
+    n = T * k
+    outs = dict(ids=n, order=n, slots=n, starts=E + 1)
+    b = {m: torch.full((s + pad,), -77, dtype=torch.int32, device=DEV) for m, s in outs.items()}
+    w = torch.full((n + pad,), float("nan"), device=DEV)
+    ws = torch.full((q4k.q4k_route_workspace(T, E) + pad,), 0xEE, dtype=torch.uint8, device=DEV)
+    q4k.q4k_route(logits.to(DEV), k, weighting, scale, b["ids"], w, b["order"], b["slots"], b["starts"], ws)
+    for m, s in outs.items():
+        assert bool((b[m][s:] == -77).all()), m
+    assert bool(w[n:].isnan().all()) and bool((ws[-pad:] == 0xEE).all())
+    return (b["ids"][:n].view(T, k).cpu(), w[:n].view(T, k).cpu(), b["order"][:n].cpu(), b["slots"][:n].view(T, k).cpu(),
+            b["starts"][:E + 1].cpu())
+
+
+def check_route(q4k, logits, k, weighting, scale=1.0):
+    got = route(q4k, logits, k, weighting, scale)
+    ids, w, order, slots, starts, d = route_ref(logits, k, weighting, scale)
+    assert torch.equal(got[0].long(), ids)
+    assert got[2].tolist() == order.tolist() and got[3].tolist() == slots.tolist() and got[4].tolist() == starts.tolist()
+    d = torch.where(torch.isfinite(d), d.abs(), 0.0)
+    assert bool(((got[1].double() - w).abs() <= (2.0 ** -18 + 2.0 ** -23 * d) * w.abs() + 1e-37 * abs(scale)).all())
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (1, 128, 8), (2, 33, 3), (3, 64, 32), (48, 128, 8), (31, 61, 4),
+                                   (64, 1024, 32), (65, 1024, 32), (513, 32, 4), (700, 128, 8), (1003, 61, 4),
+                                   (4097, 256, 1), (2000, 512, 10), (130, 1000, 17)])
+@pytest.mark.parametrize("weighting", [0, 1, 2, 3])
+def test_route(q4k, T, E, k, weighting):
+    g = gen(T + E + k)
+    logits = torch.randn(T, E, generator=g) * 3
+    check_route(q4k, logits, k, weighting, 1.0 if weighting != 2 else 2.5)
+    # ties everywhere
+    check_route(q4k, torch.round(logits), k, weighting)
+    # experts and tokens that are masked, zeros of both signs
+    m = torch.round(logits)
+    m[torch.rand(T, E, generator=g) < 0.5] = float("-inf")
+    m[torch.rand(T, E, generator=g) < 0.1] = float("nan")
+    m[torch.rand(T, E, generator=g) < 0.2] = -0.0
+    m[:, ::7] = float("-inf")
+    if T > 2:
+        m[1] = float("-inf")
+        m[T - 1] = float("nan")
+    check_route(q4k, m, k, weighting)
+
+
+@pytest.mark.parametrize("T", [4, 900])
+def test_route_extreme_logits(q4k, T):
+    inf, big = float("inf"), 3.4e38
+    rows = torch.tensor([[inf, 1, inf, -big], [big, -big, 0, 1], [-big, -big, -big, -inf], [1e-45, -1e-45, 0.0, -0.0]])
+    logits = rows.repeat((T + 3) // 4, 1)[:T]
+    for weighting in range(4):
+        check_route(q4k, logits, 3, weighting)
+
+
+@pytest.mark.parametrize("T,E,k", [(5000, 2, 2), (3000, 7, 1)])
+def test_route_one_expert_takes_all(q4k, T, E, k):
+    logits = torch.zeros(T, E)
+    logits[:, E - 1] = 1
+    check_route(q4k, logits, k, 1)
+    logits[:, 0] = float("-inf")
+    check_route(q4k, logits, k, 1)
+
+
+# ------------------------------------------------------------------ gather ---
+
+@pytest.mark.parametrize("T,k,C,eight", [(1, 1, 8, False), (1, 8, 2048, False), (3, 2, 264, False), (37, 4, 4096, False),
+                                         (300, 8, 5120, False), (2, 1, 32768, False), (1, 3, 32, True),
+                                         (37, 4, 2080, True), (300, 8, 4096, True), (2, 2, 32768, True)])
+def test_gather(q4k, T, k, C, eight):
+    g = gen(T + C)
+    x = torch.randn(T, C, generator=g).to(torch.bfloat16)
+    scales = None
+    order = torch.randperm(T * k, generator=g).to(torch.int32)
+    order[torch.rand(T * k, generator=g) < 0.2] = -1
+    if T * k > 2:
+        order[0], order[1], order[2] = T * k, -(1 << 31), 0
+    if eight:
+        x = torch.randint(0, 256, (T, C), generator=g, dtype=torch.uint8)
+        x[(x & 127) == 127] = 5
+        scales = torch.randint(90, 160, (T, C // 32), generator=g, dtype=torch.uint8)
+        scales[0, 0] = 255
+        rows = (x.view(torch.float8_e4m3fn).double().view(T, -1, 32) * torch.exp2(scales.double() - 127).unsqueeze(2)).view(T, C)
+        rows[0, :32] = float("nan")
+        rows = rows.to(torch.bfloat16)
+    else:
+        rows = x
+    out = torch.full((T * k + 2, C), 3.0, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_experts_gather(x.to(DEV), order.to(DEV), k, out, scales=None if scales is None else scales.to(DEV))
+    want = torch.full((T * k + 2, C), 3.0, dtype=torch.bfloat16)
+    for p, i in enumerate(order.tolist()):
+        if 0 <= i < T * k:
+            want[p] = rows[i // k]
+    same = (out.cpu() == want) | (out.cpu().isnan() & want.isnan())
+    assert bool(same.all())
+
+
+def test_gather_smallest_scale(q4k):
+    x = torch.full((1, 32), 0x38, dtype=torch.uint8)  # 1.0
+    out = torch.empty(1, 32, dtype=torch.bfloat16, device=DEV)
+    for s in (0, 1, 254):
+        q4k.q4k_experts_gather(x.to(DEV), ints([0]), 1, out, scales=torch.full((1, 1), s, dtype=torch.uint8, device=DEV))
+        assert bool((out.double() == 2.0 ** (s - 127)).all())
+
+
+# ---------------------------------------------------------------- products ---
+
+def parts(W, N, K):
+    """d sc q and dmin m of every weight, in 64 bits."""
+    b = W.view(N, K // 256, 144).long()
+    half = W.view(N, K // 256, 144)[:, :, :4].contiguous().view(torch.float16).double()
+    s = b[:, :, 4:16]
+    sc = torch.cat([s[..., 0:4] & 63, (s[..., 8:12] & 15) | ((s[..., 0:4] >> 6) << 4)], -1).double()
+    mn = torch.cat([s[..., 4:8] & 63, (s[..., 8:12] >> 4) | ((s[..., 4:8] >> 6) << 4)], -1).double()
+    q = b[:, :, 16:].view(N, K // 256, 4, 32)
+    q = torch.stack([q & 15, q >> 4], 3).view(N, K // 256, 8, 32).double()
+    a = (half[..., 0:1] * sc).unsqueeze(-1) * q
+    m = (half[..., 1:2] * mn).unsqueeze(-1).expand_as(a)
+    return a.reshape(N, K), m.reshape(N, K)
+
+
+class Experts:
+    def __init__(self, seed, E, N, K):
+        self.E, self.N, self.K = E, N, K
+        self.w = torch.stack([synth.weight_rows(seed + e, N, K) for e in range(E)])
+        self.dev = self.w.to(DEV)
+
+    def product(self, e, x):
+        """x W_e^T and its bound."""
+        a, m = parts(self.w[e].reshape(self.N, -1), self.N, self.K)
+        x = x.double()
+        y = x @ (a - m).T
+        tol = 2.0 ** -8 * (x.abs() @ (a - m).abs().T) + 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ (a + m).T)
+        return y, tol
+
+
+def check_experts(q4k, E, N, K, counts, gated, seed=0, lead=0, scale=1.0):
+    up = Experts(seed + 5000, E, N, K) if gated else None
+    w = Experts(seed, E, N, K)
+    P = lead + sum(counts) + 3
+    g = gen(seed + P)
+    x = (torch.randn(P, K, generator=g) * (0.02 if gated else 1.0) * scale).to(torch.bfloat16)
+    x[lead + sum(counts):] = float("nan")  # rows of no expert
+    starts = [lead]
+    for c in counts:
+        starts.append(starts[-1] + c)
+    sentinel = torch.tensor(-12345.0).to(torch.bfloat16)
+    y = torch.full((P + 1, N), -12345.0, dtype=torch.bfloat16, device=DEV)
+    if gated:
+        q4k.q4k_experts_gated(w.dev, up.dev, N, K, x.to(DEV), ints(starts), y)
+    else:
+        q4k.q4k_experts_matmul(w.dev, N, K, x.to(DEV), ints(starts), y)
+    y = y.cpu()
+    assert bool((y[:lead] == sentinel).all()) and bool((y[starts[-1]:] == sentinel).all())
+    worst = 0.0
+    for e in range(E):
+        a, b = starts[e], starts[e + 1]
+        if a == b:
+            continue
+        want, tol = w.product(e, x[a:b])
+        if gated:
+            u, tu = up.product(e, x[a:b])
+            silu = want * torch.sigmoid(want)
+            want = silu * u
+            tol = 1.1 * tol * u.abs() + silu.abs() * tu + 1.1 * tol * tu + 2.0 ** -20 * want.abs()
+        tol = tol + 2.0 ** -8 * want.abs() + 1e-38
+        worst = max(worst, float(((y[a:b].double() - want).abs() / tol).max()))
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,N,K,counts", [
+    (1, 32, 256, [1]), (1, 1, 256, [1]), (1, 7, 512, [3]), (2, 33, 256, [0, 8]), (2, 32, 256, [9, 0]),
+    (3, 130, 768, [1, 7, 2]), (4, 64, 2048, [1, 0, 1, 1]), (4, 50, 2304, [5, 6, 7, 8]), (3, 36, 4352, [2, 1, 4]),
+    (5, 16, 512, [0, 0, 3, 0, 0]), (2, 96, 1024, [16, 11]), (2, 100, 768, [17, 20]), (3, 61, 1280, [32, 1, 33]),
+    (2, 128, 512, [64, 65]), (4, 129, 256, [100, 0, 1, 31])])
+def test_experts_small(q4k, E, N, K, counts, gated):
+    check_experts(q4k, E, N, K, counts, gated, seed=E * N + K, lead=2 if N % 2 else 0)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,N,K,counts", [
+    (2, 128, 512, [128, 127]), (2, 257, 256, [300, 129]), (3, 192, 768, [256, 1, 512]), (2, 64, 2048, [700, 15]),
+    (4, 100, 512, [0, 1000, 0, 3]), (1, 384, 1024, [513])])
+def test_experts_many_rows(q4k, E, N, K, counts, gated):
+    check_experts(q4k, E, N, K, counts, gated, seed=E * N + K + 1, lead=3 if N % 2 else 0)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 40])
+def test_experts_scale_of_rows(q4k, scale):
+    check_experts(q4k, 2, 40, 512, [3, 9], False, seed=3, scale=scale)
+    check_experts(q4k, 2, 40, 512, [200, 90], False, seed=3, scale=scale)
+
+
+def test_experts_rows_with_infinity(q4k):
+    """A row with an infinity or a NaN spoils no other row."""
+    for counts in ([4, 5], [130, 200]):
+        P, N, K = sum(counts), 64, 512
+        w = Experts(9, 2, N, K)
+        x = torch.randn(P, K, generator=gen(1)).to(torch.bfloat16)
+        clean, dirty = (torch.empty(P, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        starts = ints([0, counts[0], P])
+        q4k.q4k_experts_matmul(w.dev, N, K, x.to(DEV), starts, clean)
+        x[1, 7], x[counts[0], 3] = float("inf"), float("nan")
+        q4k.q4k_experts_matmul(w.dev, N, K, x.to(DEV), starts, dirty)
+        keep = torch.ones(P, dtype=torch.bool)
+        keep[1] = keep[counts[0]] = False
+        assert torch.equal(clean.cpu()[keep], dirty.cpu()[keep])
+        assert not bool(torch.isfinite(dirty[counts[0]]).any())
+
+
+def test_experts_starts_out_of_range(q4k):
+    """Whatever starts holds, nothing outside the rows is written."""
+    N, K, P = 40, 256, 20
+    w = Experts(4, 4, N, K)
+    x = torch.randn(P, K, generator=gen(2)).to(torch.bfloat16).to(DEV)
+    for starts in ([-5, 4, 2, 9, 1 << 30], [1 << 30] * 5, [-(1 << 31)] * 5, [20, 10, 5, 2, 0], [0, 30, 3, 30, 12]):
+        y = torch.full((P + 8, N), 5.0, dtype=torch.bfloat16, device=DEV)
+        q4k.q4k_experts_matmul(w.dev, N, K, x, ints(starts), y)
+        assert bool((y[P:] == 5).all()) and bool(torch.isfinite(y).all())
+    # values that come down are taken as the highest before them
+    y = torch.full((P, N), 5.0, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_experts_matmul(w.dev, N, K, x, ints([-5, 4, 2, 9, 1 << 30]), y)
+    same = torch.full((P, N), 5.0, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_experts_matmul(w.dev, N, K, x, ints([0, 4, 4, 9, 20]), same)
+    assert torch.equal(y, same)
+
+
+def test_experts_many_experts(q4k):
+    """1024 experts, some with rows; more than a block's first pass over them."""
+    E, N, K = 1024, 8, 256
+    counts = [(e * 7919) % 5 if e % 3 else 0 for e in range(E)]
+    w = Experts(11, 8, N, K)
+    dev = w.w.repeat(E // 8, 1, 1).to(DEV)
+    P = sum(counts)
+    x = torch.randn(P, K, generator=gen(3)).to(torch.bfloat16)
+    starts = np.concatenate([[0], np.cumsum(counts)])
+    y = torch.zeros(P, N, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_experts_matmul(dev, N, K, x.to(DEV), ints(starts.tolist()), y)
+    y = y.cpu().double()
+    for e in range(E):
+        a, b = starts[e], starts[e + 1]
+        if a < b:
+            want, tol = w.product(e % 8, x[a:b])
+            assert bool(((y[a:b] - want).abs() <= tol + 2.0 ** -8 * want.abs()).all())
+
+
+# ----------------------------------------------------------------- combine ---
+
+@pytest.mark.parametrize("T,k,C", [(1, 1, 8), (1, 8, 2048), (3, 2, 24), (5, 32, 264), (37, 8, 4096), (64, 9, 5120),
+                                   (2, 3, 32768), (1000, 4, 72)])
+@pytest.mark.parametrize("base", [False, True])
+def test_combine(q4k, T, k, C, base):
+    g = gen(T + C)
+    P = T * k
+    y = torch.randn(P, C, generator=g).to(torch.bfloat16)
+    slots = torch.randperm(P, generator=g).to(torch.int32).view(T, k)
+    w = torch.randn(T, k, generator=g)
+    gone = torch.rand(T, k, generator=g) < 0.2
+    slots[gone] = -1
+    if T > 1:
+        slots[1] = torch.tensor([P, 1 << 30, -(1 << 31), -1] * 8)[:k]  # a token with nothing
+        w[1] = float("nan")
+    b = torch.randn(T, C, generator=g) if base else None
+    out = torch.full((T + 1, C), 7.0, device=DEV)
+    if base:
+        out[:T] = b.to(DEV)
+    q4k.q4k_experts_combine(y.to(DEV), slots.to(DEV), w.to(DEV), out, base=out if base else None)
+    live = (slots >= 0) & (slots < P)
+    terms = torch.where(live.unsqueeze(2), w.double().unsqueeze(2) * y.double()[slots.long().clamp(0, P - 1)], 0.0)
+    want = terms.sum(1) + (b.double() if base else 0)
+    size = terms.abs().sum(1) + (b.double().abs() if base else 0)
+    got = out.cpu().double()
+    assert bool(((got[:T] - want).abs() <= 2.0 ** -24 * (k + 1) * size).all())
+    assert bool((got[T:] == 7).all())
