@@ -87,34 +87,7 @@ __global__ void __launch_bounds__(32 * kExWarps, NB == 4 ? 1 : 2)
     // and the row tiles before each expert
     for (int e = threadIdx.x; e <= rows.experts; e += blockDim.x) starts[e] = min(max(rows.starts[e], 0), rows.pairs);
     __syncthreads();
-    if (warp == 0) {
-        int run = 0, high = 0;
-        for (int e0 = 0; e0 <= rows.experts; e0 += 32) {
-            const int e = e0 + lane;
-            int hi = e <= rows.experts ? starts[e] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, hi, o);
-                if (lane >= o) hi = max(hi, t);
-            }
-            hi = max(hi, high);
-            int prev = __shfl_up_sync(0xffffffffu, hi, 1);
-            if (lane == 0) prev = high;
-            // tiles of expert e - 1, whose rows end at starts[e]
-            int s = e > 0 && e <= rows.experts ? (hi - prev + NT - 1) / NT : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += t;
-            }
-            if (e <= rows.experts) {
-                starts[e] = hi;
-                tiles[e] = run + s;
-            }
-            run += __shfl_sync(0xffffffffu, s, 31);
-            high = __shfl_sync(0xffffffffu, hi, 31);
-        }
-    }
+    if (warp == 0) expert_tiles<NT>(starts, tiles, rows.experts, lane);
     __syncthreads();
     const int slabs = (N + kSlab - 1) / kSlab;
     const int64_t units = static_cast<int64_t>(tiles[rows.experts]) * slabs;
@@ -123,12 +96,7 @@ __global__ void __launch_bounds__(32 * kExWarps, NB == 4 ? 1 : 2)
     // A unit: its expert by bisection, then (column slab, row tile), the row tiles
     // of a slab side by side so that its words come from memory once.
     auto unit_of = [&](int64_t u, int& e, int& n0, int& p0, int& p1) {
-        int lo = 0, hi = rows.experts;  // tiles[lo] * slabs <= u < tiles[hi] * slabs
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (static_cast<int64_t>(tiles[mid]) * slabs <= u) lo = mid; else hi = mid;
-        }
-        e = lo;
+        e = expert_of(tiles, rows.experts, static_cast<int>(u / slabs));
         const int mt = tiles[e + 1] - tiles[e];
         const int in = static_cast<int>(u - static_cast<int64_t>(tiles[e]) * slabs);
         n0 = in / mt * kSlab;
@@ -366,7 +334,7 @@ cudaError_t setup_nb() {
 }  // namespace
 
 cudaError_t experts_setup(DeviceInfo&) {
-    cudaError_t e = cudaSuccess, r;
+    cudaError_t e = experts_gemm_setup(), r;
     if ((r = setup_nb<1, false>()) != cudaSuccess) e = r;
     if ((r = setup_nb<2, false>()) != cudaSuccess) e = r;
     if ((r = setup_nb<4, false>()) != cudaSuccess) e = r;
@@ -380,6 +348,7 @@ cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t stream, const Devic
     // rows of x that an expert with rows has, if they are spread evenly
     const double mean = static_cast<double>(a.rows.pairs) / (a.rows.pairs < a.rows.experts ? a.rows.pairs : a.rows.experts);
     const bool gated = a.W2 != nullptr;
+    if (mean > 24.0) return launch_experts_gemm(a, stream, dev, pdl);
     if (mean <= 5.0) return gated ? launch_nb<1, true>(a, stream, dev, pdl) : launch_nb<1, false>(a, stream, dev, pdl);
     if (mean <= 12.0) return gated ? launch_nb<2, true>(a, stream, dev, pdl) : launch_nb<2, false>(a, stream, dev, pdl);
     return gated ? launch_nb<4, true>(a, stream, dev, pdl) : launch_nb<4, false>(a, stream, dev, pdl);

@@ -22,6 +22,51 @@ struct ExpertRows {
     int experts, pairs;
 };
 
+#ifdef __CUDACC__
+// The row tiles (of up to NT rows) of every expert, by one warp: starts[0 .. E]
+// (shared memory, inside [0, pairs] whatever the caller's array held) are made
+// ascending, tiles[e] becomes the number of tiles before expert e, tiles[E] of all.
+template <int NT>
+__device__ __forceinline__ void expert_tiles(int* starts, int* tiles, int E, int lane) {
+    int run = 0, high = 0;
+    for (int e0 = 0; e0 <= E; e0 += 32) {
+        const int e = e0 + lane;
+        int hi = e <= E ? starts[e] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, hi, o);
+            if (lane >= o) hi = max(hi, t);
+        }
+        hi = max(hi, high);
+        int prev = __shfl_up_sync(0xffffffffu, hi, 1);
+        if (lane == 0) prev = high;
+        // the tiles of expert e - 1, whose rows end at starts[e]
+        int s = e > 0 && e <= E ? (hi - prev + NT - 1) / NT : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += t;
+        }
+        if (e <= E) {
+            starts[e] = hi;
+            tiles[e] = run + s;
+        }
+        run += __shfl_sync(0xffffffffu, s, 31);
+        high = __shfl_sync(0xffffffffu, hi, 31);
+    }
+}
+
+// The expert of row tile `tile` < tiles[E]: the last e with tiles[e] <= tile.
+__device__ __forceinline__ int expert_of(const int* tiles, int E, int tile) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles[mid] <= tile) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+#endif
+
 struct NormArgs {
     const void* x;
     const float* delta;
@@ -79,6 +124,8 @@ struct ExpertArgs {
 };
 cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
 cudaError_t experts_setup(DeviceInfo& dev);
+cudaError_t launch_experts_gemm(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
+cudaError_t experts_gemm_setup();
 
 // A 2-D byte map {K/256*144, N} of packed rows, box one super-block of `rows` rows
 // (a q4k_status; cached per host thread).
