@@ -279,10 +279,10 @@ __global__ void __launch_bounds__(32 * kExWarps, NB == 4 ? 1 : 2)
                 }
             }
             if (kGated) {
-                s.x = s.x / (1.f + expf(-s.x)) * v.x;
-                s.y = s.y / (1.f + expf(-s.y)) * v.y;
-                s.z = s.z / (1.f + expf(-s.z)) * v.z;
-                s.w = s.w / (1.f + expf(-s.w)) * v.w;
+                s.x = silu(s.x) * v.x;
+                s.y = silu(s.y) * v.y;
+                s.z = silu(s.z) * v.z;
+                s.w = silu(s.w) * v.w;
             }
             const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
             const uint2 o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));

@@ -56,6 +56,11 @@ __device__ __forceinline__ void expert_tiles(int* starts, int* tiles, int E, int
     }
 }
 
+// g / (1 + exp(-g)) with the fast exponential and division (a few units in the
+// last place of fp32, for a result that is rounded to bf16); 0 where exp(-g)
+// overflows.
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+
 // The expert of row tile `tile` < tiles[E]: the last e with tiles[e] <= tile.
 __device__ __forceinline__ int expert_of(const int* tiles, int E, int tile) {
     int lo = 0, hi = E;

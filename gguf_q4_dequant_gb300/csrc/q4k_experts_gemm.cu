@@ -3,7 +3,7 @@
 // matrices) with its own rows of x.
 //
 // Y^T = W X^T as in the dense GEMM: the MMA's A operand is 128 weight rows,
-// dequantised to bf16 in shared memory, its B operand up to 256 rows of x, the
+// dequantised to bf16 in TMEM, its B operand up to 192 rows of x, the
 // accumulator 128 TMEM lanes x the rows of x. A unit is (expert, rows of x,
 // 128 weight rows); of a gated product the 128 are 64 gate and 64 up rows,
 // sixteen and sixteen in turn, so that the two factors of an output lie in one
@@ -14,11 +14,11 @@
 // of one another through rings, from one unit into the next:
 //   warp 0       W producer: {144 B, 128 rows} of packed words per 256 k (TMA)
 //   warp 1       MMA issuer, TMEM (two accumulators: a unit's end overlaps the next)
-//   warp 2       X producer: the tile's rows x 64 k (TMA, 128-byte swizzle)
+//   warp 2       X producer: the tile's rows x 128 k (TMA, 128-byte swizzle)
 //   warps 4..7   the end of a unit: TMEM -> registers -> (silu(g) u) -> bf16 -> Y
 //   warps 8..23  dequantisers, four groups of 128 threads: group c has the 64 k
-//                chunk c of every super-block, thread r of it weight row r, and
-//                the A stage c of the ring
+//                chunk c of every super-block, thread r of it a weight row, and
+//                32 columns of TMEM: half the A operand of a step of 128 k
 // All waits are bounded (see mbar_wait).
 #include <cuda_bf16.h>
 
@@ -29,28 +29,30 @@
 namespace q4k {
 
 constexpr int kEgBM = 128;                    // weight rows of a unit
-constexpr int kEgBN = 256;                    // rows of x of a unit at most
-constexpr int kEgStep = 64;                   // k of an MMA step
-constexpr int kEgAStages = 4, kEgXStages = 3, kEgWStages = 3;
-constexpr int kEgAStage = kEgBM * 128;
-constexpr int kEgXStage = kEgBN * 128;
+constexpr int kEgBN = 192;                    // rows of x of a unit at most
+// k of a step, the work of one commit: a commit and its wait take the issuing warp
+// some 320 cycles whatever they cover, the eight MMAs of a step 4 cycles a row of x
+constexpr int kEgStep = 128;
+constexpr int kEgAStages = 2, kEgXStages = 3, kEgWStages = 4;
+constexpr int kEgXHalf = kEgBN * 128;         // 64 k of the rows of x
+constexpr int kEgXStage = 2 * kEgXHalf;
 constexpr int kEgWStage = kEgBM * kBlockBytes;
 constexpr int kEgEpiWarp = 4, kEgDeqWarp = 8, kEgDeqWarps = 16;
 constexpr int kEgThreads = 32 * (kEgDeqWarp + kEgDeqWarps);
-constexpr int kEgOffX = kEgAStages * kEgAStage;
-constexpr int kEgOffW = kEgOffX + kEgXStages * kEgXStage;
+constexpr int kEgOffW = kEgXStages * kEgXStage;
 constexpr int kEgOffBar = kEgOffW + kEgWStages * kEgWStage;
-// w_full, w_empty, x_full, x_empty, a_full, a_empty, acc_full[2], acc_empty[2], done
-constexpr int kEgBars = 2 * (kEgWStages + kEgXStages + kEgAStages) + 5;
+// w_full, w_empty, x_full, a_full, done (of a step's MMAs), acc_full[2], acc_empty[2], end
+constexpr int kEgBars = 2 * (kEgWStages + kEgXStages) + kEgAStages + 5;
 constexpr int kEgOffTmem = kEgOffBar + 8 * kEgBars;
 constexpr int kEgOffTab = (kEgOffTmem + 8 + 15) / 16 * 16;
-constexpr uint32_t kEgTmemCols = 2 * kEgBN;
+constexpr uint32_t kEgTmemCols = 512, kEgTmemA = 2 * kEgBN;  // the accumulators, then 64 columns a stage of A
+static_assert(kEgTmemA + 64 * kEgAStages <= kEgTmemCols, "TMEM");
 
 __host__ __device__ constexpr int eg_smem(int experts) { return kEgOffTab + 8 * (experts + 1) + 1024; }
 static_assert(eg_smem(kMaxExperts) <= 232448, "shared memory per CTA");
 
 struct XMaps {
-    CUtensorMap box[4];  // boxes of 64, 128, 192 and 256 rows x 64 k
+    CUtensorMap box[kEgBN / 32];  // boxes of 32, 64, .. rows x 64 k
 };
 
 template <bool kGated>
@@ -66,18 +68,18 @@ __global__ void __launch_bounds__(kEgThreads, 1)
     const uint32_t sbase = raw + pad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bwf = sbase + kEgOffBar, bwe = bwf + 8 * kEgWStages, bxf = bwe + 8 * kEgWStages,
-                   bxe = bxf + 8 * kEgXStages, baf = bxe + 8 * kEgXStages, bae = baf + 8 * kEgAStages,
-                   bcf = bae + 8 * kEgAStages, bce = bcf + 16, bdone = bce + 16;
+                   baf = bxf + 8 * kEgXStages, bdone = baf + 8 * kEgAStages,
+                   bcf = bdone + 8 * kEgXStages, bce = bcf + 16, bend = bce + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kEgOffTmem);
     int* starts = reinterpret_cast<int*>(smem + kEgOffTab);
     int* tiles = starts + rows.experts + 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kEgWStages; ++i) mbar_init(bwf + 8 * i, 1), mbar_init(bwe + 8 * i, kEgDeqWarps);
-        for (int i = 0; i < kEgXStages; ++i) mbar_init(bxf + 8 * i, 1), mbar_init(bxe + 8 * i, 1);
-        for (int i = 0; i < kEgAStages; ++i) mbar_init(baf + 8 * i, kEgDeqWarps / 4), mbar_init(bae + 8 * i, 1);
+        for (int i = 0; i < kEgXStages; ++i) mbar_init(bxf + 8 * i, 1), mbar_init(bdone + 8 * i, 1);
+        for (int i = 0; i < kEgAStages; ++i) mbar_init(baf + 8 * i, kEgDeqWarps / 2);
         for (int i = 0; i < 2; ++i) mbar_init(bcf + 8 * i, 1), mbar_init(bce + 8 * i, 4);
-        mbar_init(bdone, 1);
+        mbar_init(bend, 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
         r.e = expert_of(tiles, rows.experts, tile);
         r.n0 = static_cast<int>(u % ntiles) * kCols;
         const int all = starts[r.e + 1] - starts[r.e], mt = tiles[r.e + 1] - tiles[r.e];
-        const int h = ((all + mt - 1) / mt + 15) & ~15;  // <= 256
+        const int h = ((all + mt - 1) / mt + 15) & ~15;  // <= kEgBN
         const int off = (tile - tiles[r.e]) * h;
         r.p0 = starts[r.e] + off;
         r.rows = max(0, min(h, all - off));
@@ -148,13 +150,17 @@ __global__ void __launch_bounds__(kEgThreads, 1)
             bool ok = true;
             for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const Unit w = unit_of(u);
-                const int q = (max(w.rows, 1) - 1) / 64;  // a box of 64 (q + 1) rows
-                const uint32_t bytes = 64u * 128u * (q + 1);
-                for (int ks = 0; ks < 4 * KB; ++ks, ++it) {
+                const int q = (max(w.rows, 1) - 1) / 32;  // a box of 32 (q + 1) rows
+                const uint32_t bytes = 2u * 32u * 128u * (q + 1);
+                for (int ks = 0; ks < 2 * KB; ++ks, ++it) {
                     const uint32_t s = it % kEgXStages;
-                    if (!mbar_wait(bxe + 8 * s, ((it / kEgXStages) & 1) ^ 1, err)) { ok = false; break; }
+                    // free once the MMAs of step it - kEgXStages are done (that barrier's next phase
+                    // is step it's own: no wait finds its barrier two phases on)
+                    if (it >= kEgXStages && !mbar_wait(bdone + 8 * s, (it / kEgXStages - 1) & 1, err)) { ok = false; break; }
                     mbar_arrive_expect_tx(bxf + 8 * s, bytes);
-                    tma_load_2d_hint(sbase + kEgOffX + s * kEgXStage, &mapX.box[q], ks * kEgStep, w.p0, bxf + 8 * s, pol);
+                    const uint32_t dst = sbase + s * kEgXStage;
+                    tma_load_2d_hint(dst, &mapX.box[q], ks * kEgStep, w.p0, bxf + 8 * s, pol);
+                    tma_load_2d_hint(dst + kEgXHalf, &mapX.box[q], ks * kEgStep + 64, w.p0, bxf + 8 * s, pol);
                 }
             }
             if (!ok)
@@ -163,6 +169,8 @@ __global__ void __launch_bounds__(kEgThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
+        // the whole warp goes through the loop, so that addresses and descriptors stay
+        // the warp's own; one lane issues
         uint32_t it = 0, n = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
@@ -170,36 +178,34 @@ __global__ void __launch_bounds__(kEgThreads, 1)
             const uint32_t idesc = idesc_bf16_f32(kEgBM, max(16, (w.rows + 15) & ~15));
             const uint32_t d = tmem + (n & 1) * kEgBN;
             if (!__all_sync(0xffffffffu, mbar_wait(bce + 8 * (n & 1), ((n >> 1) & 1) ^ 1, err))) break;
-            tc_fence_after();
-            for (int ks = 0; ks < 4 * KB; ++ks, ++it) {
+            for (int ks = 0; ks < 2 * KB; ++ks, ++it) {
                 const uint32_t sa = it % kEgAStages, sx = it % kEgXStages;
                 const bool in = mbar_wait(bxf + 8 * sx, (it / kEgXStages) & 1, err) &&
                                 mbar_wait(baf + 8 * sa, (it / kEgAStages) & 1, err);
                 if (!__all_sync(0xffffffffu, in)) { ok = false; break; }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t a0 = sw128_desc(sbase + sa * kEgAStage);
-                    const uint64_t b0 = sw128_desc(sbase + kEgOffX + sx * kEgXStage);
+                    const uint32_t a0 = tmem + kEgTmemA + 64 * sa;
+                    const uint64_t b0 = sw128_desc(sbase + sx * kEgXStage);
 #pragma unroll
-                    for (int kk = 0; kk < kEgStep / 16; ++kk) tc_mma_bf16(d, a0 + 2 * kk, b0 + 2 * kk, idesc, ks != 0 || kk != 0);
-                    tc_commit(bae + 8 * sa);
-                    tc_commit(bxe + 8 * sx);
-                    if (ks == 4 * KB - 1) tc_commit(bcf + 8 * (n & 1));
+                    for (int kk = 0; kk < kEgStep / 16; ++kk)
+                        tc_mma_bf16_ts(d, a0 + 8 * kk, b0 + (kk >> 2) * (kEgXHalf >> 4) + 2 * (kk & 3), idesc, ks != 0 || kk != 0);
+                    tc_commit(bdone + 8 * sx);
+                    if (ks == 2 * KB - 1) tc_commit(bcf + 8 * (n & 1));
                 }
                 __syncwarp();
             }
         }
-        if (elect_one()) tc_commit(bdone);
+        if (elect_one()) tc_commit(bend);
         __syncwarp();
     } else if (warp >= kEgDeqWarp) {
         const int t = threadIdx.x - 32 * kEgDeqWarp;
-        const int r = t & (kEgBM - 1);
         const int c = t >> 7;
-        // the row of A: of a gated unit 16 gate rows, then the 16 up rows that go with them
-        const int i = r & 63;
-        const int ra = kGated ? (i >> 4) * 32 + (r >> 6) * 16 + (i & 15) : r;
-        uint8_t* arow = smem + c * kEgAStage + ra * 128;
-        const int sw = ra & 7;
+        // the TMEM lane of this thread, and the row of packed words that goes there: of a gated
+        // unit 16 gate rows, then the 16 up rows that go with them
+        const int ra = t & (kEgBM - 1);
+        const int r = kGated ? (ra & 16) * 4 + (ra >> 5) * 16 + (ra & 15) : ra;
+        const uint32_t a_tmem = tmem + kEgTmemA + 32 * c + (static_cast<uint32_t>(ra & ~31) << 16);
         // 0, read from shared memory so that the compiler cannot see through the
         // dependence that is built from it below
         const uint32_t zero = *reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
             for (int sb = 0; sb < KB; ++sb, ++it) {
                 const uint32_t s = it % kEgWStages;
-                if (!mbar_wait(bwf + 8 * s, (it / kEgWStages) & 1, err)) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, mbar_wait(bwf + 8 * s, (it / kEgWStages) & 1, err))) { ok = false; break; }
                 const uint8_t* P = smem + kEgOffW + s * kEgWStage + r * kBlockBytes;
                 const uint4 hd = *reinterpret_cast<const uint4*>(P);
                 const ulonglong2 qa = *reinterpret_cast<const ulonglong2*>(P + 16 + 32 * c);
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
                 const ScaleBytes scb = decode_scales(hd.y, hd.z, hd.w);
                 const float d = half_lo(hd.x), dmin = half_hi(hd.x);
                 const uint64_t qw[4] = {qa.x, qa.y, qb.x, qb.y};
-                uint4 o[2][4];
+                uint32_t o[32];  // the row's 64 k, two to a column
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int j = 2 * c + hh;
@@ -232,16 +238,28 @@ __global__ void __launch_bounds__(kEgThreads, 1)
                     const float d1s0 = d1 * exp2i(-4 * hh), d1s1 = d1 * exp2i(-8 - 4 * hh);
                     const uint64_t D0 = pack2(d1s0, d1s0), D1 = pack2(d1s1, d1s1), NM = pack2(-m1, -m1);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) o[hh][v] = dequant8x(qw[v], hh, D0, D1, NM);
+                    for (int v = 0; v < 4; ++v) {
+                        const uint4 w = dequant8x(qw[v], hh, D0, D1, NM);
+                        o[16 * hh + 4 * v] = w.x;
+                        o[16 * hh + 4 * v + 1] = w.y;
+                        o[16 * hh + 4 * v + 2] = w.z;
+                        o[16 * hh + 4 * v + 3] = w.w;
+                    }
                 }
-                if (!mbar_wait(bae + 8 * c, (it & 1) ^ 1, err)) { ok = false; break; }
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(arow + (((4 * hh + v) ^ sw) << 4)) = o[hh][v];
-                fence_proxy_async_smem();
+                // the stage is free once the MMAs of two steps before are done (the barrier's next
+                // phase is a step behind this one's: it cannot be further)
+                const uint32_t step = 2 * it + (c >> 1), was = step - kEgAStages;
+                if (step >= kEgAStages &&
+                    !__all_sync(0xffffffffu, mbar_wait(bdone + 8 * (was % kEgXStages), (was / kEgXStages) & 1, err))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_st_32x32b_x32(a_tmem, o);
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(baf + 8 * c);
+                if (lane == 0) mbar_arrive(baf + 8 * (c >> 1));
             }
         }
     } else if (warp >= kEgEpiWarp) {
@@ -252,31 +270,30 @@ __global__ void __launch_bounds__(kEgThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(bcf + 8 * (n & 1), (n >> 1) & 1, err))) break;
             tc_fence_after();
             const uint32_t acc = tmem + (n & 1) * kEgBN + (static_cast<uint32_t>(32 * q) << 16);
+            // gated: lane i < 16 has gate row i, lane i + 16 the up row of the same column: they
+            // swap one value for two rows of x, and each has one output
+            const int col = w.n0 + (kGated ? 16 * q + (lane & 15) : 32 * q + lane);
+            uint16_t* y = Y + static_cast<int64_t>(w.p0 + (kGated ? lane >> 4 : 0)) * N + col;
             for (int c0 = 0; c0 < w.rows; c0 += 32) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(acc + c0, v);
                 tmem_ld_wait();
+                const int left = col < N ? w.rows - c0 : 0;
                 if (kGated) {
-                    // lane i < 16 has gate row i, lane i + 16 the up row of the same
-                    // column: they swap one value for two rows of x, and each has one output
-                    const int col = w.n0 + 16 * q + (lane & 15);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float mine = __uint_as_float(lane < 16 ? v[j] : v[j + 1]);
                         const float away = __uint_as_float(__shfl_xor_sync(0xffffffffu, lane < 16 ? v[j + 1] : v[j], 16));
-                        const float g = lane < 16 ? mine : away, up = lane < 16 ? away : mine;
-                        const float y = g / (1.f + expf(-g)) * up;
-                        const int row = c0 + j + (lane >> 4);
-                        if (row < w.rows && col < N)
-                            Y[static_cast<int64_t>(w.p0 + row) * N + col] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                        const uint16_t o = __bfloat16_as_ushort(__float2bfloat16_rn(lane < 16 ? silu(mine) * away : silu(away) * mine));
+                        if (j + (lane >> 4) < left) *y = o;
+                        y += 2 * N;
                     }
                 } else {
-                    const int col = w.n0 + 32 * q + lane;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j < w.rows && col < N)
-                            Y[static_cast<int64_t>(w.p0 + c0 + j) * N + col] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+                    for (int j = 0; j < 32; ++j) {
+                        if (j < left) *y = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+                        y += N;
+                    }
                 }
             }
             tc_fence_before();
@@ -287,7 +304,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
-        mbar_wait(bdone, 0, err);  // no MMA is under way when the accumulators are given back
+        mbar_wait(bend, 0, err);  // no MMA is under way when the accumulators are given back
         tc_fence_after();
         tmem_dealloc(tmem, kEgTmemCols);
     }
@@ -306,8 +323,8 @@ cudaError_t launch_gated(const ExpertArgs& a, cudaStream_t stream, const DeviceI
     if (kGated && weight_map(&mapW2, a.W2, a.rows.experts * a.N, a.K, cols) != Q4K_OK) return cudaErrorInvalidValue;
     XMaps mapX;
     const uint64_t dims[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.rows.pairs)}, strides[1] = {2ull * a.K};
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t box[2] = {kEgStep, 64u * (i + 1)};
+    for (int i = 0; i < kEgBN / 32; ++i) {
+        const uint32_t box[2] = {64, 32u * (i + 1)};
         if (!encode_bf16_sw128(&mapX.box[i], a.X, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
     const int64_t busy = a.rows.pairs < a.rows.experts ? a.rows.pairs : a.rows.experts;
