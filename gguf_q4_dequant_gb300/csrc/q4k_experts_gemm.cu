@@ -55,6 +55,28 @@ struct XMaps {
     CUtensorMap box[kEgBN / 32];  // boxes of 32, 64, .. rows x 64 k
 };
 
+// Eight weights of one nibble half (hh) from the qs words w0 and w1, as bf16 pairs.
+// A nibble at bit s of a word, under the bits of 1.0, is the float 1 + q 2^(s-23),
+// and d1 q - m1 = (1 + q 2^(s-23)) E - (E + m1) with E = d1 2^(23-s): one masking
+// and half a paired FMA a weight. The constant's rounding, 2^-24 E, is 2^-8 d1
+// at most (s >= 7) and mostly far less, beside the rounding to 8 significant bits
+// that the weight meets anyway. Bytes 0 and 1 are brought to bits 7 and 15, bytes
+// 2 and 3 too. E0, C0 and E1, C1: (E, E) and -(E + m1, E + m1) for s = 7 + 4 hh and 15 + 4 hh.
+__device__ __forceinline__ void dequant8(uint32_t w0, uint32_t w1, int hh, uint64_t E0, uint64_t C0, uint64_t E1,
+                                         uint64_t C1, uint32_t* o) {
+    const uint32_t one = 0x3F800000u, m0 = 0x780u << (4 * hh), m1 = 0x78000u << (4 * hh);
+    const uint32_t u0 = w0 << 7, u1 = w1 << 7, v0 = w0 >> 9, v1 = w1 >> 9;
+    auto two = [&](uint32_t a, uint32_t b, uint32_t m) {
+        return static_cast<uint64_t>((a & m) | one) | static_cast<uint64_t>((b & m) | one) << 32;
+    };
+    const float2 a = unpack2(fma2(two(u0, u1, m0), E0, C0)), b = unpack2(fma2(two(u0, u1, m1), E1, C1));
+    const float2 c = unpack2(fma2(two(v0, v1, m0), E0, C0)), d = unpack2(fma2(two(v0, v1, m1), E1, C1));
+    const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(a.x, b.x), __floats2bfloat162_rn(c.x, d.x),
+                                 __floats2bfloat162_rn(a.y, b.y), __floats2bfloat162_rn(c.y, d.y)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const uint32_t*>(&r[i]);
+}
+
 template <bool kGated>
 __global__ void __launch_bounds__(kEgThreads, 1)
     q4k_experts_gemm_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapW2,
@@ -206,6 +228,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
         const int ra = t & (kEgBM - 1);
         const int r = kGated ? (ra & 16) * 4 + (ra >> 5) * 16 + (ra & 15) : ra;
         const uint32_t a_tmem = tmem + kEgTmemA + 32 * c + (static_cast<uint32_t>(ra & ~31) << 16);
+        const int sh = 16 * (c & 1);
         // 0, read from shared memory so that the compiler cannot see through the
         // dependence that is built from it below
         const uint32_t zero = *reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
@@ -217,34 +240,27 @@ __global__ void __launch_bounds__(kEgThreads, 1)
                 if (!__all_sync(0xffffffffu, mbar_wait(bwf + 8 * s, (it / kEgWStages) & 1, err))) { ok = false; break; }
                 const uint8_t* P = smem + kEgOffW + s * kEgWStage + r * kBlockBytes;
                 const uint4 hd = *reinterpret_cast<const uint4*>(P);
-                const ulonglong2 qa = *reinterpret_cast<const ulonglong2*>(P + 16 + 32 * c);
-                const ulonglong2 qb = *reinterpret_cast<const ulonglong2*>(P + 32 + 32 * c);
+                const uint4 qa = *reinterpret_cast<const uint4*>(P + 16 + 32 * c);
+                const uint4 qb = *reinterpret_cast<const uint4*>(P + 32 + 32 * c);
                 // the stage is given back once every lane has its words: the vote
                 // needs all of them, so the arrival cannot come before the loads
-                const uint64_t seen = hd.x | qa.x | qb.x | qa.y | qb.y;
-                const unsigned all = __ballot_sync(0xffffffffu, seen != 0u);
+                const unsigned all = __ballot_sync(0xffffffffu, (hd.x | qa.x | qb.x) != 0u);
                 if (lane == 0) mbar_arrive(bwe + 8 * s + (all & zero));
-                const ScaleBytes scb = decode_scales(hd.y, hd.z, hd.w);
+                // the two scales and mins of sub-blocks 2c and 2c + 1, a byte each
+                const uint32_t s0 = hd.y >> sh, s1 = hd.z >> sh, s2 = hd.w >> sh;
+                const uint32_t sc = c < 2 ? s0 & 0x3F3Fu : (s2 & 0x0F0Fu) | ((s0 >> 2) & 0x3030u);
+                const uint32_t mn = c < 2 ? s1 & 0x3F3Fu : ((s2 >> 4) & 0x0F0Fu) | ((s1 >> 2) & 0x3030u);
                 const float d = half_lo(hd.x), dmin = half_hi(hd.x);
-                const uint64_t qw[4] = {qa.x, qa.y, qb.x, qb.y};
+                const uint32_t qw[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
                 uint32_t o[32];  // the row's 64 k, two to a column
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const int j = 2 * c + hh;
-                    const uint32_t scw = j < 4 ? scb.sc_lo : scb.sc_hi;
-                    const uint32_t mw = j < 4 ? scb.m_lo : scb.m_hi;
-                    const float d1 = d * byte_to_float(scw, j & 3);
-                    const float m1 = dmin * byte_to_float(mw, j & 3);
-                    const float d1s0 = d1 * exp2i(-4 * hh), d1s1 = d1 * exp2i(-8 - 4 * hh);
-                    const uint64_t D0 = pack2(d1s0, d1s0), D1 = pack2(d1s1, d1s1), NM = pack2(-m1, -m1);
+                    const float d1 = d * byte_to_float(sc, hh), m1 = dmin * byte_to_float(mn, hh);
+                    const float e0 = d1 * exp2i(16 - 4 * hh), e1 = d1 * exp2i(8 - 4 * hh);
+                    const float c0 = -(e0 + m1), c1 = -(e1 + m1);
+                    const uint64_t E0 = pack2(e0, e0), C0 = pack2(c0, c0), E1 = pack2(e1, e1), C1 = pack2(c1, c1);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const uint4 w = dequant8x(qw[v], hh, D0, D1, NM);
-                        o[16 * hh + 4 * v] = w.x;
-                        o[16 * hh + 4 * v + 1] = w.y;
-                        o[16 * hh + 4 * v + 2] = w.z;
-                        o[16 * hh + 4 * v + 3] = w.w;
-                    }
+                    for (int v = 0; v < 4; ++v) dequant8(qw[2 * v], qw[2 * v + 1], hh, E0, C0, E1, C1, o + 16 * hh + 4 * v);
                 }
                 // the stage is free once the MMAs of two steps before are done (the barrier's next
                 // phase is a step behind this one's: it cannot be further)
