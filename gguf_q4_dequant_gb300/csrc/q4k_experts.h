@@ -70,6 +70,13 @@ __device__ __forceinline__ int expert_of(const int* tiles, int E, int tile) {
     }
     return lo;
 }
+
+// The same by a whole warp: of every 32nd expert, then of the 32 from there.
+__device__ __forceinline__ int expert_at(const int* tiles, int E, int tile, int lane) {
+    const int i = 32 * lane;
+    const int b = 32 * (__popc(__ballot_sync(0xffffffffu, i < E && tiles[i] <= tile)) - 1), j = b + lane;
+    return b + __popc(__ballot_sync(0xffffffffu, j < E && tiles[j] <= tile)) - 1;
+}
 #endif
 
 struct NormArgs {
