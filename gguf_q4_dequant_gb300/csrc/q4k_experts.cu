@@ -57,6 +57,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum.
+__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Physical row of an MMA operand's row: consecutive weight rows of a fragment two
 // rows apart, so that eight lanes' words of a 144-byte row lie in different banks.
 __device__ __forceinline__ int ex_row(int g) { return ((g & 3) << 1) | (g >> 2); }
@@ -79,7 +86,7 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* con
             hx[m][r] = head.x;
             d[m][r] = half_lo(head.x) * exp2i(69);
         }
-    float low[2][NB][4] = {};  // sum over j of m_j (sum of x)
+    float low[2][NB][4];  // sum over j of m_j (sum of x)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         if (c < 3) {
@@ -112,29 +119,43 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* con
                                        __byte_perm(q0.x, 0, 0x4342), __byte_perm(q1.x, 0, 0x4342)},
                                       {__byte_perm(q0.y, 0, 0x4140), __byte_perm(q1.y, 0, 0x4140),
                                        __byte_perm(q0.y, 0, 0x4342), __byte_perm(q1.y, 0, 0x4342)}};
+            // the low nibbles by a mask, the high ones (16 times their codes) as what is left: exact, and
+            // a subtraction goes to the FMA pipe, the masks fill the integer one
+            uint32_t a[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    a[0][i][k] = p[i][k] & 0x000F000Fu;
+                    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p[i][k]), *reinterpret_cast<const __nv_bfloat162*>(&a[0][i][k]));
+                    a[1][i][k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int j = 2 * c + h;
-                const uint32_t mask = h ? 0x00F000F0u : 0x000F000Fu;
                 float s[2];
                 uint32_t mn[4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t scw = j < 4 ? sb[m][r].sc_lo : sb[m][r].sc_hi;
                     const uint32_t mw = j < 4 ? sb[m][r].m_lo : sb[m][r].m_hi;
-                    s[r] = byte_to_float(scw, j & 3) * (h ? d[m][r] * 0.0625f : d[m][r]);
+                    // (2^23 + sc) d - 2^23 d: both exact, so the FMA rounds sc d once
+                    const float dh = h ? d[m][r] * 0.0625f : d[m][r];
+                    s[r] = fmaf(__uint_as_float(__byte_perm(scw, 0x4B000000u, 0x7440u | (j & 3))), dh, -8388608.f * dh);
                     mn[r] = mn[r + 2] = __byte_perm(mw, 0, (j & 3) * 0x0101 | 0x4040);
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    float f[4] = {};
+                    float f[4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t a4[4] = {p[i][0] & mask, p[i][1] & mask, p[i][2] & mask, p[i][3] & mask};
-                        mma_bf16(f, a4, xs[b][h][2 * i], xs[b][h][2 * i + 1]);
+                        if (i == 0) mma_bf16_zero(f, a[h][i], xs[b][h][0], xs[b][h][1]); else mma_bf16(f, a[h][i], xs[b][h][2], xs[b][h][3]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) mma_bf16(low[m][b], mn, xs[b][h][2 * i], xs[b][h][2 * i + 1]);
+                    for (int i = 0; i < 2; ++i) {
+                        if (j == 0 && i == 0) mma_bf16_zero(low[m][b], mn, xs[b][h][0], xs[b][h][1]);
+                        else mma_bf16(low[m][b], mn, xs[b][h][2 * i], xs[b][h][2 * i + 1]);
+                    }
                     acc[m][b][0] = fmaf(f[0], s[0], acc[m][b][0]);
                     acc[m][b][1] = fmaf(f[1], s[0], acc[m][b][1]);
                     acc[m][b][2] = fmaf(f[2], s[1], acc[m][b][2]);
@@ -337,8 +358,11 @@ cudaError_t launch_nb(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo
     const int64_t busy = a.rows.pairs < a.rows.experts ? a.rows.pairs : a.rows.experts, slabs = (a.N + kExRows - 1) / kExRows;
     const int KB = static_cast<int>(a.K / kBlockWeights);
     // wk, the warps that share K: few units are split further, so that every warp
-    // of the GPU has some of the words on their way; many are not, as adding the
-    // sums costs about half a step
+    // of the GPU has some of the words on their way (8 experts of 128 with one row
+    // each, gated 768 x 2048: 12.6 us with 8, 32 with 1); many are not, as the warps of
+    // a unit wait for one another (64 rows for each of 128 experts of 2048 x 768: 37 us
+    // with 1, 44 with 2). In between the units' count decides how full the last
+    // round is (128 experts with four rows each, gated: 76, 73, 68, 72 us with 1, 2, 4, 8).
     const int64_t tiles = busy > a.rows.pairs / (8 * NB) ? busy : a.rows.pairs / (8 * NB);
     int wk = 1, per = 1;
     double best = 1e300;
@@ -349,7 +373,7 @@ cudaError_t launch_nb(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo
         const double groups = static_cast<double>(dev.num_sms) * p * kExWarps / w;
         // the experts with rows are known on the device only: half a round is lost on average
         const double rounds = static_cast<double>(tiles * slabs) / groups + 0.5;
-        const double cost = (rounds > 1.0 ? rounds : 1.0) * ((KB + w - 1) / w * (kGated ? 2 : 1) + (w > 1 ? 1.0 : 0.5));
+        const double cost = (rounds > 1.0 ? rounds : 1.0) * ((KB + w - 1) / w * (kGated ? 2 : 1) + (w > 1 ? 0.5 : 0.25));
         if (cost < best * 0.999) best = cost, wk = w, per = p;
     }
     const int64_t units = (a.rows.pairs / (8 * NB) + busy) * slabs, groups = kExWarps / wk;
