@@ -344,6 +344,22 @@ int check_matmul(int count, const void* const* W, const int64_t* N, int64_t K, c
 int device_info(const DeviceInfo** info) { return current_device(info); }
 int pdl_mode() { return g_pdl.load(std::memory_order_relaxed); }
 
+int rows_map(CUtensorMap* map, const void* X, int64_t rows, int64_t K, int box_rows) {
+    const MapKey key{reinterpret_cast<uintptr_t>(X), rows, K, box_rows, 2};
+    MapEntry* e = map_slot(key);
+    if (!e->valid || !(e->key == key)) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)}, strides[1] = {2ull * static_cast<uint64_t>(K)};
+        const uint32_t box[2] = {64, static_cast<uint32_t>(box_rows)};
+        if (!encode_bf16_sw128(map, X, 2, dims, strides, box)) return Q4K_ERR_CUDA;
+        e->map = *map;
+        e->key = key;
+        e->valid = true;
+        return Q4K_OK;
+    }
+    *map = e->map;
+    return Q4K_OK;
+}
+
 int weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K, int rows) { return encode_w(map, W, N, K, rows); }
 
 bool encode_bf16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,

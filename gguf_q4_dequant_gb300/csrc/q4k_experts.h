@@ -15,6 +15,9 @@ namespace q4k {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 32;
 
+// Whether results of so many bytes are written past L2 (129 MB): more than about half of it.
+inline bool passes_l2(int64_t bytes) { return bytes > (int64_t(64) << 20); }
+
 // The rows of a step in the order of their experts: expert e has rows
 // starts[e] .. starts[e+1]-1 of `pairs` rows.
 struct ExpertRows {
@@ -91,6 +94,7 @@ struct NormArgs {
     int C;
     float eps;
     bool x_bf16, out_bf16;
+    bool stream = false;  // set by the launcher
 };
 cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t stream, int pdl);
 
@@ -112,8 +116,9 @@ struct GatherArgs {
     const int32_t* order;
     uint16_t* out;
     int T, C, k, pairs;
+    bool stream = false;  // set by the launcher
 };
-cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream, int pdl);
+cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
 
 struct CombineArgs {
     const uint16_t* y;
@@ -123,6 +128,7 @@ struct CombineArgs {
     float* out;
     int64_t T;
     int C, k, pairs;
+    bool stream = false;  // set by the launcher
 };
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream, int pdl);
 
@@ -141,6 +147,8 @@ cudaError_t experts_gemm_setup();
 
 // A 2-D byte map {K/256*144, N} of packed rows, box one super-block of `rows` rows
 // (a q4k_status; cached per host thread).
+// Rows of bf16 [rows][K], box 64 k x box_rows rows with the 128-byte swizzle (the same).
+int rows_map(CUtensorMap* map, const void* X, int64_t rows, int64_t K, int box_rows);
 int weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K, int rows);
 
 }  // namespace q4k

@@ -99,7 +99,7 @@ int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* orde
     const int rc = device_info(&dev);
     if (rc != Q4K_OK) return rc;
     const GatherArgs a{X, scales, order, out, static_cast<int>(T), static_cast<int>(C), k, static_cast<int>(T * k)};
-    return status(launch_gather(a, static_cast<cudaStream_t>(stream), pdl_mode()));
+    return status(launch_gather(a, static_cast<cudaStream_t>(stream), *dev, pdl_mode()));
 }
 
 int q4k_experts_matmul(const void* W, int64_t E, int64_t N, int64_t K, const uint16_t* X, const int32_t* starts,

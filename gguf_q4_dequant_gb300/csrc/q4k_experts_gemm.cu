@@ -338,11 +338,8 @@ cudaError_t launch_gated(const ExpertArgs& a, cudaStream_t stream, const DeviceI
     mapW2 = mapW;
     if (kGated && weight_map(&mapW2, a.W2, a.rows.experts * a.N, a.K, cols) != Q4K_OK) return cudaErrorInvalidValue;
     XMaps mapX;
-    const uint64_t dims[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.rows.pairs)}, strides[1] = {2ull * a.K};
-    for (int i = 0; i < kEgBN / 32; ++i) {
-        const uint32_t box[2] = {64, 32u * (i + 1)};
-        if (!encode_bf16_sw128(&mapX.box[i], a.X, 2, dims, strides, box)) return cudaErrorInvalidValue;
-    }
+    for (int i = 0; i < kEgBN / 32; ++i)
+        if (rows_map(&mapX.box[i], a.X, a.rows.pairs, a.K, 32 * (i + 1)) != Q4K_OK) return cudaErrorInvalidValue;
     const int64_t busy = a.rows.pairs < a.rows.experts ? a.rows.pairs : a.rows.experts;
     const int64_t most = (a.rows.pairs / kEgBN + busy) * ((a.N + cols - 1) / cols);
     return launch_serve(q4k_experts_gemm_kernel<kGated>, dim3(static_cast<unsigned>(most < dev.num_sms ? most : dev.num_sms)),

@@ -29,18 +29,22 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], bool stream) {
+    float4* o = reinterpret_cast<float4*>(p);
+    const float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+    if (stream) __stcs(o, lo), __stcs(o + 1, hi);
+    else o[0] = lo, o[1] = hi;
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], bool stream) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
+    if (stream) __stcs(reinterpret_cast<uint4*>(p), o);
+    else *reinterpret_cast<uint4*>(p) = o;
 }
 
 // Eight of the 32 columns of a scale (the lanes 4i .. 4i+3 hold them): the
@@ -114,20 +118,30 @@ __global__ void __launch_bounds__(1024) q4k_add_norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    const float rs = 1.f / sqrtf(ss / static_cast<float>(a.C) + a.eps);
+    // 1 / sqrt(mean + eps) as the sum of two floats (a Newton step's correction of the rounded
+    // root), and r * w * that with its products' errors taken along: y is the exact value but for its
+    // last bit, so that codes and scales, which jump at borders, are those of the exact y almost always
+    const float mean = ss / static_cast<float>(a.C) + a.eps;
+    const float rs = 1.f / sqrtf(mean);
+    const float t = mean * rs, rest = fmaf(-t, rs, fmaf(-fmaf(mean, rs, -t), rs, 1.f));
+    const float rs_lo = mean > 0.f && rs < INFINITY ? 0.5f * rs * rest : 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int c = 8 * (at + r * n);
         const bool in = c < a.C;  // C is a multiple of 32: the same for the four lanes of a scale
         float w[8] = {};
         if (in) {
-            if (a.sum != nullptr) store8(static_cast<X*>(a.sum) + off + c, v[r]);
+            if (a.sum != nullptr) store8(static_cast<X*>(a.sum) + off + c, v[r], a.stream);
             const float4 p = *reinterpret_cast<const float4*>(a.weight + c), q = *(reinterpret_cast<const float4*>(a.weight + c) + 1);
             w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w;
             w[4] = q.x; w[5] = q.y; w[6] = q.z; w[7] = q.w;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= v[r][i] * rs;
-            if (a.out != nullptr) store8(static_cast<O*>(a.out) + off + c, w);
+            for (int i = 0; i < 8; ++i) {
+                const float m = v[r][i] * w[i], off_m = fmaf(v[r][i], w[i], -m);
+                const float y = fmaf(m, rs, fmaf(m, rs_lo, off_m * rs));
+                w[i] = isfinite(y) ? y : m * rs;
+            }
+            if (a.out != nullptr) store8(static_cast<O*>(a.out) + off + c, w, a.stream);
         }
         if (a.codes != nullptr) store_eight(w, a.codes + off + c, a.scales + (off + c) / 32, in, (lane & 3) == 0);
     }
@@ -158,7 +172,10 @@ cudaError_t launch_xo(const NormArgs& a, cudaStream_t stream, int pdl) {
 
 }  // namespace
 
-cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t stream, int pdl) {
+cudaError_t launch_add_norm(const NormArgs& args, cudaStream_t stream, int pdl) {
+    NormArgs a = args;
+    const int64_t x = a.x_bf16 ? 2 : 4, o = a.out_bf16 ? 2 : 4;
+    a.stream = passes_l2(a.T * a.C * ((a.sum != nullptr ? x : 0) + (a.out != nullptr ? o : 0)));
     if (a.x_bf16)
         return a.out_bf16 ? launch_xo<uint16_t, uint16_t>(a, stream, pdl) : launch_xo<uint16_t, float>(a, stream, pdl);
     return a.out_bf16 ? launch_xo<float, uint16_t>(a, stream, pdl) : launch_xo<float, float>(a, stream, pdl);

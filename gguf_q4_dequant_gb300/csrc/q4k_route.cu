@@ -11,7 +11,12 @@
 namespace q4k {
 
 constexpr int kRouteTokens = 64;    // tokens of a block of the sort
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 1024;
+// Threads of a block that picks: a lane holds R logits and their keys.
+__host__ __device__ constexpr int pick_threads(int R) { return R <= 8 ? 1024 : 512; }
+// Steps of up to so many blocks have no scan of their own: each block adds up the
+// counts of the blocks before it (64 of them: two rounds of loads for 128 experts).
+constexpr int kRouteFew = 128;
 
 // ------------------------------------------------------------------- top k ---
 
@@ -104,12 +109,9 @@ __device__ __forceinline__ void pick_block(const RouteArgs& a, int t0, int n, in
 // of the pairs. Each warp takes a run of whole 32 pairs: it counts its own in
 // `hist[warp]`, the counts are summed over the warps before it, and it goes
 // over its run again, 32 pairs at a time (lanes with the same expert find one
-// another). place(i, e, rank) is called for every pair with an expert, after
-// offsets(e) has been taken in. hist: [warps][E].
+// another). hist: [warps][E], zeros; `used` warps have pairs.
 __device__ __forceinline__ void count_pairs(const int16_t* chosen, int pairs, int E, int* hist, int run) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < (blockDim.x >> 5) * E; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
     for (int i0 = warp * run; i0 < min((warp + 1) * run, pairs); i0 += 32) {
         const int i = i0 + lane;
         const int e = i < pairs ? chosen[i] : -1;
@@ -121,14 +123,14 @@ __device__ __forceinline__ void count_pairs(const int16_t* chosen, int pairs, in
 }
 
 __device__ __forceinline__ void place_pairs(const RouteArgs& a, const int16_t* chosen, int64_t first, int pairs, int E,
-                                            int* hist, int run) {
+                                            int* hist, const int* base, int run) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i0 = warp * run; i0 < min((warp + 1) * run, pairs); i0 += 32) {
         const int i = i0 + lane;
         const int e = i < pairs ? chosen[i] : -1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
         int at = -1;
-        if (e >= 0) at = hist[warp * E + e] + __popc(same & ((1u << lane) - 1u));
+        if (e >= 0) at = base[e] + hist[warp * E + e] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
         if (e >= 0 && lane == __ffs(same) - 1) hist[warp * E + e] += __popc(same);
         __syncwarp();
@@ -140,30 +142,32 @@ __device__ __forceinline__ void place_pairs(const RouteArgs& a, const int16_t* c
 }
 
 // Exclusive scan of the counts cnt[0 .. E-1] (shared memory) by the block, to
-// base[0 .. E] (base[E]: the total). E <= 1024, blockDim.x >= 32.
+// base[0 .. E] (base[E]: the total): a lane of the first warp has E / 32 of them
+// side by side. E <= 1024.
 __device__ __forceinline__ void scan_experts(const int* cnt, int E, int* base) {
     if (threadIdx.x < 32) {
-        int run = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + threadIdx.x;
-            const int c = e < E ? cnt[e] : 0;
-            int s = c;
+        const int per = (E + 31) / 32, e0 = threadIdx.x * per, e1 = min(e0 + per, E);
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) sum += cnt[e];
+        int s = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, s, o);
-                if (static_cast<int>(threadIdx.x) >= o) s += t;
-            }
-            if (e < E) base[e] = run + s - c;
-            run += __shfl_sync(0xffffffffu, s, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, s, o);
+            if (static_cast<int>(threadIdx.x) >= o) s += t;
         }
-        if (threadIdx.x == 0) base[E] = run;
+        int at = s - sum;
+        for (int e = e0; e < e1; ++e) {
+            base[e] = at;
+            at += cnt[e];
+        }
+        if (threadIdx.x == 31) base[E] = s;
     }
     __syncthreads();
 }
 
 // One block does everything: a step of a few tokens is one launch.
 template <int R>
-__global__ void __launch_bounds__(1024) q4k_route_one_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(pick_threads(R)) q4k_route_one_kernel(const RouteArgs a) {
     extern __shared__ int route_smem[];
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -172,13 +176,14 @@ __global__ void __launch_bounds__(1024) q4k_route_one_kernel(const RouteArgs a) 
     int* cnt = hist + warps * a.E;      // [E]
     int* base = cnt + a.E;              // [E + 1]
     int16_t* chosen = reinterpret_cast<int16_t*>(base + a.E + 1);
+    const int run = ((pairs + warps - 1) / warps + 31) / 32 * 32, used = (pairs + run - 1) / run;
+    for (int i = threadIdx.x; i < used * a.E; i += blockDim.x) hist[i] = 0;
     pick_block<R>(a, 0, a.T, chosen);
     __syncthreads();
-    const int run = ((pairs + warps - 1) / warps + 31) / 32 * 32;
     count_pairs(chosen, pairs, a.E, hist, run);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int s = 0;
-        for (int w = 0; w < warps; ++w) {
+        for (int w = 0; w < used; ++w) {
             const int c = hist[w * a.E + e];
             hist[w * a.E + e] = s;
             s += c;
@@ -187,16 +192,14 @@ __global__ void __launch_bounds__(1024) q4k_route_one_kernel(const RouteArgs a) 
     }
     __syncthreads();
     scan_experts(cnt, a.E, base);
-    for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) hist[i] += base[i % a.E];
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.starts[e] = base[e];
     for (int i = base[a.E] + threadIdx.x; i < pairs; i += blockDim.x) a.order[i] = -1;
-    __syncthreads();
-    place_pairs(a, chosen, 0, pairs, a.E, hist, run);
+    place_pairs(a, chosen, 0, pairs, a.E, hist, base, run);
 }
 
 // Many tokens: blocks of kRouteTokens pick and count (counts: [blocks][E]), ...
 template <int R>
-__global__ void __launch_bounds__(kRouteThreads) q4k_route_pick_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(pick_threads(R)) q4k_route_pick_kernel(const RouteArgs a) {
     extern __shared__ int route_smem[];
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -239,35 +242,61 @@ __global__ void __launch_bounds__(1024) q4k_route_scan_kernel(int32_t* counts, i
     }
 }
 
-// ... and each block places its pairs.
-__global__ void __launch_bounds__(kRouteThreads) q4k_route_place_kernel(const RouteArgs a) {
+// ... and each block places its pairs. kScanned: ws holds those sums and totals,
+// else the counts of each block.
+template <bool kScanned>
+__global__ void __launch_bounds__(kRouteThreads) q4k_route_place_kernel(const RouteArgs a, int most) {
     extern __shared__ int route_smem[];
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
-    constexpr int warps = kRouteThreads / 32;
-    const int E = a.E;
-    int* hist = route_smem;        // [warps][E]
-    int* cnt = hist + warps * E;   // [E]
-    int* base = cnt + E;           // [E + 1]
+    const int E = a.E, blocks = gridDim.x;
+    int* hist = route_smem;        // [most][E], most: warps with pairs
+    int* cnt = hist + most * E;    // [E]
+    int* before = cnt + E;         // [E]
+    int* base = before + E;        // [E + 1]
     int16_t* chosen = reinterpret_cast<int16_t*>(base + E + 1);
     const int t0 = blockIdx.x * kRouteTokens, n = min(kRouteTokens, a.T - t0), pairs = n * a.k;
     const int64_t first = static_cast<int64_t>(t0) * a.k;
+    const int run = ((kRouteTokens * a.k + most - 1) / most + 31) / 32 * 32, used = (pairs + run - 1) / run;
+    for (int i = threadIdx.x; i < used * E; i += blockDim.x) hist[i] = 0;
     for (int i = threadIdx.x; i < pairs; i += blockDim.x) chosen[i] = static_cast<int16_t>(a.ids[first + i]);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = a.ws[static_cast<int64_t>(gridDim.x) * E + e];
-    __syncthreads();
+    if (kScanned) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            cnt[e] = a.ws[static_cast<int64_t>(blocks) * E + e];
+            before[e] = a.ws[static_cast<int64_t>(blockIdx.x) * E + e];
+        }
+        __syncthreads();
+    } else {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = before[e] = 0;
+        __syncthreads();
+        // as many slices of the blocks as there are threads for; sums of integers: any order
+        const int slices = max(1, static_cast<int>(blockDim.x) / E);
+        for (int i = threadIdx.x; i < slices * E; i += blockDim.x) {
+            const int e = i % E, slice = i / E;
+            int all = 0, mine = 0;
+#pragma unroll 8
+            for (int b = slice; b < blocks; b += slices) {
+                const int c = a.ws[static_cast<int64_t>(b) * E + e];
+                all += c;
+                if (b < static_cast<int>(blockIdx.x)) mine += c;
+            }
+            atomicAdd(&cnt[e], all);
+            atomicAdd(&before[e], mine);
+        }
+        __syncthreads();
+    }
     scan_experts(cnt, E, base);
-    const int run = ((pairs + warps - 1) / warps + 31) / 32 * 32;
     count_pairs(chosen, pairs, E, hist, run);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int s = base[e] + a.ws[static_cast<int64_t>(blockIdx.x) * E + e];
-        for (int w = 0; w < warps; ++w) {
+        int s = before[e];
+        for (int w = 0; w < used; ++w) {
             const int c = hist[w * E + e];
             hist[w * E + e] = s;
             s += c;
         }
     }
     __syncthreads();
-    place_pairs(a, chosen, first, pairs, E, hist, run);
+    place_pairs(a, chosen, first, pairs, E, hist, base, run);
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e <= E; e += blockDim.x) a.starts[e] = base[e];
     // what is behind the last row: each block its share
@@ -301,32 +330,44 @@ __device__ __forceinline__ uint4 row8(const uint8_t* x, const uint8_t* scales, i
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A warp per row, kGatherLoads loads of a lane in flight; the rows of a token
-// are read once from memory and from L2 for its other experts.
-constexpr int kGatherWarps = 4, kGatherLoads = 8;
+// Results that outgrow half of L2 pass it by: 8192 tokens to 8 experts each, 268 MB, 71 us
+// for the sort of a prompt chunk instead of 87; smaller ones stay for the product that reads them.
+__device__ __forceinline__ void store16(uint16_t* p, uint4 v, bool stream) {
+    if (stream) __stcs(reinterpret_cast<uint4*>(p), v);
+    else *reinterpret_cast<uint4*>(p) = v;
+}
+
+// A warp takes rows in turn, kGatherLoads loads of a lane in flight, the next
+// row's place asked for meanwhile; the rows of a token are read once from memory
+// and from L2 for its other experts.
+constexpr int kGatherWarps = 4, kGatherLoads = 8, kGatherBlocks = 16;
 
 template <typename X>
 __global__ void __launch_bounds__(32 * kGatherWarps) q4k_gather_kernel(const GatherArgs a) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t p = static_cast<int64_t>(blockIdx.x) * kGatherWarps + (threadIdx.x >> 5);
-    if (p >= a.pairs) return;
-    const int pair = a.order[p];
-    if (pair < 0 || pair >= a.pairs) return;
-    const int64_t src = static_cast<int64_t>(pair / a.k) * a.C, dst = p * a.C;
+    const int64_t every = static_cast<int64_t>(gridDim.x) * kGatherWarps;
     const X* x = static_cast<const X*>(a.x);
-    for (int c0 = 0; c0 < a.C; c0 += 256 * kGatherLoads) {
-        uint4 v[kGatherLoads];
+    int64_t p = static_cast<int64_t>(blockIdx.x) * kGatherWarps + (threadIdx.x >> 5);
+    int pair = p < a.pairs ? a.order[p] : -1;
+    for (; p < a.pairs; p += every) {
+        const int now = pair;
+        if (p + every < a.pairs) pair = a.order[p + every];
+        if (now < 0 || now >= a.pairs) continue;
+        const int64_t src = static_cast<int64_t>(now / a.k) * a.C, dst = p * a.C;
+        for (int c0 = 0; c0 < a.C; c0 += 256 * kGatherLoads) {
+            uint4 v[kGatherLoads];
 #pragma unroll
-        for (int j = 0; j < kGatherLoads; ++j) {
-            const int c = c0 + 256 * j + 8 * lane;
-            if (c < a.C) v[j] = row8(x, a.scales, src + c);
-        }
+            for (int j = 0; j < kGatherLoads; ++j) {
+                const int c = c0 + 256 * j + 8 * lane;
+                if (c < a.C) v[j] = row8(x, a.scales, src + c);
+            }
 #pragma unroll
-        for (int j = 0; j < kGatherLoads; ++j) {
-            const int c = c0 + 256 * j + 8 * lane;
-            if (c < a.C) *reinterpret_cast<uint4*>(a.out + dst + c) = v[j];
+            for (int j = 0; j < kGatherLoads; ++j) {
+                const int c = c0 + 256 * j + 8 * lane;
+                if (c < a.C) store16(a.out + dst + c, v[j], a.stream);
+            }
         }
     }
 }
@@ -374,17 +415,17 @@ __global__ void __launch_bounds__(256) q4k_combine_kernel(const CombineArgs a) {
         }
     }
     float4* o = reinterpret_cast<float4*>(a.out + t * a.C + c);
-    o[0] = make_float4(s[0], s[1], s[2], s[3]);
-    o[1] = make_float4(s[4], s[5], s[6], s[7]);
+    const float4 lo = make_float4(s[0], s[1], s[2], s[3]), hi = make_float4(s[4], s[5], s[6], s[7]);
+    if (a.stream) __stcs(o, lo), __stcs(o + 1, hi);
+    else o[0] = lo, o[1] = hi;
 }
 
 // ------------------------------------------------------------------ host ---
 
 namespace {
 
-// Steps of up to this many pairs are sorted by one block: 27.5 KB of shared memory
-// at 128 experts, within the 48 KB that need no attribute at 1024 experts too
-// with 8 warps.
+// Steps of up to this many pairs are sorted by one block, with as many warps as
+// their counts have room for in the 48 KB that need no attribute.
 constexpr int kOnePairs = 2048;
 
 template <int R>
@@ -393,19 +434,26 @@ cudaError_t route_r(const RouteArgs& a, cudaStream_t stream, int pdl) {
     if (pairs <= kOnePairs) {
         // a warp per token, as many as the counts of a warp leave room for
         const int most = (40960 - 4 * (2 * a.E + 1)) / (4 * a.E);
-        int warps = a.T < 32 ? a.T : 32;
+        int warps = a.T < pick_threads(R) / 32 ? a.T : pick_threads(R) / 32;
         warps = warps < most ? warps : most;
         const size_t smem = 4 * (static_cast<size_t>(warps) * a.E + 2 * a.E + 1) + 2 * pairs;
         return launch_serve(q4k_route_one_kernel<R>, dim3(1), dim3(32 * warps), smem, stream, pdl, 1, a);
     }
     const int blocks = (a.T + kRouteTokens - 1) / kRouteTokens;
     const size_t chosen = 2 * static_cast<size_t>(kRouteTokens) * a.k;
-    cudaError_t e = launch_serve(q4k_route_pick_kernel<R>, dim3(blocks), dim3(kRouteThreads), 4 * a.E + chosen, stream, pdl, 1, a);
+    cudaError_t e = launch_serve(q4k_route_pick_kernel<R>, dim3(blocks), dim3(pick_threads(R)), 4 * a.E + chosen, stream, pdl, 1, a);
     if (e != cudaSuccess) return e;
+    // counts for as many warps as have 32 pairs each, within 48 KB
+    int most = (44 * 1024 - static_cast<int>(chosen) - 4 * (3 * a.E + 1)) / (4 * a.E);
+    const int runs = (kRouteTokens * a.k + 31) / 32;
+    most = most < runs ? most : runs;
+    most = most < kRouteThreads / 32 ? most : kRouteThreads / 32;
+    const size_t smem = 4 * (static_cast<size_t>(most) * a.E + 3 * a.E + 1) + chosen;
+    if (blocks <= kRouteFew)
+        return launch_serve(q4k_route_place_kernel<false>, dim3(blocks), dim3(kRouteThreads), smem, stream, pdl, 1, a, most);
     e = launch_serve(q4k_route_scan_kernel, dim3((a.E + 31) / 32), dim3(1024), 0, stream, pdl, 1, a.ws, blocks, a.E);
     if (e != cudaSuccess) return e;
-    const size_t smem = 4 * (static_cast<size_t>(kRouteThreads / 32) * a.E + 2 * a.E + 1) + chosen;
-    return launch_serve(q4k_route_place_kernel, dim3(blocks), dim3(kRouteThreads), smem, stream, pdl, 1, a);
+    return launch_serve(q4k_route_place_kernel<true>, dim3(blocks), dim3(kRouteThreads), smem, stream, pdl, 1, a, most);
 }
 
 }  // namespace
@@ -421,13 +469,18 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int pdl) {
     return route_r<32>(a, stream, pdl);
 }
 
-cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream, int pdl) {
-    const dim3 grid((a.pairs + kGatherWarps - 1) / kGatherWarps), block(32 * kGatherWarps);
+cudaError_t launch_gather(const GatherArgs& args, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
+    GatherArgs a = args;
+    a.stream = passes_l2(2 * static_cast<int64_t>(a.pairs) * a.C);
+    const int64_t rows = (static_cast<int64_t>(a.pairs) + kGatherWarps - 1) / kGatherWarps, most = static_cast<int64_t>(dev.num_sms) * kGatherBlocks;
+    const dim3 grid(static_cast<unsigned>(rows < most ? rows : most)), block(32 * kGatherWarps);
     if (a.scales != nullptr) return launch_serve(q4k_gather_kernel<uint8_t>, grid, block, 0, stream, pdl, 1, a);
     return launch_serve(q4k_gather_kernel<uint16_t>, grid, block, 0, stream, pdl, 1, a);
 }
 
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream, int pdl) {
+cudaError_t launch_combine(const CombineArgs& args, cudaStream_t stream, int pdl) {
+    CombineArgs a = args;
+    a.stream = passes_l2(4 * a.T * a.C);
     const int c8 = a.C / 8;
     int bx = 1;
     while (bx < c8 && bx < 256) bx *= 2;
