@@ -433,3 +433,177 @@ def test_combine(q4k, T, k, C, base):
     got = out.cpu().double()
     assert bool(((got[:T] - want).abs() <= 2.0 ** -24 * (k + 1) * size).all())
     assert bool((got[T:] == 7).all())
+
+
+# ---------------------------------------------------------------- together ---
+
+def test_binding_refuses_on_the_device(q4k):
+    z = lambda *s, d=torch.float32: torch.zeros(*s, dtype=d, device=DEV)  # noqa: E731
+    b16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    x, w = z(4, 64), z(64)
+    bad = [
+        lambda: q4k.q4k_add_norm(x, z(3, 64), w, out=z(4, 64)),
+        lambda: q4k.q4k_add_norm(x, None, z(63), out=z(4, 64)),
+        lambda: q4k.q4k_add_norm(x, None, w, sum=z(4, 64, d=b16), out=z(4, 64)),
+        lambda: q4k.q4k_add_norm(x, None, w, out=z(3, 64)),
+        lambda: q4k.q4k_add_norm(x.t().contiguous().t(), None, w, out=z(4, 64)),
+        lambda: q4k.q4k_add_norm(x, None, w, codes=z(4, 64, d=u8), scales=z(7, d=u8)),
+        lambda: q4k.q4k_route(x, 2, 0, 1.0, z(8, d=i32), z(7), z(8, d=i32), z(8, d=i32), z(65, d=i32), z(1024, d=u8)),
+        lambda: q4k.q4k_route(x, 2, 0, 1.0, z(8, d=i32), z(8), z(8, d=i32), z(8, d=i32), z(64, d=i32), z(1024, d=u8)),
+        lambda: q4k.q4k_route(x, 2, 0, 1.0, z(8, d=torch.int64), z(8), z(8, d=i32), z(8, d=i32), z(65, d=i32), z(1024, d=u8)),
+        lambda: q4k.q4k_experts_gather(x, z(8, d=i32), 2, z(8, 64, d=b16)),
+        lambda: q4k.q4k_experts_gather(z(4, 64, d=b16), z(7, d=i32), 2, z(8, 64, d=b16)),
+        lambda: q4k.q4k_experts_gather(z(4, 64, d=u8), z(8, d=i32), 2, z(8, 64, d=b16), scales=z(7, d=u8)),
+        lambda: q4k.q4k_experts_matmul(z(2 * 64 * 144 - 1, d=u8), 64, 256, z(4, 256, d=b16), z(3, d=i32), z(4, 64, d=b16)),
+        lambda: q4k.q4k_experts_matmul(z(2 * 64 * 144, d=u8), 64, 256, z(4, 256, d=b16), z(3, d=i32), z(255, d=b16)),
+        lambda: q4k.q4k_experts_gated(z(2 * 64 * 144, d=u8), z(64 * 144, d=u8), 64, 256, z(4, 256, d=b16), z(3, d=i32), z(4, 64, d=b16)),
+        lambda: q4k.q4k_experts_combine(z(8, 64, d=b16), z(4, 2, d=i32), z(7), z(4, 64)),
+        lambda: q4k.q4k_experts_combine(z(8, 64, d=b16), z(4, 2, d=i32), z(8), z(3, 64)),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(q4k.Q4KError) as e:
+        q4k.q4k_route(x, 2, 0, 1.0, z(8, d=i32), z(8), z(8, d=i32), z(8, d=i32), z(65, d=i32), z(4 * 64 * 2 - 4, d=u8))
+    assert e.value.status == q4k.Q4K_ERR_SPACE
+
+
+class Layer:
+    """An expert layer: norm, router, picks, gathered rows, gate and up, down, back to the tokens."""
+
+    def __init__(self, q4k, T, E, top, hidden, ffn, eight, seed=0):
+        g = gen(seed)
+        self.q, self.T, self.E, self.top, self.hidden, self.ffn, self.eight = q4k, T, E, top, hidden, ffn, eight
+        self.router = synth.weight_rows(seed + 77, E, hidden)
+        self.gate, self.up = Experts(seed, E, ffn, hidden), Experts(seed + 1000, E, ffn, hidden)
+        self.down = Experts(seed + 2000, E, hidden, ffn)
+        sign = 1.0 - 2.0 * (torch.arange(hidden) % 2)
+        self.weight = 0.05 * sign * (0.5 + torch.rand(hidden, generator=g))
+        self.x, self.delta = torch.randn(T, hidden, generator=g), torch.randn(T, hidden, generator=g)
+        d = lambda t: t.to(DEV)  # noqa: E731
+        e = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device=DEV)  # noqa: E731
+        i32, b16, u8 = torch.int32, torch.bfloat16, torch.uint8
+        self.dx, self.ddelta, self.dweight, self.drouter = d(self.x), d(self.delta), d(self.weight), d(self.router)
+        self.sum, self.h, self.codes, self.scales = e(T, hidden), e(T, hidden, t=b16), e(T, hidden, t=u8), e(T, hidden // 32, t=u8)
+        self.logits, self.ids, self.w = e(T, E), e(T, top, t=i32), e(T, top)
+        self.order, self.slots, self.starts = e(T * top, t=i32), e(T, top, t=i32), e(E + 1, t=i32)
+        self.ws = e(q4k.q4k_route_workspace(T, E), t=u8)
+        self.rows, self.act, self.y, self.out = (e(T * top, n, t=b16) for n in (hidden, ffn, hidden, hidden))
+        self.out = e(T, hidden)
+
+    def run(self, stream=None):
+        q = self.q
+        kw = dict(stream=stream)
+        codes, scales = (self.codes, self.scales) if self.eight else (None, None)
+        q.q4k_add_norm(self.dx, self.ddelta, self.dweight, sum=self.sum, out=self.h, codes=codes, scales=scales, **kw)
+        q.matmul(self.drouter, self.E, self.hidden, self.h, self.logits, **kw)
+        q.q4k_route(self.logits, self.top, q.ROUTE_SOFTMAX_TOP, 1.0, self.ids, self.w, self.order, self.slots, self.starts, self.ws, **kw)
+        q.q4k_experts_gather(self.codes if self.eight else self.h, self.order, self.top, self.rows, scales=scales, **kw)
+        q.q4k_experts_gated(self.gate.dev, self.up.dev, self.ffn, self.hidden, self.rows, self.starts, self.act, **kw)
+        q.q4k_experts_matmul(self.down.dev, self.hidden, self.ffn, self.act, self.starts, self.y, **kw)
+        q.q4k_experts_combine(self.y, self.slots, self.w, self.out, base=self.sum, **kw)
+        return self.out
+
+    def check(self):
+        """Each step against 64 bits of what the step before gave, so that a pick near a border counts as it fell."""
+        cpu = lambda t: t.cpu().double()  # noqa: E731
+        r, h = norm_ref(self.dx.cpu(), self.ddelta.cpu(), self.weight, 1e-6)
+        assert bool(((cpu(self.sum) - r).abs() <= 2.0 ** -24 * r.abs()).all())
+        assert bool(((cpu(self.h) - h).abs() <= (2.0 ** -8 + 2.0 ** -18) * h.abs()).all())
+        ids, w, order, slots, starts, d = route_ref(self.logits.cpu(), self.top, 1, 1.0)
+        assert torch.equal(self.ids.cpu().long(), ids) and self.order.tolist() == order.tolist()
+        assert bool(((cpu(self.w) - w).abs() <= (2.0 ** -18 + 2.0 ** -23 * d.abs()) * w).all())
+        rows = cpu(self.h)
+        if self.eight:
+            rows = (self.codes.cpu().view(torch.float8_e4m3fn).double().view(self.T, -1, 32)
+                    * torch.exp2(cpu(self.scales) - 127).unsqueeze(2)).view(self.T, -1)
+            # half a step of 4 significant bits (or of the smallest ones, 2^-10 of the scale) from the fp32 rows
+            near = 2.0 ** -4 * h.abs() * (1 + 2.0 ** -18) + 2.0 ** -10 * torch.exp2(cpu(self.scales) - 127).repeat_interleave(32, 1)
+            assert bool(((rows - h).abs() <= near).all())
+        assert torch.equal(cpu(self.rows), rows[order // self.top])
+        for e in range(self.E):
+            a, b = int(starts[e]), int(starts[e + 1])
+            if a == b:
+                continue
+            x, act = self.rows[a:b].cpu(), self.act[a:b].cpu()
+            (gt, tg), (u, tu) = self.gate.product(e, x), self.up.product(e, x)
+            silu = gt * torch.sigmoid(gt)
+            tol = 1.1 * tg * (u.abs() + tu) + silu.abs() * tu + (2.0 ** -8 + 2.0 ** -20) * (silu * u).abs() + 1e-38
+            assert bool(((act.double() - silu * u).abs() <= tol).all())
+            want, tol = self.down.product(e, act)
+            assert bool(((self.y[a:b].cpu().double() - want).abs() <= tol + 2.0 ** -8 * want.abs() + 1e-38).all())
+        terms = cpu(self.w).unsqueeze(2) * cpu(self.y)[torch.tensor(slots)]
+        size = cpu(self.sum).abs() + terms.abs().sum(1)
+        assert bool(((cpu(self.out) - cpu(self.sum) - terms.sum(1)).abs() <= 2.0 ** -24 * (self.top + 1) * size).all())
+
+
+@pytest.mark.parametrize("T,E,top,hidden,ffn,eight", [(1, 8, 2, 512, 256, False), (5, 16, 4, 512, 512, True),
+                                                      (33, 8, 3, 256, 768, False), (300, 6, 2, 512, 256, True)])
+def test_layer(q4k, T, E, top, hidden, ffn, eight):
+    layer = Layer(q4k, T, E, top, hidden, ffn, eight, seed=T)
+    layer.run()
+    layer.check()
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("T", [3, 150])
+def test_layer_captured(q4k, mode, T):
+    """A captured layer replays right on new inputs, in every launch mode, back to back with itself."""
+    layer = Layer(q4k, T, 6, 2, 256, 256, True, seed=3)
+    old = q4k.q4k_set_pdl(mode)
+    try:
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            layer.run()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=side):
+                layer.run()
+                layer.run()
+        for _ in range(3):
+            layer.dx.normal_()
+            layer.out.fill_(float("nan"))
+            layer.act.fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            graph.replay()
+            torch.cuda.synchronize()
+            layer.check()
+    finally:
+        q4k.q4k_set_pdl(old)
+
+
+def test_layers_on_two_streams(q4k):
+    """Two layers at once, each on a stream of its own, and the same one again: the same bits."""
+    layers = [Layer(q4k, T, 8, 2, 512, 512, T == 40, seed=T) for T in (40, 260)]
+    want = []
+    for layer in layers:
+        layer.run()
+        torch.cuda.synchronize()
+        layer.check()
+        want.append(layer.out.clone())
+    streams = [torch.cuda.Stream() for _ in layers]
+    for _ in range(10):
+        for layer, s in zip(layers, streams):
+            layer.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for layer, s in zip(layers, streams):
+            layer.run(stream=s)
+        torch.cuda.synchronize()
+        for layer, w in zip(layers, want):
+            assert torch.equal(layer.out, w)
+
+
+def test_rows_do_not_depend_on_other_rows(q4k):
+    """A row's product is the same bits whichever rows are beside it, while the kernel is the same."""
+    N, K = 96, 1024
+    w = Experts(21, 3, N, K)
+    for counts in ([3, 2, 4], [90, 0, 150]):
+        P = sum(counts)
+        x = torch.randn(P, K, generator=gen(8)).to(torch.bfloat16).to(DEV)
+        a, b = (torch.empty(P, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        starts = ints(np.concatenate([[0], np.cumsum(counts)]).tolist())
+        q4k.q4k_experts_matmul(w.dev, N, K, x, starts, a)
+        other = x.clone()
+        other[1:] = torch.randn(P - 1, K, generator=gen(9)).to(torch.bfloat16).to(DEV)
+        q4k.q4k_experts_matmul(w.dev, N, K, other, starts, b)
+        assert torch.equal(a[0], b[0])
