@@ -93,6 +93,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
     }
 }
 
+// The same for waits that are long and many in a block whose other warps need the
+// issue slots: the thread is suspended up to kIdleNs at a time instead of asking
+// again and again.
+constexpr uint32_t kIdleNs = 100000;
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, unsigned int* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kIdleNs)
+            : "memory");
+        if (ok) return true;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            atomicOr(err, 1u);
+            return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ TMA ---
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

@@ -59,10 +59,15 @@ __device__ __forceinline__ void expert_tiles(int* starts, int* tiles, int E, int
     }
 }
 
-// g / (1 + exp(-g)) with the fast exponential and division (a few units in the
-// last place of fp32, for a result that is rounded to bf16); 0 where exp(-g)
-// overflows.
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+// g / (1 + exp(-g)) with the approximate base-2 exponential and reciprocal, results
+// below 2^-126 as 0: a few units in the last place of fp32, for a result that is
+// rounded to bf16; 0 where exp(-g) overflows.
+__device__ __forceinline__ float silu(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return g * r;
+}
 
 // The expert of row tile `tile` < tiles[E]: the last e with tiles[e] <= tile.
 __device__ __forceinline__ int expert_of(const int* tiles, int E, int tile) {

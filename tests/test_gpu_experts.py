@@ -10,8 +10,10 @@ Tolerances follow from the number formats, half a step for every rounding (bf16
 * weights of the picks: exp and the division are good to 2 steps, sums of at most
   32 terms and a tree of 5 to 37; exp of a difference x has its rounding |x| times.
 * combine: k + 1 roundings of the sums' magnitudes.
-* products: the output's rounding 2^-8 |y|; the weights' rounding to bf16 where
-  the rows are many, 2^-8 sum |w x|; fp32 sums over K / 16 products of 16 and what
+* products: the output's rounding 2^-8 |y|; where the rows are many the weights as
+  bf16, w = (q - c) d + r with c the code nearest to w = 0, of two roundings: r = c d - m's,
+  and the sum's, 2^-8 sum (|w| + |r|) |x| (d is kept as two bf16; c may fall to either
+  side of a tie, 2^-20 |d|); fp32 sums over K / 16 products of 16 and what
   is behind them, 2^-23 (K/16 + 64) sum (|d sc q x| + |dmin m x|).
 * a gated product has the errors of both factors: |silu'| <= 1.1, silu(g) <= |g|.
 """
@@ -266,7 +268,7 @@ def test_gather_smallest_scale(q4k):
 # ---------------------------------------------------------------- products ---
 
 def parts(W, N, K):
-    """d sc q and dmin m of every weight, in 64 bits."""
+    """d sc q and dmin m of every weight, in 64 bits, and |r|."""
     b = W.view(N, K // 256, 144).long()
     half = W.view(N, K // 256, 144)[:, :, :4].contiguous().view(torch.float16).double()
     s = b[:, :, 4:16]
@@ -274,9 +276,12 @@ def parts(W, N, K):
     mn = torch.cat([s[..., 4:8] & 63, (s[..., 8:12] >> 4) | ((s[..., 4:8] >> 6) << 4)], -1).double()
     q = b[:, :, 16:].view(N, K // 256, 4, 32)
     q = torch.stack([q & 15, q >> 4], 3).view(N, K // 256, 8, 32).double()
-    a = (half[..., 0:1] * sc).unsqueeze(-1) * q
-    m = (half[..., 1:2] * mn).unsqueeze(-1).expand_as(a)
-    return a.reshape(N, K), m.reshape(N, K)
+    d = (half[..., 0:1] * sc).unsqueeze(-1)
+    a = d * q
+    m = (half[..., 1:2] * mn).unsqueeze(-1)
+    r = (m / d).nan_to_num(0, 15, 0).round().clamp(0, 15) * d - m
+    flat = lambda t: t.expand_as(a).reshape(N, K)  # noqa: E731
+    return flat(a), flat(m), flat(r.abs() + 2.0 ** -20 * d.abs())
 
 
 class Experts:
@@ -287,10 +292,10 @@ class Experts:
 
     def product(self, e, x):
         """x W_e^T and its bound."""
-        a, m = parts(self.w[e].reshape(self.N, -1), self.N, self.K)
+        a, m, r = parts(self.w[e].reshape(self.N, -1), self.N, self.K)
         x = x.double()
         y = x @ (a - m).T
-        tol = 2.0 ** -8 * (x.abs() @ (a - m).abs().T) + 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ (a + m).T)
+        tol = 2.0 ** -8 * (x.abs() @ ((a - m).abs() + r).T) + 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ (a + m).T)
         return y, tol
 
 
