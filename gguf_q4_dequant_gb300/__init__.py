@@ -526,6 +526,17 @@ def q4k_logits_pick(logits, M: int, V: int, out=None, pick=None, history=None, h
 
 # ------------------------------------------------------- the expert layer ---
 
+_dtypes = None  # torch's float32, bfloat16, int32, uint8, float8_e4m3fn
+
+
+def _types():
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = (torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn)
+    return _dtypes
+
+
 def _rows(t, name):
     """(rows, columns) of a tensor of a row per token or pair."""
     if isinstance(t, int) or t.dim() != 2:
@@ -533,35 +544,29 @@ def _rows(t, name):
     return t.shape
 
 
-def _float_type(t, name):
-    """q4k_type of a tensor."""
-    import torch
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name} must be {torch.float32} or {torch.bfloat16}, got {t.dtype}")
-    return int(t.dtype == torch.bfloat16)
-
-
 def _bytes(t, need, name):
     """Address of a tensor of 8-bit codes (uint8, or torch's e4m3)."""
-    import torch
-    if t is not None and not isinstance(t, int) and t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    return _tensor(t, torch.uint8, need, name)
+    _, _, _, u8, e4m3 = _types()
+    return _tensor(t, e4m3 if not isinstance(t, (int, type(None))) and t.dtype is e4m3 else u8, need, name)
 
 
 def q4k_add_norm(x, delta, weight, eps: float = 1e-6, sum=None, out=None, codes=None, scales=None, stream=None):
     """sum = x + delta [T, C] (x and sum fp32 or bf16; delta fp32 or None), and its RMS norm times weight as out
     (fp32 or bf16) and as e4m3 codes with scales [T, C/32] (uint8 exponents); each output may be None."""
-    import torch
+    f32, bf16, _, u8, _ = _types()
     T, C = _rows(x, "x")
-    kind = _float_type(x, "x")
+    n, kind = T * C, x.dtype
+    if kind is not f32 and kind is not bf16:
+        raise ValueError(f"x must be {f32} or {bf16}, got {kind}")
     if isinstance(out, int):
         raise ValueError("out must be a tensor, its type is taken from it")
-    out_kind = 0 if out is None else _float_type(out, "out")
+    out_kind = bf16 if out is None else out.dtype
+    if out_kind is not f32 and out_kind is not bf16:
+        raise ValueError(f"out must be {f32} or {bf16}, got {out_kind}")
     _check(lib().q4k_add_norm(
-        _ptr(x), kind, _tensor(delta, torch.float32, T * C, "delta"), _tensor(weight, torch.float32, C, "weight"), eps, T, C,
-        _tensor(sum, x.dtype, T * C, "sum"), _tensor(out, None if out is None else out.dtype, T * C, "out"), out_kind,
-        _bytes(codes, T * C, "codes"), _tensor(scales, torch.uint8, T * (C // 32), "scales"), _stream(stream)), "q4k_add_norm")
+        _tensor(x, kind, n, "x"), kind is bf16, _tensor(delta, f32, n, "delta"), _tensor(weight, f32, C, "weight"), eps, T, C,
+        _tensor(sum, kind, n, "sum"), _tensor(out, out_kind, n, "out"), out_kind is bf16, _bytes(codes, n, "codes"),
+        _tensor(scales, u8, T * (C // 32), "scales"), _stream(stream)), "q4k_add_norm")
 
 
 def q4k_route_workspace(T: int, E: int) -> int:
@@ -575,63 +580,60 @@ def q4k_route_workspace(T: int, E: int) -> int:
 def q4k_route(logits, k: int, weighting: int, scale: float, ids, weights, order, slots, starts, workspace, stream=None):
     """The k largest of the router's logits [T, E] of each token: ids, weights, slots [T, k], and the pairs by expert:
     order [T*k], starts [E + 1] (see include/q4k.h)."""
-    import torch
+    f32, _, i32, u8, _ = _types()
     T, E = _rows(logits, "logits")
-    i32 = torch.int32
-    ws_bytes = q4k_route_workspace(T, E) if isinstance(workspace, int) else workspace.numel() if workspace is not None else 0
+    n = T * k
+    if isinstance(workspace, int):
+        ws_bytes = q4k_route_workspace(T, E)  # an address is taken to have the bytes that the call needs
+    else:
+        ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib().q4k_route(
-        _tensor(logits, torch.float32, T * E, "logits"), T, E, k, weighting, scale, _tensor(ids, i32, T * k, "ids"),
-        _tensor(weights, torch.float32, T * k, "weights"), _tensor(order, i32, T * k, "order"),
-        _tensor(slots, i32, T * k, "slots"), _tensor(starts, i32, E + 1, "starts"),
-        _tensor(workspace, torch.uint8, 0, "workspace"), ws_bytes, _stream(stream)), "q4k_route")
+        _tensor(logits, f32, T * E, "logits"), T, E, k, weighting, scale, _tensor(ids, i32, n, "ids"),
+        _tensor(weights, f32, n, "weights"), _tensor(order, i32, n, "order"), _tensor(slots, i32, n, "slots"),
+        _tensor(starts, i32, E + 1, "starts"), _tensor(workspace, u8, 0, "workspace"), ws_bytes, _stream(stream)), "q4k_route")
 
 
 def q4k_experts_gather(X, order, k: int, out, scales=None, stream=None):
     """out[p] = X[order[p] // k] (bf16 [T*k, C]) from rows X [T, C] in bf16, or in e4m3 codes with their scales."""
-    import torch
+    _, bf16, i32, u8, _ = _types()
     T, C = _rows(X, "X")
-    x = _tensor(X, torch.bfloat16, T * C, "X") if scales is None else _bytes(X, T * C, "X")
+    x = _tensor(X, bf16, T * C, "X") if scales is None else _bytes(X, T * C, "X")
     _check(lib().q4k_experts_gather(
-        x, _tensor(scales, torch.uint8, T * (C // 32), "scales"), _tensor(order, torch.int32, T * k, "order"), T, k, C,
-        _tensor(out, torch.bfloat16, T * k * C, "out"), _stream(stream)), "q4k_experts_gather")
+        x, _tensor(scales, u8, T * (C // 32), "scales"), _tensor(order, i32, T * k, "order"), T, k, C,
+        _tensor(out, bf16, T * k * C, "out"), _stream(stream)), "q4k_experts_gather")
 
 
 def _experts(N, K, X, starts, Y):
-    """(E, X, starts, pairs, Y) of an experts' product, checked."""
-    import torch
+    """(E, bytes of E packed matrices, X, starts, pairs, Y) of an experts' product, checked."""
+    _, bf16, i32, _, _ = _types()
     pairs, cols = _rows(X, "X")
     if cols != K:
         raise ValueError(f"X has {cols} columns, K is {K}")
     E = _count(starts, "starts") - 1
-    return (E, _tensor(X, torch.bfloat16, pairs * K, "X"), _tensor(starts, torch.int32, E + 1, "starts"), pairs,
-            _tensor(Y, torch.bfloat16, pairs * max(N, 0), "Y"))
+    return (E, E * _w_bytes(N, K) if _dims_valid(N, K) else 0, _tensor(X, bf16, pairs * K, "X"),
+            _tensor(starts, i32, E + 1, "starts"), pairs, _tensor(Y, bf16, pairs * max(N, 0), "Y"))
 
 
 def q4k_experts_matmul(W, N: int, K: int, X, starts, Y, stream=None):
     """Y[p] = X[p] W_e^T (bf16) for the rows p of each expert e: starts [E + 1], W the E packed matrices [N, K]."""
-    import torch
-    E, x, st, pairs, y = _experts(N, K, X, starts, Y)
-    need = E * _w_bytes(N, K) if _dims_valid(N, K) else 0
-    _check(lib().q4k_experts_matmul(_tensor(W, torch.uint8, need, "W"), E, N, K, x, st, pairs, y, _stream(stream)),
+    E, need, x, st, pairs, y = _experts(N, K, X, starts, Y)
+    _check(lib().q4k_experts_matmul(_tensor(W, _types()[3], need, "W"), E, N, K, x, st, pairs, y, _stream(stream)),
            "q4k_experts_matmul")
 
 
 def q4k_experts_gated(gate, up, N: int, K: int, X, starts, Y, stream=None):
     """Y[p] = silu(X[p] gate_e^T) * (X[p] up_e^T) (bf16) for the rows p of each expert e."""
-    import torch
-    E, x, st, pairs, y = _experts(N, K, X, starts, Y)
-    need = E * _w_bytes(N, K) if _dims_valid(N, K) else 0
-    _check(lib().q4k_experts_gated(_tensor(gate, torch.uint8, need, "gate"), _tensor(up, torch.uint8, need, "up"), E, N, K, x,
-                                   st, pairs, y, _stream(stream)), "q4k_experts_gated")
+    E, need, x, st, pairs, y = _experts(N, K, X, starts, Y)
+    u8 = _types()[3]
+    _check(lib().q4k_experts_gated(_tensor(gate, u8, need, "gate"), _tensor(up, u8, need, "up"), E, N, K, x, st, pairs, y,
+                                   _stream(stream)), "q4k_experts_gated")
 
 
 def q4k_experts_combine(Y, slots, weights, out, base=None, stream=None):
     """out[t] = base[t] + sum_j weights[t, j] * Y[slots[t, j]] (fp32 [T, C]); slots below 0 add nothing."""
-    import torch
+    f32, bf16, i32, _, _ = _types()
     pairs, C = _rows(Y, "Y")
     T, k = _rows(slots, "slots")
-    f32 = torch.float32
     _check(lib().q4k_experts_combine(
-        _tensor(Y, torch.bfloat16, pairs * C, "Y"), pairs, _tensor(slots, torch.int32, T * k, "slots"),
-        _tensor(weights, f32, T * k, "weights"), _tensor(base, f32, T * C, "base"), T, k, C, _tensor(out, f32, T * C, "out"),
-        _stream(stream)), "q4k_experts_combine")
+        _tensor(Y, bf16, pairs * C, "Y"), pairs, _tensor(slots, i32, T * k, "slots"), _tensor(weights, f32, T * k, "weights"),
+        _tensor(base, f32, T * C, "base"), T, k, C, _tensor(out, f32, T * C, "out"), _stream(stream)), "q4k_experts_combine")

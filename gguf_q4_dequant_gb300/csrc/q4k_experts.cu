@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(32 * kExWarps, 2)
     if (lane == 0) {
         for (int i = 0; i < kExStages; ++i) mbar_init(bar + 8 * i, 1);
         fence_barrier_init();
+        tma_prefetch_desc(words);
     }
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();

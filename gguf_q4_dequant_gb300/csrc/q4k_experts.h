@@ -29,33 +29,38 @@ struct ExpertRows {
 // The row tiles (of up to NT rows) of every expert, by one warp: starts[0 .. E]
 // (shared memory, inside [0, pairs] whatever the caller's array held) are made
 // ascending, tiles[e] becomes the number of tiles before expert e, tiles[E] of all.
+// A lane has (E + 32) / 32 entries side by side.
 template <int NT>
 __device__ __forceinline__ void expert_tiles(int* starts, int* tiles, int E, int lane) {
-    int run = 0, high = 0;
-    for (int e0 = 0; e0 <= E; e0 += 32) {
-        const int e = e0 + lane;
-        int hi = e <= E ? starts[e] : 0;
+    const int per = E / 32 + 1, e0 = lane * per, e1 = min(e0 + per, E + 1);
+    int high = 0;  // the highest up to this lane's last
+    for (int e = e0; e < e1; ++e) high = max(high, starts[e]);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, hi, o);
-            if (lane >= o) hi = max(hi, t);
-        }
-        hi = max(hi, high);
-        int prev = __shfl_up_sync(0xffffffffu, hi, 1);
-        if (lane == 0) prev = high;
-        // the tiles of expert e - 1, whose rows end at starts[e]
-        int s = e > 0 && e <= E ? (hi - prev + NT - 1) / NT : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, high, o);
+        if (lane >= o) high = max(high, t);
+    }
+    int prev = __shfl_up_sync(0xffffffffu, high, 1);
+    if (lane == 0) prev = e1 > e0 ? starts[0] : 0;
+    // the tiles of experts e0 - 1 .. e1 - 2, whose rows end at starts[e0 .. e1 - 1]
+    int sum = 0;
+    for (int e = e0, p = prev; e < e1; ++e) {
+        const int hi = max(p, starts[e]);
+        starts[e] = hi;
+        sum += (hi - p + NT - 1) / NT;
+        p = hi;
+    }
+    int at = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += t;
-        }
-        if (e <= E) {
-            starts[e] = hi;
-            tiles[e] = run + s;
-        }
-        run += __shfl_sync(0xffffffffu, s, 31);
-        high = __shfl_sync(0xffffffffu, hi, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += t;
+    }
+    at -= sum;
+    for (int e = e0, p = prev; e < e1; ++e) {
+        at += (starts[e] - p + NT - 1) / NT;
+        p = starts[e];
+        tiles[e] = at;
     }
 }
 

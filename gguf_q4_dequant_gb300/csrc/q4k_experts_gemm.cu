@@ -71,7 +71,9 @@ struct EgScale {
 };
 // unit: the q - c of dequant8 come as this much of themselves, 2^-6 for low nibbles, 2^-2 for high ones
 __device__ __forceinline__ EgScale eg_scale(float d1, float m1, float unit) {
-    const float c = fminf(fmaxf(rintf(__fdividef(m1, d1)), 0.f), 15.f);  // (0 where the quotient is not a number)
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d1));
+    const float c = fminf(fmaxf(rintf(m1 * inv), 0.f), 15.f);  // (0 where the quotient is not a number)
     const float d = d1 * (1.f / unit);
     EgScale s;
     s.dh = __float2bfloat162_rn(d);
