@@ -91,13 +91,17 @@ class Server:
             q4k.q4k_cache_append(cache, l, seqs, starts, *ys, q, m.heads, self.rope, 2, m.q_norm, m.k_norm)
             q4k.q4k_cache_attention(cache, l, seqs, starts, q, att, m.heads, max(news), m.dim ** -0.5,
                                     workspace=self.workspace)
-            x = x + 0.02 * q4k.matmul(m.w[l, "o"], m.hidden, m.heads * m.dim, att.view(T, -1))
-            ys = [torch.empty(T, m.ffn, **f32) for _ in range(2)]
-            q4k.q4k_matmul_multi([m.w[l, "gate"], m.w[l, "up"]], [m.ffn] * 2, m.hidden, rms(x, m.norm), T, ys)
-            act = (torch.nn.functional.silu(ys[0]) * ys[1] * m.act_scale).to(torch.bfloat16)
-            x = x + q4k.matmul(m.w[l, "down"], m.hidden, m.ffn, act)
+            x = self.feed_forward(l, x, 0.02 * q4k.matmul(m.w[l, "o"], m.hidden, m.heads * m.dim, att.view(T, -1)))
         last = rms(x[ends.to(m.device) - 1], m.norm)
         return q4k.matmul(m.w["head"], m.vocab, m.hidden, last)
+
+    def feed_forward(self, l, x, delta):
+        """The residual stream x [T, hidden] behind the feed-forward part of layer l; delta: what its attention adds."""
+        m, x, T = self.m, x + delta, x.shape[0]
+        ys = [torch.empty(T, m.ffn, dtype=torch.float32, device=m.device) for _ in range(2)]
+        q4k.q4k_matmul_multi([m.w[l, "gate"], m.w[l, "up"]], [m.ffn] * 2, m.hidden, rms(x, m.norm), T, ys)
+        act = (torch.nn.functional.silu(ys[0]) * ys[1] * m.act_scale).to(torch.bfloat16)
+        return x + q4k.matmul(m.w[l, "down"], m.hidden, m.ffn, act)
 
     def pick(self, seqs, logits, repeat=1.3, mask=None):
         """Greedy tokens under a repeat penalty over each sequence's tokens."""

@@ -434,7 +434,8 @@ enum q4k_weighting {
  *   ids, weights, slots  device, [T][k] int32, floats, int32
  *   order   device, [T*k] int32;  starts  device, [E+1] int32
  *   ws      device, ws_bytes >= q4k_route_workspace(T, E), 4-byte aligned; needs no
- *           set-up, and holds nothing between calls
+ *           set-up and holds nothing between calls; calls that may run at the same
+ *           time need one each
  * 1 <= k <= 32, k <= E <= 1024; T >= 1, T*k < 2^31; scale finite.
  */
 int64_t q4k_route_workspace(int64_t T, int64_t E); /* 4 E (ceil(T / 64) + 1) */
@@ -459,10 +460,15 @@ int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* orde
  * the e-th of E packed matrices [N][K] that follow one another; accumulated in
  * fp32 and rounded once to bf16. q4k_experts_gated takes two of them and gives
  * Y[p] = g / (1 + exp(-g)) * u with g = X[p] gate_e^T and u = X[p] up_e^T in fp32.
+ * With pairs <= 10 min(E, pairs) the weights enter exactly, each row's sums in
+ * fp32; with more the tcgen05 tensor cores take them as bf16 (off by 2^-8 (|w| +
+ * |r|) at most, r the weight of the code nearest to 0; see q4k_matmul_bf16, whose
+ * weights of 17 rows and more are off by 2^-8 |w|).
  * Rows before starts[0] and from starts[E] on are left as they are; starts is
  * taken as ascending and inside [0, pairs] (values are clamped to that).
  *   W, gate, up  device, E*N*K/256*144 bytes, 16-byte aligned
- *   X  device, [pairs][K] bf16, values below 2^64;  Y  device, [pairs][N] bf16
+ *   X  device, [pairs][K] bf16, values below 2^64 (those below 2^-56 may count as
+ *      zero);  Y  device, [pairs][N] bf16
  *   starts  device, [E+1] int32
  * 1 <= E <= 1024, N >= 1, E*N < 2^31; K a multiple of 256, 256 .. 2^24; 1 <= pairs < 2^31.
  */

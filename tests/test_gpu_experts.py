@@ -351,7 +351,7 @@ def test_experts_many_rows(q4k, E, N, K, counts, gated):
     check_experts(q4k, E, N, K, counts, gated, seed=E * N + K + 1, lead=3 if N % 2 else 0)
 
 
-@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 40])
+@pytest.mark.parametrize("scale", [2.0 ** -50, 2.0 ** -40, 2.0 ** 40, 2.0 ** 60])
 def test_experts_scale_of_rows(q4k, scale):
     check_experts(q4k, 2, 40, 512, [3, 9], False, seed=3, scale=scale)
     check_experts(q4k, 2, 40, 512, [200, 90], False, seed=3, scale=scale)
