@@ -359,16 +359,27 @@ cudaError_t experts_setup(DeviceInfo&) {
     return e;
 }
 
-// The mean number of rows of an expert that has any, as far as the host knows
-// (all experts, or as many as there are rows), decides between the kernels: the
-// one for few rows goes over the weights again for every eight rows of an expert,
-// the tcgen05 kernel's time hardly depends on the rows while they are few. 128
-// experts, gated 768 x 2048: 8 rows each 92 us for 109, 12 rows 124 for 109; down
-// 2048 x 768: 8 rows 49 us for 61, 12 rows 64.6 for 61.6. (Wider tiles of 16 and
+// The two kernels' times in us, from the sizes that the host knows: experts with
+// rows are taken to be all of them or as many as there are rows, with equal
+// shares. The one for few rows goes over the words again for every eight rows of
+// an expert, 1.25 ns a step of 32 weight rows and 256 k on all of the GPU; the
+// tcgen05 kernel's blocks take 2 us for 256 k of a unit, whatever rows it has, and 1.6
+// for its end, and have nothing to share out when there are few units. 128 experts, gated
+// 768 x 2048: 8 rows each 92 us for 109 (model: 97, 110), 12 rows 124 for 109 (128, 110); down
+// 2048 x 768: 8 rows 49 us for 61 (51, 57), 12 rows 65 for 62 (66, 57). (Tiles of 16 and
 // 32 rows in the first kernel were slower than its 8 or the second at every size.)
+static bool many_rows(const ExpertArgs& a, const DeviceInfo& dev) {
+    const double pairs = a.rows.pairs, busy = pairs < a.rows.experts ? pairs : a.rows.experts, mats = a.W2 != nullptr ? 2 : 1;
+    const double KB = static_cast<double>(a.K / kBlockWeights);
+    const double slabs = static_cast<double>((a.N + kExRows - 1) / kExRows);
+    double tiles = pairs / kExTile + 0.5 * busy;
+    tiles = tiles > busy ? tiles : busy;
+    const double few = 5.0 + 1.25e-3 * tiles * slabs * KB * mats;
+    return experts_gemm_us(a, dev) < few;
+}
+
 cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
-    const int64_t busy = a.rows.pairs < a.rows.experts ? a.rows.pairs : a.rows.experts;
-    if (a.rows.pairs > 10 * busy) return launch_experts_gemm(a, stream, dev, pdl);
+    if (many_rows(a, dev)) return launch_experts_gemm(a, stream, dev, pdl);
     return a.W2 != nullptr ? launch_few<true>(a, stream, dev, pdl) : launch_few<false>(a, stream, dev, pdl);
 }
 

@@ -153,6 +153,7 @@ struct ExpertArgs {
 cudaError_t launch_experts(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
 cudaError_t experts_setup(DeviceInfo& dev);
 cudaError_t launch_experts_gemm(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
+double experts_gemm_us(const ExpertArgs& a, const DeviceInfo& dev);  // its time, about
 cudaError_t experts_gemm_setup();
 
 // A 2-D byte map {K/256*144, N} of packed rows, box one super-block of `rows` rows

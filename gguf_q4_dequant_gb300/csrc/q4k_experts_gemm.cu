@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kEgThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             tma_prefetch_desc(&mapW);
-            const uint64_t pol = policy_evict_first();
+            // (kept in L2: the words of an expert with several row tiles are read for each; 155 us, 159)
+            const uint64_t pol = policy_evict_last();
             uint32_t it = 0;
             bool ok = true;
             for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -413,6 +414,15 @@ cudaError_t experts_gemm_setup() {
     const cudaError_t r = cudaFuncSetAttribute(q4k_experts_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                eg_smem(kMaxExperts));
     return e != cudaSuccess ? e : r;
+}
+
+// See launch_experts.
+double experts_gemm_us(const ExpertArgs& a, const DeviceInfo& dev) {
+    const int64_t pairs = a.rows.pairs, busy = pairs < a.rows.experts ? pairs : a.rows.experts;
+    const int64_t cols = a.W2 != nullptr ? kEgBM : 2 * kEgBM, each = (pairs + busy - 1) / busy;
+    const double units = static_cast<double>(busy) * ((each + kEgBN - 1) / kEgBN) * ((a.N + cols - 1) / cols);
+    const double rounds = units <= dev.num_sms ? 1.0 : units / dev.num_sms + 0.5;
+    return 4.0 + rounds * (1.6 + 2.0 * static_cast<double>(a.K / kBlockWeights));
 }
 
 cudaError_t launch_experts_gemm(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl) {

@@ -460,10 +460,10 @@ int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* orde
  * the e-th of E packed matrices [N][K] that follow one another; accumulated in
  * fp32 and rounded once to bf16. q4k_experts_gated takes two of them and gives
  * Y[p] = g / (1 + exp(-g)) * u with g = X[p] gate_e^T and u = X[p] up_e^T in fp32.
- * With pairs <= 10 min(E, pairs) the weights enter exactly, each row's sums in
- * fp32; with more the tcgen05 tensor cores take them as bf16 (off by 2^-8 (|w| +
- * |r|) at most, r the weight of the code nearest to 0; see q4k_matmul_bf16, whose
- * weights of 17 rows and more are off by 2^-8 |w|).
+ * By the sizes (never by what the arrays hold) one of two kernels runs: for few
+ * rows the weights enter exactly; for many the tcgen05 tensor cores take them as
+ * bf16, off by 2^-8 (|w| + |r|) at most, r the weight of the code nearest to 0 (as
+ * q4k_matmul_bf16's, by 2^-8 |w|, for 17 rows and more).
  * Rows before starts[0] and from starts[E] on are left as they are; starts is
  * taken as ascending and inside [0, pairs] (values are clamped to that).
  *   W, gate, up  device, E*N*K/256*144 bytes, 16-byte aligned

@@ -346,7 +346,9 @@ def test_experts_small(q4k, E, N, K, counts, gated):
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("E,N,K,counts", [
     (2, 128, 512, [128, 127]), (2, 257, 256, [300, 129]), (3, 192, 768, [256, 1, 512]), (2, 64, 2048, [700, 15]),
-    (4, 100, 512, [0, 1000, 0, 3]), (1, 384, 1024, [513])])
+    (4, 100, 512, [0, 1000, 0, 3]), (1, 384, 1024, [513]), (1, 256, 256, [4100]), (2, 300, 256, [2000, 2501]),
+    (3, 640, 512, [1537, 0, 1500]), (3, 1000, 768, [900, 193, 1700]), (5, 512, 1280, [300, 1, 0, 192, 800]),
+    (1, 129, 256, [9000]), (2, 2047, 512, [400, 385])])
 def test_experts_many_rows(q4k, E, N, K, counts, gated):
     check_experts(q4k, E, N, K, counts, gated, seed=E * N + K + 1, lead=3 if N % 2 else 0)
 
@@ -355,12 +357,13 @@ def test_experts_many_rows(q4k, E, N, K, counts, gated):
 def test_experts_scale_of_rows(q4k, scale):
     check_experts(q4k, 2, 40, 512, [3, 9], False, seed=3, scale=scale)
     check_experts(q4k, 2, 40, 512, [200, 90], False, seed=3, scale=scale)
+    check_experts(q4k, 2, 256, 256, [2500, 2000], False, seed=3, scale=scale)
 
 
 def test_experts_rows_with_infinity(q4k):
     """A row with an infinity or a NaN spoils no other row."""
-    for counts in ([4, 5], [130, 200]):
-        P, N, K = sum(counts), 64, 512
+    for counts in ([4, 5], [130, 200], [3000, 2900]):
+        P, N, K = sum(counts), 256 if sum(counts) > 1000 else 64, 512
         w = Experts(9, 2, N, K)
         x = torch.randn(P, K, generator=gen(1)).to(torch.bfloat16)
         clean, dirty = (torch.empty(P, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
@@ -543,7 +546,8 @@ class Layer:
 
 
 @pytest.mark.parametrize("T,E,top,hidden,ffn,eight", [(1, 8, 2, 512, 256, False), (5, 16, 4, 512, 512, True),
-                                                      (33, 8, 3, 256, 768, False), (300, 6, 2, 512, 256, True)])
+                                                      (33, 8, 3, 256, 768, False), (300, 6, 2, 512, 256, True),
+                                                      (3000, 6, 2, 512, 512, True)])
 def test_layer(q4k, T, E, top, hidden, ffn, eight):
     layer = Layer(q4k, T, E, top, hidden, ffn, eight, seed=T)
     layer.run()
@@ -551,7 +555,7 @@ def test_layer(q4k, T, E, top, hidden, ffn, eight):
 
 
 @pytest.mark.parametrize("mode", [0, 1, 2])
-@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("T", [3, 150, 2600])
 def test_layer_captured(q4k, mode, T):
     """A captured layer replays right on new inputs, in every launch mode, back to back with itself."""
     layer = Layer(q4k, T, 6, 2, 256, 256, True, seed=3)
@@ -579,7 +583,7 @@ def test_layer_captured(q4k, mode, T):
 
 def test_layers_on_two_streams(q4k):
     """Two layers at once, each on a stream of its own, and the same one again: the same bits."""
-    layers = [Layer(q4k, T, 8, 2, 512, 512, T == 40, seed=T) for T in (40, 260)]
+    layers = [Layer(q4k, T, 8, 2, 512, 512, T == 40, seed=T) for T in (40, 2800)]
     want = []
     for layer in layers:
         layer.run()
@@ -602,7 +606,7 @@ def test_rows_do_not_depend_on_other_rows(q4k):
     """A row's product is the same bits whichever rows are beside it, while the kernel is the same."""
     N, K = 96, 1024
     w = Experts(21, 3, N, K)
-    for counts in ([3, 2, 4], [90, 0, 150]):
+    for counts in ([3, 2, 4], [90, 0, 150], [2900, 0, 4000]):
         P = sum(counts)
         x = torch.randn(P, K, generator=gen(8)).to(torch.bfloat16).to(DEV)
         a, b = (torch.empty(P, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
