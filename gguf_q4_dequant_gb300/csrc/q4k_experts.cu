@@ -31,7 +31,9 @@
 
 namespace q4k {
 
-constexpr int kExWarps = 8;                            // warps of a block
+// Warps of a block, blocks of an SM: 12 warps with 168 registers each (128 experts
+// with four rows each, gated: 62 us; 16 warps with 128, 68; 8 with 255, 77).
+constexpr int kExWarps = 4, kExBlocks = 3;
 constexpr int kExRows = 32;                            // weight rows of a step, output columns of a unit
 constexpr int kExStage = kExRows * kBlockBytes;        // 4608
 constexpr int kExTile = 8;                             // rows of x of a unit
@@ -107,6 +109,7 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
                 xs[h][i] = *reinterpret_cast<const uint32_t*>(&y);
             }
         }
+        uint32_t a[2][2][2][4];  // [row tile][nibble half][which 16 k]
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const uint2 q0 = *reinterpret_cast<const uint2*>(wrow + 16 * m * kBlockBytes + 16 + 32 * c + 8 * t4);
@@ -118,41 +121,59 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
                                        __byte_perm(q0.x, 0, 0x4342), __byte_perm(q1.x, 0, 0x4342)},
                                       {__byte_perm(q0.y, 0, 0x4140), __byte_perm(q1.y, 0, 0x4140),
                                        __byte_perm(q0.y, 0, 0x4342), __byte_perm(q1.y, 0, 0x4342)}};
-            uint32_t a[2][2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    a[0][i][k] = p[i][k] & 0x000F000Fu;
+                    a[m][0][i][k] = p[i][k] & 0x000F000Fu;
                     const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p[i][k]),
-                                                     *reinterpret_cast<const __nv_bfloat162*>(&a[0][i][k]));
-                    a[1][i][k] = *reinterpret_cast<const uint32_t*>(&y);
+                                                     *reinterpret_cast<const __nv_bfloat162*>(&a[m][0][i][k]));
+                    a[m][1][i][k] = *reinterpret_cast<const uint32_t*>(&y);
                 }
+        }
+        float s[2][2][2], f[2][2][4];
+        uint32_t mn[2][2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int j = 2 * c + h;
-                float s[2], f[4];
-                uint32_t mn[4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t scw = j < 4 ? sb[m][r].sc_lo : sb[m][r].sc_hi;
                     const uint32_t mw = j < 4 ? sb[m][r].m_lo : sb[m][r].m_hi;
                     // (2^23 + sc) d - 2^23 d: both exact, so the FMA rounds sc d once
                     const float dh = h ? d[m][r] * 0.0625f : d[m][r];
-                    s[r] = fmaf(__uint_as_float(__byte_perm(scw, 0x4B000000u, 0x7440u | (j & 3))), dh, -8388608.f * dh);
-                    mn[r] = mn[r + 2] = __byte_perm(mw, 0, (j & 3) * 0x0101 | 0x4040);
+                    s[m][h][r] = fmaf(__uint_as_float(__byte_perm(scw, 0x4B000000u, 0x7440u | (j & 3))), dh, -8388608.f * dh);
+                    mn[m][h][r] = mn[m][h][r + 2] = __byte_perm(mw, 0, (j & 3) * 0x0101 | 0x4040);
                 }
-                mma_bf16_zero(f, a[h][0], xs[h][0], xs[h][1]);
-                mma_bf16(f, a[h][1], xs[h][2], xs[h][3]);
-                if (j == 0) mma_bf16_zero(low[m], mn, xs[h][0], xs[h][1]);
-                else mma_bf16(low[m], mn, xs[h][0], xs[h][1]);
-                mma_bf16(low[m], mn, xs[h][2], xs[h][3]);
-                acc[m][0] = fmaf(f[0], s[0], acc[m][0]);
-                acc[m][1] = fmaf(f[1], s[0], acc[m][1]);
-                acc[m][2] = fmaf(f[2], s[1], acc[m][2]);
-                acc[m][3] = fmaf(f[3], s[1], acc[m][3]);
             }
+        // a sum's next product comes four products later: the tensor core takes them one behind the other
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma_bf16_zero(f[m][h], a[m][h][0], xs[h][0], xs[h][1]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (c == 0) mma_bf16_zero(low[m], mn[m][0], xs[0][0], xs[0][1]);
+            else mma_bf16(low[m], mn[m][0], xs[0][0], xs[0][1]);
         }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma_bf16(f[m][h], a[m][h][1], xs[h][2], xs[h][3]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) mma_bf16(low[m], mn[m][0], xs[0][2], xs[0][3]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) mma_bf16(low[m], mn[m][1], xs[1][0], xs[1][1]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(f[m][h][i], s[m][h][i >> 1], acc[m][i]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) mma_bf16(low[m], mn[m][1], xs[1][2], xs[1][3]);
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -165,7 +186,7 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
 }
 
 template <bool kGated>
-__global__ void __launch_bounds__(32 * kExWarps, 2)
+__global__ void __launch_bounds__(32 * kExWarps, kExBlocks)
     q4k_experts_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map2, const uint16_t* X,
                        const ExpertRows rows, int N, int K, int wk, uint16_t* Y, unsigned int* err) {
     extern __shared__ __align__(128) uint8_t ex_smem_raw[];
@@ -319,10 +340,10 @@ cudaError_t launch_few(const ExpertArgs& a, cudaStream_t stream, const DeviceInf
     const int KB = static_cast<int>(a.K / kBlockWeights);
     // wk, the warps that share K: few units are split further, so that every warp
     // of the GPU has some of the words on their way (8 experts of 128 with one row
-    // each, gated 768 x 2048: 12.6 us with 8, 32 with 1); many are not, as the warps of
-    // a unit wait for one another (64 rows for each of 128 experts of 2048 x 768: 37 us
-    // with 1, 44 with 2). In between the units' count decides how full the last
-    // round is (128 experts with four rows each, gated: 76, 73, 68, 72 us with 1, 2, 4, 8).
+    // each, gated 768 x 2048: 12.2 us with 4, 14.6 with 2); many are not, as the warps of
+    // a unit wait for one another (four rows for each of 128 experts of 2048 x 768: 37 us
+    // with 1, 43 with 2). In between it counts how full the last round is (5 tokens to
+    // 2 of 8 experts of 4096 x 12288: 72, 51, 46 us with 1, 2, 4).
     const int64_t tiles = busy > a.rows.pairs / kExTile ? busy : a.rows.pairs / kExTile;
     int wk = kGated ? 2 : 1, per = 1;
     double best = 1e300;
@@ -330,7 +351,7 @@ cudaError_t launch_few(const ExpertArgs& a, cudaStream_t stream, const DeviceInf
         const int nk = kGated ? w / 2 : w;
         if (nk > KB) break;
         int p = static_cast<int>((228 * 1024) / (ex_smem(w, a.rows.experts).total + 1024));
-        p = p < 1 ? 1 : p < 2 ? p : 2;
+        p = p < 1 ? 1 : p < kExBlocks ? p : kExBlocks;
         const double groups = static_cast<double>(dev.num_sms) * p * kExWarps / w;
         // the experts with rows are known on the device only: half a round is lost on average
         const double rounds = static_cast<double>(tiles * slabs) / groups + 0.5;
@@ -362,19 +383,19 @@ cudaError_t experts_setup(DeviceInfo&) {
 // The two kernels' times in us, from the sizes that the host knows: experts with
 // rows are taken to be all of them or as many as there are rows, with equal
 // shares. The one for few rows goes over the words again for every eight rows of
-// an expert, 1.25 ns a step of 32 weight rows and 256 k on all of the GPU; the
+// an expert, 1.05 ns a step of 32 weight rows and 256 k on all of the GPU; the
 // tcgen05 kernel's blocks take 2 us for 256 k of a unit, whatever rows it has, and 1.6
 // for its end, and have nothing to share out when there are few units. 128 experts, gated
-// 768 x 2048: 8 rows each 92 us for 109 (model: 97, 110), 12 rows 124 for 109 (128, 110); down
-// 2048 x 768: 8 rows 49 us for 61 (51, 57), 12 rows 65 for 62 (66, 57). (Tiles of 16 and
-// 32 rows in the first kernel were slower than its 8 or the second at every size.)
+// 768 x 2048: 8 rows each 82 us for 109 (here 82, 110), 12 rows 103 for 109 (108, 110), 16 rows
+// 129 (here) for 109; down 2048 x 768: 8 rows 46 us for 61 (44, 57), 12 rows 60 for 62 (57, 57).
+// (Tiles of 16 and 32 rows in the first kernel were slower than its 8 or the second at every size.)
 static bool many_rows(const ExpertArgs& a, const DeviceInfo& dev) {
     const double pairs = a.rows.pairs, busy = pairs < a.rows.experts ? pairs : a.rows.experts, mats = a.W2 != nullptr ? 2 : 1;
     const double KB = static_cast<double>(a.K / kBlockWeights);
     const double slabs = static_cast<double>((a.N + kExRows - 1) / kExRows);
     double tiles = pairs / kExTile + 0.5 * busy;
     tiles = tiles > busy ? tiles : busy;
-    const double few = 5.0 + 1.25e-3 * tiles * slabs * KB * mats;
+    const double few = 5.0 + 1.05e-3 * tiles * slabs * KB * mats;
     return experts_gemm_us(a, dev) < few;
 }
 
