@@ -24,8 +24,9 @@
 //   warp 0       W producer: {144 B, 128 rows} of packed words per tile and 256 k (TMA)
 //   warps 1, 2   MMA issuers, one a tile
 //   warp 3       X producer: the tile's rows x 64 k (TMA, 128-byte swizzle)
-//   warps 4..7   the end of a unit: TMEM -> registers -> (silu(g) u) -> bf16 -> Y
-//   warps 8..23  dequantisers, four groups of 128 threads: two a tile, each with every
+//   warps 4..11  the end of a unit: TMEM -> registers -> (silu(g) u) -> bf16 -> Y, four
+//                warps with a tile each, or with half of a gated unit's rows of x
+//   warps 12..27 dequantisers, four groups of 128 threads: two a tile, each with every
 //                other 64 k, a thread with a weight row of them and 32 columns of TMEM
 // All waits are bounded (see mbar_wait).
 #include <cuda_bf16.h>
@@ -44,7 +45,7 @@ constexpr int kEgStep = 64;                   // k of a step
 constexpr int kEgXStages = 4, kEgWStages = 3;  // W stages of each tile
 constexpr int kEgXStage = kEgBN * 128;
 constexpr int kEgWStage = kEgBM * kBlockBytes;
-constexpr int kEgEpiWarp = 4, kEgDeqWarp = 8, kEgDeqWarps = 16;
+constexpr int kEgEpiWarp = 4, kEgDeqWarp = 12, kEgDeqWarps = 16;
 constexpr int kEgThreads = 32 * (kEgDeqWarp + kEgDeqWarps);
 constexpr int kEgOffW = kEgXStages * kEgXStage;
 constexpr int kEgOffBar = kEgOffW + 2 * kEgWStages * kEgWStage;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
         for (int i = 0; i < 2 * kEgWStages; ++i) mbar_init(bwf + 8 * i, 1), mbar_init(bwe + 8 * i, kEgDeqWarps / 2);
         for (int i = 0; i < kEgXStages; ++i) mbar_init(bxf + 8 * i, 1), mbar_init(bxe + 8 * i, 2);
         for (int i = 0; i < 4; ++i) mbar_init(baf + 8 * i, kEgDeqWarps / 4), mbar_init(bae + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(bcf + 8 * i, 1), mbar_init(bce + 8 * i, 4);
+        for (int i = 0; i < 2; ++i) mbar_init(bcf + 8 * i, 1), mbar_init(bce + 8 * i, kGated ? 8 : 4);
         mbar_init(bend, 2);
         fence_barrier_init();
     }
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
             }
         }
     } else if (warp >= kEgEpiWarp) {
-        const int q = warp & 3;
+        const int q = warp & 3, part = (warp - kEgEpiWarp) >> 2;
         uint32_t n = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kEgThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const int rows_out = w.n0 + 32 * q + lane < N ? w.rows : 0;
-                for (int c0 = 0; c0 < w.rows; c0 += 16) {
+                for (int c0 = 16 * part; c0 < w.rows; c0 += 32) {
                     uint32_t g[16], up[16];
                     tmem_ld_32x32b(acc + c0, g);
                     tmem_ld_32x32b(acc + kEgBN + c0, up);
@@ -355,24 +356,21 @@ __global__ void __launch_bounds__(kEgThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bce), mbar_arrive(bce + 8);
             } else {
-#pragma unroll 1
-                for (int tile = 0; tile < 2; ++tile) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_idle(bcf + 8 * tile, n & 1, err))) { ok = false; break; }
-                    tc_fence_after();
-                    const int rows_out = w.n0 + tile * kEgBM + 32 * q + lane < N ? w.rows : 0;
-                    for (int c0 = 0; c0 < w.rows; c0 += 16) {
-                        uint32_t a[16];
-                        tmem_ld_32x32b(acc + tile * kEgBN + c0, a);
-                        tmem_ld_wait();
-                        float v[16];
+                if (!__all_sync(0xffffffffu, mbar_wait_idle(bcf + 8 * part, n & 1, err))) break;
+                tc_fence_after();
+                const int rows_out = w.n0 + part * kEgBM + 32 * q + lane < N ? w.rows : 0;
+                for (int c0 = 0; c0 < w.rows; c0 += 16) {
+                    uint32_t a[16];
+                    tmem_ld_32x32b(acc + part * kEgBN + c0, a);
+                    tmem_ld_wait();
+                    float v[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(a[j]);
-                        store(base + 2 * kEgBM * tile + static_cast<uint64_t>(step) * c0, v, rows_out - c0);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bce + 8 * tile);
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(a[j]);
+                    store(base + 2 * kEgBM * part + static_cast<uint64_t>(step) * c0, v, rows_out - c0);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bce + 8 * part);
             }
         }
     }
