@@ -379,9 +379,7 @@ int q4k_logits_pick(const float* logits, int64_t M, int64_t V, float* out, int64
  * and the order of the rows by expert (q4k_route, from the logits of the
  * router's product), the rows in that order (q4k_experts_gather), the experts'
  * products (q4k_experts_gated for gate and up, q4k_experts_matmul for down),
- * and the way back with the weights applied (q4k_experts_combine). The pages of
- * the reference name the gathered product of quantised experts (mlx-rs #356:
- * gather_qmm, QuantizedSwitchLinear) and the norms of every layer.
+ * and the way back with the weights applied (q4k_experts_combine).
  *
  * The rules of the calls above hold: asynchronous on `stream`, no allocation,
  * no host synchronisation, capturable, arguments checked before any launch,
@@ -421,7 +419,7 @@ enum q4k_weighting {
     Q4K_ROUTE_SOFTMAX = 0,     /* softmax over all experts */
     Q4K_ROUTE_SOFTMAX_TOP = 1, /* softmax over the picked ones */
     Q4K_ROUTE_SIGMOID = 2,     /* 1 / (1 + exp(-logit)) */
-    Q4K_ROUTE_SIGMOID_TOP = 3  /* the same divided by their sum over the picked ones */
+    Q4K_ROUTE_SIGMOID_TOP = 3  /* the same divided by their sum over the picked ones (0 where the largest logit is below -1000) */
 };
 
 /*
