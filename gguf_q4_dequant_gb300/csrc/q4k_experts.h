@@ -158,8 +158,8 @@ cudaError_t experts_gemm_setup();
 
 // A 2-D byte map {K/256*144, N} of packed rows, box one super-block of `rows` rows
 // (a q4k_status; cached per host thread).
+int weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K, int rows);
 // Rows of bf16 [rows][K], box 64 k x box_rows rows with the 128-byte swizzle (the same).
 int rows_map(CUtensorMap* map, const void* X, int64_t rows, int64_t K, int box_rows);
-int weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K, int rows);
 
 }  // namespace q4k

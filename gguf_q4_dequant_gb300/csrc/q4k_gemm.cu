@@ -122,6 +122,34 @@ struct GemmCfg {
     static_assert((kGemmBM + 16) * BN * 4 <= kOffW, "split-K slots must fit in the A/B region");
 };
 
+// Eight weights of one nibble half (hh) from the qs word pair P = (w0, w1)
+// (bytes b0..b7, little-endian): w = d1*q - m1 in fp32, rounded to bf16.
+// A nibble masked in place at bit s of a word, OR'ed with 0x4B000000, is the
+// float 2^23 + 2^s*q exactly (s + 4 <= 23); pairs are handled with 64-bit
+// masks and the paired fp32 ops: bytes (i, i+4) of the pair form one fp32 pair.
+// Bytes 2 and 3 are first brought down by a 64-bit shift by 16. d1s0 / d1s1 are
+// (d1*2^-s, d1*2^-s) for s = 4*hh and 8 + 4*hh; nm1 is (-m1, -m1).
+__device__ __forceinline__ uint4 dequant8x(uint64_t P, int hh, uint64_t d1s0, uint64_t d1s1,
+                                           uint64_t nm1) {
+    const uint64_t magic = 0x4B0000004B000000ull;
+    const uint64_t neg = 0xCB000000CB000000ull;  // (-2^23, -2^23)
+    const uint64_t m0 = 0x0000000F0000000Full << (4 * hh);
+    const uint64_t m1 = 0x00000F0000000F00ull << (4 * hh);
+    const uint64_t S = P >> 16;
+    const uint64_t f0 = fma2(add2((P & m0) | magic, neg), d1s0, nm1);  // (w_b0, w_b4)
+    const uint64_t f1 = fma2(add2((P & m1) | magic, neg), d1s1, nm1);  // (w_b1, w_b5)
+    const uint64_t f2 = fma2(add2((S & m0) | magic, neg), d1s0, nm1);  // (w_b2, w_b6)
+    const uint64_t f3 = fma2(add2((S & m1) | magic, neg), d1s1, nm1);  // (w_b3, w_b7)
+    const float2 a = unpack2(f0), b = unpack2(f1), c = unpack2(f2), d = unpack2(f3);
+    uint32_t o[4];
+    __nv_bfloat162 t;
+    t = __floats2bfloat162_rn(a.x, b.x); o[0] = *reinterpret_cast<uint32_t*>(&t);
+    t = __floats2bfloat162_rn(c.x, d.x); o[1] = *reinterpret_cast<uint32_t*>(&t);
+    t = __floats2bfloat162_rn(a.y, b.y); o[2] = *reinterpret_cast<uint32_t*>(&t);
+    t = __floats2bfloat162_rn(c.y, d.y); o[3] = *reinterpret_cast<uint32_t*>(&t);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // 32 columns of a lane's accumulator row: the sum of the two MMA warps'
 // accumulators (columns c and BN + c), 16 columns of each per load.
 template <int BN>

@@ -15,7 +15,7 @@ constexpr int kRouteThreads = 1024;
 // Threads of a block that picks: a lane holds R logits and their keys.
 __host__ __device__ constexpr int pick_threads(int R) { return R <= 8 ? 1024 : 512; }
 // Steps of up to so many blocks have no scan of their own: each block adds up the
-// counts of the blocks before it (64 of them: two rounds of loads for 128 experts).
+// counts of the blocks before it (128 of them and 128 experts: two rounds of eight loads).
 constexpr int kRouteFew = 128;
 
 // ------------------------------------------------------------------- top k ---
@@ -75,7 +75,10 @@ __device__ __forceinline__ int pick_experts(const float* row, int E, int k, int 
                 if (logit_key(x[r]) != 0u) total += rel_exp(x[r], top);
         }
     } else {
-        if (mine >= 0) rel = 1.f / (1.f + expf(-mine_x));
+        // far below 0 the sigmoid is e^x: where they are divided by their sum, and would leave fp32's
+        // range first, they are taken relative to the largest
+        const bool far = weighting == Q4K_ROUTE_SIGMOID_TOP && top < -64.f && top >= -1000.f;
+        if (mine >= 0) rel = far ? rel_exp(mine_x, top) : 1.f / (1.f + expf(-mine_x));
         total = rel;
     }
     if (weighting != Q4K_ROUTE_SIGMOID) {

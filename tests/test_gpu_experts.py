@@ -215,6 +215,17 @@ def test_route_extreme_logits(q4k, T):
         check_route(q4k, logits, 3, weighting)
 
 
+@pytest.mark.parametrize("T", [4, 900])
+@pytest.mark.parametrize("top", [-64.5, -87.0, -104.0, -300.0, -999.0])
+def test_route_sigmoids_far_below(q4k, T, top):
+    # divided by their sum they stay what they are, e^x / sum e^x, wherever fp32 ends (2^-92 off at most: 1 + e^x)
+    logits = top - torch.rand(T, 9, generator=gen(T)) * 6
+    logits[:, 3] = top
+    _, w, _, _, _, d = route_ref(logits, 4, 1, 1.5)
+    got = route(q4k, logits, 4, 3, 1.5)[1].double()
+    assert bool(((got - w).abs() <= (2.0 ** -18 + 2.0 ** -23 * d.abs()) * w).all())
+
+
 @pytest.mark.parametrize("T,E,k", [(5000, 2, 2), (3000, 7, 1)])
 def test_route_one_expert_takes_all(q4k, T, E, k):
     logits = torch.zeros(T, E)
