@@ -306,7 +306,7 @@ class Experts:
         a, m, r = parts(self.w[e].reshape(self.N, -1), self.N, self.K)
         x = x.double()
         y = x @ (a - m).T
-        tol = 2.0 ** -8 * (x.abs() @ ((a - m).abs() + r).T) + 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ (a + m).T)
+        tol = 2.0 ** -8 * (x.abs() @ ((a - m).abs() + r).T) + 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ (a.abs() + m.abs()).T)
         return y, tol
 
 
@@ -403,6 +403,91 @@ def test_experts_starts_out_of_range(q4k):
     same = torch.full((P, N), 5.0, dtype=torch.bfloat16, device=DEV)
     q4k.q4k_experts_matmul(w.dev, N, K, x, ints([0, 4, 4, 9, 20]), same)
     assert torch.equal(y, same)
+
+
+def test_experts_starts_out_of_range_many_rows(q4k):
+    """The same for the kernel of many rows."""
+    N, K, P = 300, 256, 2900
+    w = Experts(4, 4, N, K)
+    x = torch.randn(P, K, generator=gen(2)).to(torch.bfloat16).to(DEV)
+    for gated in (False, True):
+        def product(starts, y):
+            if gated:
+                q4k.q4k_experts_gated(w.dev, w.dev, N, K, x * 0.02, ints(starts), y)
+            else:
+                q4k.q4k_experts_matmul(w.dev, N, K, x, ints(starts), y)
+            return y
+        new = lambda: torch.full((P + 8, N), 5.0, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+        # X's rows are those of Y, 8 more would be read if pairs were taken from there
+        for starts in ([1 << 30] * 5, [-(1 << 31)] * 5, [P, 10, 5, 2, 0], [0, 2000, 3, 1 << 30, 12]):
+            y = product(starts, new())
+            assert bool((y[P:] == 5).all()) and bool(torch.isfinite(y).all())
+        assert torch.equal(product([-5, 900, 2, 1900, 1 << 30], new()), product([0, 900, 900, 1900, P], new()))
+
+
+@pytest.mark.parametrize("counts", [[3, 9], [200, 90], [2500, 2000]])
+def test_experts_odd_heads(q4k, counts):
+    """Super-blocks whose d or dmin is 0, negative, or the smallest number: the bounds hold as they are."""
+    E, N, K = 2, 40, 512
+    w = Experts(31, E, N, K)
+    head = torch.tensor([[0.0, 1.0], [1.0, 0.0], [0.0, 0.0], [-1.0, 2.0], [2.0, -1.0], [-1.0, -4.0], [2.0 ** -24, 2.0 ** -24],
+                         [2.0 ** -24, 1.0], [1.0, 2.0 ** -24], [60.0, 60.0]]).to(torch.float16)
+    blocks = w.w.view(E, N, K // 256, 144)
+    at = torch.arange(E * N * (K // 256)).view(E, N, K // 256) % len(head)
+    blocks[..., 0:4] = head[at].view(torch.uint8)
+    w.dev = w.w.to(DEV)
+    P = sum(counts)
+    x = torch.randn(P, K, generator=gen(5)).to(torch.bfloat16)
+    y = torch.empty(P, N, dtype=torch.bfloat16, device=DEV)
+    q4k.q4k_experts_matmul(w.dev, N, K, x.to(DEV), ints([0, counts[0], P]), y)
+    for e, rows in enumerate((slice(0, counts[0]), slice(counts[0], P))):
+        want, tol = w.product(e, x[rows])
+        assert bool(((y[rows].cpu().double() - want).abs() <= tol + 2.0 ** -8 * want.abs()).all())
+
+
+def test_offsets_past_31_bits(q4k):
+    """The last rows of arrays of more than 2^31 elements."""
+    g, T, C = torch.Generator(device=DEV).manual_seed(1), 65700, 32768
+    tail = slice(T - 3, T)
+    x = torch.empty(T, C, dtype=torch.bfloat16, device=DEV)
+    x[tail] = torch.randn(3, C, generator=g, device=DEV).to(torch.bfloat16)
+    # rows that change places, and back, with a weight
+    order = torch.arange(T, dtype=torch.int32, device=DEV)
+    order[T - 1], order[0] = 0, T - 1
+    x[0] = 2.0
+    rows = torch.empty_like(x)
+    q4k.q4k_experts_gather(x, order, 1, rows)
+    assert torch.equal(rows[0], x[T - 1]) and torch.equal(rows[T - 2], x[T - 2]) and bool((rows[T - 1] == 2).all())
+    out = torch.empty(T, C, device=DEV)
+    q4k.q4k_experts_combine(rows, order.view(T, 1), torch.full((T, 1), 0.5, device=DEV), out)
+    assert torch.equal(out[tail], 0.5 * x[tail].float()) and bool((out[0] == 1).all())
+    del rows
+    codes, scales = torch.empty(T, C, dtype=torch.uint8, device=DEV), torch.empty(T, C // 32, dtype=torch.uint8, device=DEV)
+    w = torch.ones(C, device=DEV)
+    q4k.q4k_add_norm(x, None, w, 1e-5, out=out, codes=codes, scales=scales)
+    few = [torch.empty_like(t[:3]) for t in (out, codes, scales)]
+    q4k.q4k_add_norm(x[tail].clone(), None, w, 1e-5, out=few[0], codes=few[1], scales=few[2])
+    for t, f in zip((out, codes, scales), few):
+        assert torch.equal(t[tail], f)
+
+
+@pytest.mark.parametrize("E,N,K,P", [(2, 32768, 256, 65700), (1024, 8, 1 << 18, 8200)])
+def test_products_past_31_bits(q4k, E, N, K, P):
+    """Rows of Y (many rows an expert) and of X (few) past 2^31 elements."""
+    w = synth.weight_rows(77, 8, K)
+    dev = w.to(DEV).repeat(E * N // 8, 1)
+    x = torch.zeros(P, K, dtype=torch.bfloat16, device=DEV)
+    x[P - 3:] = torch.randn(3, K, generator=gen(6)).to(torch.bfloat16).to(DEV)
+    y = torch.full((P, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    starts = torch.linspace(0, P, E + 1).round().int().to(DEV)
+    q4k.q4k_experts_matmul(dev, N, K, x, starts, y)
+    assert bool((y[:P - 3] == 0).all())
+    a, m, r = parts(w.reshape(8, -1), 8, K)
+    xs = x[P - 3:].cpu().double()
+    want = xs @ (a - m).T
+    tol = 2.0 ** -8 * (xs.abs() @ ((a - m).abs() + r).T + want.abs()) + 2.0 ** -23 * (K / 16 + 64) * (xs.abs() @ (a + m).T)
+    got = y[P - 3:].cpu().double().view(3, N // 8, 8)
+    assert bool(((got - want.unsqueeze(1)).abs() <= tol.unsqueeze(1)).all())
 
 
 def test_experts_many_experts(q4k):
