@@ -22,7 +22,9 @@
 // warps of a unit add their sums in shared memory, in warp order; with wk = 1
 // warps never wait for one another. A unit is (up to 8 rows of x of an expert, 32 output
 // columns); units are dealt out to resident warps, the next unit's words on their
-// way during this one's end.
+// way during this one's end. 64 tokens to 8 of 128 experts, gated 768 x 2048: 59.5 us, 3.6 TB/s
+// of words (without the products 38: what remains is spreading bytes and loading x); 5
+// tokens to 2 of 8 experts, 4096 x 12288: 50 us, 3.4 TB/s; one token to 8 of 128, gated: 9.8 us.
 #include <cuda_bf16.h>
 
 #include "q4k_device.cuh"

@@ -29,6 +29,10 @@
 //   warps 12..27 dequantisers, four groups of 128 threads: two a tile, each with every
 //                other 64 k, a thread with a weight row of them and 32 columns of TMEM
 // All waits are bounded (see mbar_wait).
+//
+// 4096 tokens to 8 of 128 experts, gated 768 x 2048: 152 us, 1.35 PFLOP/s; 2048 tokens to 4 of 16,
+// 4096 x 2048: 100 us, 1.37 PFLOP/s (70 % of the dense peak; tensor core busy 67 and 71 %,
+// dequantisers' issue slots 67 %). Over many calls the power cap takes a tenth.
 #include <cuda_bf16.h>
 
 #include <type_traits>
