@@ -11,9 +11,12 @@
 // of the subnormal numbers and of the first binade count on evenly), so a byte
 // spread to 16 bits and masked is the operand, the high nibble 16 times its
 // code. x is multiplied by 2^64 (exact), which keeps the products in fp32's
-// normal range, and the scales by 2^69. The mins are the same trick: m_j as
-// the A operand for all 32 k of its sub-block, one accumulator for all of them.
-// Rows of x with values of 2^64 and more are out of range.
+// normal range, and the scales by 2^69. The sums of x come from products too, with
+// x as the A operand (its first and second 16 k in the upper and lower eight rows) and a
+// column of ones for each sub-block, so that they end where one more product with
+// the m_j wants its B operand: 42 products a step (m_j against all of x took 64, and 7 us
+// of the 62 for 64 tokens to 8 of 128 experts). Rows of x with values of 2^64 and more are
+// out of range.
 //
 // What bounds it: few rows leave the memory's rate for the packed words (each
 // read once) and the issue slots. So the work is laid out for the words: a warp
@@ -83,7 +86,8 @@ __device__ __forceinline__ void ex_load(const uint16_t* x, int off, uint4 (&v)[2
 // One super-block of 32 weight rows (a stage, at wrow for this lane) with eight rows
 // of x: acc += this step's products. x: this lane's row of x at this super-block
 // and the lane's 8 k of 32, or NULL; xv[0] holds its first 64 k.
-__device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, int t4, uint4 (&xv)[2][2], float (&acc)[2][4]) {
+__device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, int g, int t4, uint4 (&xv)[2][2],
+                                        float (&acc)[2][4]) {
     uint32_t hx[2][2];
     ScaleBytes sb[2][2];
     float d[2][2];
@@ -96,7 +100,7 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
             hx[m][r] = head.x;
             d[m][r] = half_lo(head.x) * exp2i(69);
         }
-    float low[2][4];  // sum over j of m_j (sum of x)
+    float sums[4];  // of x (2^59 x) over sub-blocks 2 t4 and 2 t4 + 1: their first, then their second 16 k
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         if (c < 3) ex_load(x, 64 * (c + 1), xv[(c + 1) & 1]);
@@ -134,7 +138,6 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
                 }
         }
         float s[2][2][2], f[2][2][4];
-        uint32_t mn[2][2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -143,47 +146,55 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t scw = j < 4 ? sb[m][r].sc_lo : sb[m][r].sc_hi;
-                    const uint32_t mw = j < 4 ? sb[m][r].m_lo : sb[m][r].m_hi;
                     // (2^23 + sc) d - 2^23 d: both exact, so the FMA rounds sc d once
                     const float dh = h ? d[m][r] * 0.0625f : d[m][r];
                     s[m][h][r] = fmaf(__uint_as_float(__byte_perm(scw, 0x4B000000u, 0x7440u | (j & 3))), dh, -8388608.f * dh);
-                    mn[m][h][r] = mn[m][h][r + 2] = __byte_perm(mw, 0, (j & 3) * 0x0101 | 0x4040);
                 }
             }
-        // a sum's next product comes four products later: the tensor core takes them one behind the other
+        // a sum's next product comes some products later: the tensor core takes them one behind the other
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) mma_bf16_zero(f[m][h], a[m][h][0], xs[h][0], xs[h][1]);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            if (c == 0) mma_bf16_zero(low[m], mn[m][0], xs[0][0], xs[0][1]);
-            else mma_bf16(low[m], mn[m][0], xs[0][0], xs[0][1]);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t rows[4] = {xs[h][0], xs[h][2], xs[h][1], xs[h][3]};
+            const uint32_t one = g == 2 * c + h ? 0x3D003D00u : 0u;  // 2^-5 in column j
+            if (c == 0 && h == 0) mma_bf16_zero(sums, rows, one, one);
+            else mma_bf16(sums, rows, one, one);
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) mma_bf16(f[m][h], a[m][h][1], xs[h][2], xs[h][3]);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) mma_bf16(low[m], mn[m][0], xs[0][2], xs[0][3]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) mma_bf16(low[m], mn[m][1], xs[1][0], xs[1][1]);
-#pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(f[m][h][i], s[m][h][i >> 1], acc[m][i]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) mma_bf16(low[m], mn[m][1], xs[1][2], xs[1][3]);
     }
+    // the mins: one product over the eight sub-blocks, each sum as two bf16 (good to 2^-17), m_j as m_j 2^-33
+    const float even = sums[0] + sums[2], odd = sums[1] + sums[3];
+    const __nv_bfloat162 top = __floats2bfloat162_rn(even, odd);
+    const __nv_bfloat162 rest = __floats2bfloat162_rn(even - __low2float(top), odd - __high2float(top));
+    const __nv_bfloat162 up = __floats2bfloat162_rn(exp2i(100), exp2i(100));
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-        const float lo0 = half_hi(hx[m][0]) * exp2i(69), lo1 = half_hi(hx[m][1]) * exp2i(69);
-        acc[m][0] = fmaf(-lo0, low[m][0], acc[m][0]);
-        acc[m][1] = fmaf(-lo0, low[m][1], acc[m][1]);
-        acc[m][2] = fmaf(-lo1, low[m][2], acc[m][2]);
-        acc[m][3] = fmaf(-lo1, low[m][3], acc[m][3]);
+        uint32_t mn[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t pair = __byte_perm(t4 < 2 ? sb[m][r].m_lo : sb[m][r].m_hi, 0, t4 & 1 ? 0x4342 : 0x4140);
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&pair), up);
+            mn[r] = mn[r + 2] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        float low[4];  // 2^26 sum over j of m_j (sum of x)
+        mma_bf16_zero(low, mn, *reinterpret_cast<const uint32_t*>(&top), *reinterpret_cast<const uint32_t*>(&rest));
+        const float lo0 = half_hi(hx[m][0]) * exp2i(-26), lo1 = half_hi(hx[m][1]) * exp2i(-26);
+        acc[m][0] = fmaf(-lo0, low[0], acc[m][0]);
+        acc[m][1] = fmaf(-lo0, low[1], acc[m][1]);
+        acc[m][2] = fmaf(-lo1, low[2], acc[m][2]);
+        acc[m][3] = fmaf(-lo1, low[3], acc[m][3]);
     }
 }
 
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(32 * kExWarps, kExBlocks)
                 for (uint32_t i = step; i < asked; ++i)
                     mbar_wait(bar + 8 * (i % kExStages), (i / kExStages) & 1, err, kDrainLimitNs);
             }
-            ex_step(ring_ptr + stage * kExStage + ex_row(g) * kBlockBytes, x, t4, xv, acc);
+            ex_step(ring_ptr + stage * kExStage + ex_row(g) * kBlockBytes, x, g, t4, xv, acc);
             // every word of the stage has gone through a product that has been issued
             __syncwarp();
             ask(stage);
