@@ -396,11 +396,12 @@ cudaError_t experts_setup(DeviceInfo&) {
 // The two kernels' times in us, from the sizes that the host knows: experts with
 // rows are taken to be all of them or as many as there are rows, with equal
 // shares. The one for few rows goes over the words again for every eight rows of
-// an expert, 1.05 ns a step of 32 weight rows and 256 k on all of the GPU; the
-// tcgen05 kernel's blocks take 2 us for 256 k of a unit, whatever rows it has, and 1.6
+// an expert, 0.92 ns a step of 32 weight rows and 256 k on all of the GPU; the
+// tcgen05 kernel's blocks take 1.55 us for 256 k of a unit, whatever rows it has, and 1.6
 // for its end, and have nothing to share out when there are few units. 128 experts, gated
-// 768 x 2048: 8 rows each 82 us for 109 (here 82, 110), 12 rows 103 for 109 (108, 110), 16 rows
-// 129 (here) for 109; down 2048 x 768: 8 rows 46 us for 61 (44, 57), 12 rows 60 for 62 (57, 57).
+// 768 x 2048: 8 rows each 70 us for 84 (here 73, 83), 12 rows 97 for 84 (95, 83); down 2048 x
+// 768: 8 rows 41 us for 46 (39, 49), 12 rows 53 for 47 (50, 49); 8 experts of 4096 x 12288: 8 rows
+// 68 for 82 (73, 80), 12 rows 90 for 82 (95, 80); 2 experts of 144 x 7168, 300 rows: 17 for 49 (15, 49).
 // (Tiles of 16 and 32 rows in the first kernel were slower than its 8 or the second at every size.)
 static bool many_rows(const ExpertArgs& a, const DeviceInfo& dev) {
     const double pairs = a.rows.pairs, busy = pairs < a.rows.experts ? pairs : a.rows.experts, mats = a.W2 != nullptr ? 2 : 1;
@@ -408,7 +409,7 @@ static bool many_rows(const ExpertArgs& a, const DeviceInfo& dev) {
     const double slabs = static_cast<double>((a.N + kExRows - 1) / kExRows);
     double tiles = pairs / kExTile + 0.5 * busy;
     tiles = tiles > busy ? tiles : busy;
-    const double few = 5.0 + 1.05e-3 * tiles * slabs * KB * mats;
+    const double few = 5.0 + 0.92e-3 * tiles * slabs * KB * mats;
     return experts_gemm_us(a, dev) < few;
 }
 

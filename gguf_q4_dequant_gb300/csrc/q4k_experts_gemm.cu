@@ -424,7 +424,7 @@ double experts_gemm_us(const ExpertArgs& a, const DeviceInfo& dev) {
     const int64_t cols = a.W2 != nullptr ? kEgBM : 2 * kEgBM, each = (pairs + busy - 1) / busy;
     const double units = static_cast<double>(busy) * ((each + kEgBN - 1) / kEgBN) * ((a.N + cols - 1) / cols);
     const double rounds = units <= dev.num_sms ? 1.0 : units / dev.num_sms + 0.5;
-    return 4.0 + rounds * (1.6 + 2.0 * static_cast<double>(a.K / kBlockWeights));
+    return 4.0 + rounds * (1.6 + 1.55 * static_cast<double>(a.K / kBlockWeights));
 }
 
 cudaError_t launch_experts_gemm(const ExpertArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
