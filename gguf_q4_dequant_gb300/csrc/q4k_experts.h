@@ -118,7 +118,7 @@ struct RouteArgs {
     int32_t* ws;
 };
 int64_t route_scratch_bytes(int64_t T, int E);
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int pdl);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl);
 
 struct GatherArgs {
     const void* x;

@@ -87,7 +87,7 @@ int q4k_route(const float* logits, int64_t T, int64_t E, int k, int weighting, f
     if (rc != Q4K_OK) return rc;
     const RouteArgs a{logits,  static_cast<int>(T), static_cast<int>(E), k, weighting, scale, ids, weights, order, slots,
                       starts, static_cast<int32_t*>(ws)};
-    return status(launch_route(a, static_cast<cudaStream_t>(stream), pdl_mode()));
+    return status(launch_route(a, static_cast<cudaStream_t>(stream), *dev, pdl_mode()));
 }
 
 int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* order, int64_t T, int k, int64_t C,

@@ -97,19 +97,19 @@ __device__ __forceinline__ int pick_experts(const float* row, int E, int k, int 
     return mine;
 }
 
-// The picks of tokens t0 .. t0 + n - 1, by the warps of the block: to ids and
-// weights, and to shared memory.
-template <int R>
-__device__ __forceinline__ void pick_block(const RouteArgs& a, int t0, int n, int16_t* chosen) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    for (int i = warp; i < n; i += warps) {
+// The picks of every `step`-th of tokens t0 .. t0 + n - 1 from the i0-th on, a warp
+// each: to ids and weights, and to put(pair of the block, expert).
+template <int R, typename Put>
+__device__ __forceinline__ void pick_tokens(const RouteArgs& a, int t0, int n, int i0, int step, Put put) {
+    const int lane = threadIdx.x & 31;
+    for (int i = i0; i < n; i += step) {
         float w;
         const int64_t t = t0 + i;
         const int e = pick_experts<R>(a.logits + t * a.E, a.E, a.k, a.weighting, a.scale, lane, &w);
         if (lane < a.k) {
             a.ids[t * a.k + lane] = e;
             a.weights[t * a.k + lane] = w;
-            chosen[i * a.k + lane] = static_cast<int16_t>(e);
+            put(i * a.k + lane, e);
         }
     }
 }
@@ -174,20 +174,35 @@ __device__ __forceinline__ void scan_experts(const int* cnt, int E, int* base) {
     __syncthreads();
 }
 
-// One block does everything: a step of a few tokens is one launch.
+// A step of a few tokens is one launch: a cluster's blocks share the picks, which
+// fill a block's integer pipe (48 tokens: 5.9 us, 8.6 by one block), and hand them
+// to the first one's shared memory, which does the rest.
 template <int R>
 __global__ void __launch_bounds__(pick_threads(R)) q4k_route_one_kernel(const RouteArgs a) {
     extern __shared__ int route_smem[];
+    const int blocks = gridDim.x;  // of the one cluster
+    if (blocks > 1) cluster_arrive_relaxed();
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
-    const int warps = blockDim.x >> 5, pairs = a.T * a.k;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, pairs = a.T * a.k;
     int* hist = route_smem;             // [warps][E]
     int* cnt = hist + warps * a.E;      // [E]
     int* base = cnt + a.E;              // [E + 1]
     int16_t* chosen = reinterpret_cast<int16_t*>(base + a.E + 1);
     const int run = ((pairs + warps - 1) / warps + 31) / 32 * 32, used = (pairs + run - 1) / run;
+    if (blocks > 1) {
+        const uint32_t first = map_shared_rank(smem_u32(chosen), 0);
+        cluster_wait();  // every block of the cluster has begun
+        pick_tokens<R>(a, 0, a.T, blockIdx.x + blocks * warp, blocks * warps, [&](int i, int e) {
+            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(first + 2 * i), "h"(static_cast<int16_t>(e)) : "memory");
+        });
+        __syncwarp();
+        cluster_sync_all();
+        if (blockIdx.x != 0) return;
+    } else {
+        pick_tokens<R>(a, 0, a.T, warp, warps, [&](int i, int e) { chosen[i] = static_cast<int16_t>(e); });
+    }
     for (int i = threadIdx.x; i < used * a.E; i += blockDim.x) hist[i] = 0;
-    pick_block<R>(a, 0, a.T, chosen);
     __syncthreads();
     count_pairs(chosen, pairs, a.E, hist, run);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
@@ -206,22 +221,37 @@ __global__ void __launch_bounds__(pick_threads(R)) q4k_route_one_kernel(const Ro
     place_pairs(a, chosen, 0, pairs, a.E, hist, base, run);
 }
 
-// Many tokens: blocks of kRouteTokens pick and count (counts: [blocks][E]), ...
+// Many tokens: groups of kRouteTokens are picked and counted (counts: [groups][E]), by a
+// block each or, while there are SMs for it, by a cluster of `spread`, counted in the first one's
+// shared memory, ...
 template <int R>
-__global__ void __launch_bounds__(pick_threads(R)) q4k_route_pick_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(pick_threads(R)) q4k_route_pick_kernel(const RouteArgs a, int spread) {
     extern __shared__ int route_smem[];
+    int* hist = route_smem;  // [E]
+    const int group = blockIdx.x / spread, rank = blockIdx.x - group * spread;
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+    if (spread > 1) cluster_sync_all();
+    else __syncthreads();
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
-    int* hist = route_smem;  // [E]
-    int16_t* chosen = reinterpret_cast<int16_t*>(hist + a.E);
-    const int t0 = blockIdx.x * kRouteTokens, n = min(kRouteTokens, a.T - t0);
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
-    pick_block<R>(a, t0, n, chosen);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * a.k; i += blockDim.x)
-        if (chosen[i] >= 0) atomicAdd(&hist[chosen[i]], 1);  // counts: the order does not matter
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.ws[static_cast<int64_t>(blockIdx.x) * a.E + e] = hist[e];
+    const int t0 = group * kRouteTokens, n = min(kRouteTokens, a.T - t0);
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    // (counts: their order does not matter)
+    if (spread > 1) {
+        const uint32_t first = map_shared_rank(smem_u32(hist), 0);
+        pick_tokens<R>(a, t0, n, rank + spread * warp, spread * warps, [&](int, int e) {
+            if (e >= 0) asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(first + 4 * e), "r"(1) : "memory");
+        });
+        __syncwarp();
+        cluster_sync_all();
+        if (rank != 0) return;
+    } else {
+        pick_tokens<R>(a, t0, n, warp, warps, [&](int, int e) {
+            if (e >= 0) atomicAdd(&hist[e], 1);
+        });
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.ws[static_cast<int64_t>(group) * a.E + e] = hist[e];
 }
 
 // ... the counts become, for each expert, the sums over the blocks before (in
@@ -435,24 +465,31 @@ __global__ void __launch_bounds__(256) q4k_combine_kernel(const CombineArgs a) {
 
 namespace {
 
-// Steps of up to this many pairs are sorted by one block, with as many warps as
-// their counts have room for in the 48 KB that need no attribute.
-constexpr int kOnePairs = 2048;
+// Steps of up to so many tokens and pairs take one launch (128 experts, 8 picks: 128 tokens 8.3 us
+// for 8.4, 192 tokens 9.6 for 8.5; 16 experts, one pick: 512 tokens 6.2 for 6.8, 2048 13.3 for 7.0).
+constexpr int kOneTokens = 512, kOnePairs = 1024;
+// Fewer tokens stay with one block, whose warps have room (8 tokens: 4.3 us either way), unless a
+// token alone keeps it busy (8 tokens to 32 of 1024 experts: 28 us, 16 shared out).
+constexpr int kOneSpread = 8, kOneSpreadExperts = 256;
 
 template <int R>
-cudaError_t route_r(const RouteArgs& a, cudaStream_t stream, int pdl) {
+cudaError_t route_r(const RouteArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
     const int64_t pairs = static_cast<int64_t>(a.T) * a.k;
-    if (pairs <= kOnePairs) {
-        // a warp per token, as many as the counts of a warp leave room for
+    if (a.T <= kOneTokens && pairs <= kOnePairs) {
+        // a warp per token, as many as the counts of a warp leave room for in the 48 KB that need no attribute
         const int most = (40960 - 4 * (2 * a.E + 1)) / (4 * a.E);
         int warps = a.T < pick_threads(R) / 32 ? a.T : pick_threads(R) / 32;
         warps = warps < most ? warps : most;
         const size_t smem = 4 * (static_cast<size_t>(warps) * a.E + 2 * a.E + 1) + 2 * pairs;
-        return launch_serve(q4k_route_one_kernel<R>, dim3(1), dim3(32 * warps), smem, stream, pdl, 1, a);
+        const int spread = a.T > (a.E <= kOneSpreadExperts ? kOneSpread : 1) ? 8 : 1;
+        return launch_serve(q4k_route_one_kernel<R>, dim3(spread), dim3(32 * warps), smem, stream, pdl, spread, a);
     }
     const int blocks = (a.T + kRouteTokens - 1) / kRouteTokens;
     const size_t chosen = 2 * static_cast<size_t>(kRouteTokens) * a.k;
-    cudaError_t e = launch_serve(q4k_route_pick_kernel<R>, dim3(blocks), dim3(pick_threads(R)), 4 * a.E + chosen, stream, pdl, 1, a);
+    int spread = 1;  // (1003 tokens, 61 experts: 8.1 us, 9.4 with 1)
+    while (spread < 8 && 2 * spread * blocks <= dev.num_sms) spread *= 2;
+    const int threads = pick_threads(R) < 32 * kRouteTokens / spread ? pick_threads(R) : 32 * kRouteTokens / spread;
+    cudaError_t e = launch_serve(q4k_route_pick_kernel<R>, dim3(blocks * spread), dim3(threads), 4 * a.E, stream, pdl, spread, a, spread);
     if (e != cudaSuccess) return e;
     // counts for as many warps as have 32 pairs each, within 48 KB
     int most = (44 * 1024 - static_cast<int>(chosen) - 4 * (3 * a.E + 1)) / (4 * a.E);
@@ -471,13 +508,13 @@ cudaError_t route_r(const RouteArgs& a, cudaStream_t stream, int pdl) {
 
 int64_t route_scratch_bytes(int64_t T, int E) { return 4 * E * ((T + kRouteTokens - 1) / kRouteTokens + 1); }
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int pdl) {
-    if (a.E <= 32) return route_r<1>(a, stream, pdl);
-    if (a.E <= 64) return route_r<2>(a, stream, pdl);
-    if (a.E <= 128) return route_r<4>(a, stream, pdl);
-    if (a.E <= 256) return route_r<8>(a, stream, pdl);
-    if (a.E <= 512) return route_r<16>(a, stream, pdl);
-    return route_r<32>(a, stream, pdl);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
+    if (a.E <= 32) return route_r<1>(a, stream, dev, pdl);
+    if (a.E <= 64) return route_r<2>(a, stream, dev, pdl);
+    if (a.E <= 128) return route_r<4>(a, stream, dev, pdl);
+    if (a.E <= 256) return route_r<8>(a, stream, dev, pdl);
+    if (a.E <= 512) return route_r<16>(a, stream, dev, pdl);
+    return route_r<32>(a, stream, dev, pdl);
 }
 
 cudaError_t launch_gather(const GatherArgs& args, cudaStream_t stream, const DeviceInfo& dev, int pdl) {
