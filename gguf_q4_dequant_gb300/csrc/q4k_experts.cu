@@ -80,12 +80,12 @@ __device__ __forceinline__ int ex_row(int g) { return ((g & 3) << 1) | (g >> 2);
 __device__ __forceinline__ void ex_load(const uint16_t* x, int off, uint4 (&v)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        v[h] = x != nullptr ? *reinterpret_cast<const uint4*>(x + off + 32 * h) : make_uint4(0, 0, 0, 0);
+        v[h] = *reinterpret_cast<const uint4*>(x + off + 32 * h);
 }
 
 // One super-block of 32 weight rows (a stage, at wrow for this lane) with eight rows
 // of x: acc += this step's products. x: this lane's row of x at this super-block
-// and the lane's 8 k of 32, or NULL; xv[0] holds its first 64 k.
+// and the lane's 8 k of 32; xv[0] holds its first 64 k.
 __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, int g, int t4, uint4 (&xv)[2][2],
                                         float (&acc)[2][4]) {
     uint32_t hx[2][2];
@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(32 * kExWarps, kExBlocks)
         const int e = expert_at(tiles, rows.experts, t, lane), n0 = s * kExRows;
         const int p0 = starts[e] + (t - tiles[e]) * kExTile, p1 = min(p0 + kExTile, starts[e + 1]);
         float acc[2][4] = {};
-        const uint16_t* x = p0 + g < p1 ? X + static_cast<int64_t>(p0 + g) * K + k0 * kBlockWeights + 8 * t4 : nullptr;
+        // (lanes without a row have the last one again: its products go nowhere)
+        const uint16_t* x = X + static_cast<int64_t>(min(p0 + g, p1 - 1)) * K + k0 * kBlockWeights + 8 * t4;
         for (int kb = k0; kb < KB; kb += nk, ++step) {
             const int stage = step % kExStages;
             uint4 xv[2][2];
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(32 * kExWarps, kExBlocks)
             // every word of the stage has gone through a product that has been issued
             __syncwarp();
             ask(stage);
-            if (x != nullptr) x += nk * kBlockWeights;
+            x += nk * kBlockWeights;
         }
         if (!kGated && wk == 1) {
 #pragma unroll
