@@ -25,9 +25,9 @@
 // warps of a unit add their sums in shared memory, in warp order; with wk = 1
 // warps never wait for one another. A unit is (up to 8 rows of x of an expert, 32 output
 // columns); units are dealt out to resident warps, the next unit's words on their
-// way during this one's end. 64 tokens to 8 of 128 experts, gated 768 x 2048: 59.5 us, 3.6 TB/s
-// of words (without the products 38: what remains is spreading bytes and loading x); 5
-// tokens to 2 of 8 experts, 4096 x 12288: 50 us, 3.4 TB/s; one token to 8 of 128, gated: 9.8 us.
+// way during this one's end. 64 tokens to 8 of 128 experts, gated 768 x 2048: 51 us, 4.2 TB/s
+// of words (38 without the products, 48 with them alone); 5 tokens to 2 of 8 experts, 4096 x
+// 12288: 43 us, 4.0 TB/s; one token to 8 of 128, gated: 8.9 us.
 #include <cuda_bf16.h>
 
 #include "q4k_device.cuh"
@@ -37,7 +37,7 @@
 namespace q4k {
 
 // Warps of a block, blocks of an SM: 12 warps with 168 registers each (128 experts
-// with four rows each, gated: 62 us; 16 warps with 128, 68; 8 with 255, 77).
+// with four rows each, gated: 55 us; 16 warps with 128, 62).
 constexpr int kExWarps = 4, kExBlocks = 3;
 constexpr int kExRows = 32;                            // weight rows of a step, output columns of a unit
 constexpr int kExStage = kExRows * kBlockBytes;        // 4608
@@ -354,10 +354,10 @@ cudaError_t launch_few(const ExpertArgs& a, cudaStream_t stream, const DeviceInf
     const int KB = static_cast<int>(a.K / kBlockWeights);
     // wk, the warps that share K: few units are split further, so that every warp
     // of the GPU has some of the words on their way (8 experts of 128 with one row
-    // each, gated 768 x 2048: 12.2 us with 4, 14.6 with 2); many are not, as the warps of
-    // a unit wait for one another (four rows for each of 128 experts of 2048 x 768: 37 us
-    // with 1, 43 with 2). In between it counts how full the last round is (5 tokens to
-    // 2 of 8 experts of 4096 x 12288: 72, 51, 46 us with 1, 2, 4).
+    // each, gated 768 x 2048: 10.7 us with 4, 12.6 with 2); many are not, as the warps of
+    // a unit wait for one another (four rows for each of 128 experts of 2048 x 768: 32 us
+    // with 1, 38 with 2). In between it counts how full the last round is (5 tokens to
+    // 2 of 8 experts of 4096 x 12288: 61, 45, 45 us with 1, 2, 4).
     const int64_t tiles = busy > a.rows.pairs / kExTile ? busy : a.rows.pairs / kExTile;
     int wk = kGated ? 2 : 1, per = 1;
     double best = 1e300;

@@ -31,7 +31,7 @@
 // All waits are bounded (see mbar_wait).
 //
 // 4096 tokens to 8 of 128 experts, gated 768 x 2048: 152 us, 1.35 PFLOP/s; 2048 tokens to 4 of 16,
-// 4096 x 2048: 100 us, 1.37 PFLOP/s (70 % of the dense peak; tensor core busy 67 and 71 %,
+// 4096 x 2048: 98 us, 1.40 PFLOP/s (70 and 73 % of cuBLAS's rate; tensor core busy 67 and 71 %,
 // dequantisers' issue slots 67 %). Over many calls the power cap takes a tenth.
 #include <cuda_bf16.h>
 
