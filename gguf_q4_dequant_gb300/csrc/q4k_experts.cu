@@ -174,7 +174,7 @@ __device__ __forceinline__ void ex_step(const uint8_t* wrow, const uint16_t* x, 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(f[m][h][i], s[m][h][i >> 1], acc[m][i]);
     }
-    // the mins: one product over the eight sub-blocks, each sum as two bf16 (good to 2^-17), m_j as m_j 2^-33
+    // the mins: one product over the eight sub-blocks, each sum as two bf16 (off by 2^-16 at most), m_j as m_j 2^-33
     const float even = sums[0] + sums[2], odd = sums[1] + sums[3];
     const __nv_bfloat162 top = __floats2bfloat162_rn(even, odd);
     const __nv_bfloat162 rest = __floats2bfloat162_rn(even - __low2float(top), odd - __high2float(top));

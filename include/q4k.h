@@ -459,8 +459,9 @@ int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* orde
  * fp32 and rounded once to bf16. q4k_experts_gated takes two of them and gives
  * Y[p] = g / (1 + exp(-g)) * u with g = X[p] gate_e^T and u = X[p] up_e^T in fp32.
  * By the sizes (never by what the arrays hold) one of two kernels runs: for few
- * rows the weights enter exactly (the sums of x beside the mins as two bf16, off by 2^-17); for many the tcgen05 tensor cores take them as
- * bf16, off by 2^-8 (|w| + |r|) at most, r the weight of the code nearest to 0 (as
+ * rows the weights enter exactly (the sums of x beside the mins as two bf16 each,
+ * off by 2^-16); for many the tcgen05 tensor cores take them as bf16, off by
+ * 2^-8 (|w| + |r|) at most, r the weight of the code nearest to 0 (as
  * q4k_matmul_bf16's, by 2^-8 |w|, for 17 rows and more).
  * Rows before starts[0] and from starts[E] on are left as they are; starts is
  * taken as ascending and inside [0, pairs] (values are clamped to that).

@@ -13,8 +13,9 @@ Tolerances follow from the number formats, half a step for every rounding (bf16
 * products: the output's rounding 2^-8 |y|; where the rows are many the weights as
   bf16, w = (q - c) d + r with c the code nearest to w = 0, of two roundings: r = c d - m's,
   and the sum's, 2^-8 sum (|w| + |r|) |x| (d is kept as two bf16; c may fall to either
-  side of a tie, 2^-20 |d|); fp32 sums over K / 16 products of 16 and what
-  is behind them, 2^-23 (K/16 + 64) sum (|d sc q x| + |dmin m x|).
+  side of a tie, 2^-20 |d|); where they are few the sums of x beside the mins as two bf16,
+  2^-16 sum |dmin m x|; fp32 sums over K / 16 products of 16 and what is behind them,
+  2^-23 (K/16 + 64) sum (|d sc q x| + |dmin m x|).
 * a gated product has the errors of both factors: |silu'| <= 1.1, silu(g) <= |g|.
 """
 import numpy as np
@@ -307,7 +308,7 @@ class Experts:
         x = x.double()
         y = x @ (a - m).T
         tol = 2.0 ** -8 * (x.abs() @ ((a - m).abs() + r).T) + 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ (a.abs() + m.abs()).T)
-        return y, tol
+        return y, tol + 2.0 ** -16 * (x.abs() @ m.abs().T)
 
 
 def check_experts(q4k, E, N, K, counts, gated, seed=0, lead=0, scale=1.0):
