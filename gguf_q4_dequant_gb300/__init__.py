@@ -537,10 +537,22 @@ def _types():
     return _dtypes
 
 
+_device = None  # a function that gives the current device
+
+
 def _rows(t, name):
-    """(rows, columns) of a tensor of a row per token or pair."""
+    """(rows, columns) of a tensor of a row per token or pair, which is on the device that the call goes to."""
+    global _device
     if isinstance(t, int) or t.dim() != 2:
         raise ValueError(f"{name} must be a tensor of two dimensions")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("tensor must live in CUDA device memory")
+    if _device is None:
+        import torch
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if device != _device():
+        raise ValueError(f"{name} is on device {device}, the current one is {_device()}")
     return t.shape
 
 

@@ -383,8 +383,9 @@ int q4k_logits_pick(const float* logits, int64_t M, int64_t V, float* out, int64
  *
  * The rules of the calls above hold: asynchronous on `stream`, no allocation,
  * no host synchronisation, capturable, arguments checked before any launch,
- * contents of device arrays never lead outside the arrays. Arrays that a call
- * writes overlap no other array of the call unless it is said.
+ * contents of device arrays never lead outside the arrays. Arrays and stream belong to
+ * the current device. Arrays that a call writes overlap no other array of the call unless it
+ * is said.
  *
  * A step has T tokens. Its pairs are (t, j), token t with its j-th pick, numbered
  * t*k + j. Sorted by expert and within an expert by number they are the rows of
@@ -469,7 +470,7 @@ int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* orde
  *   X  device, [pairs][K] bf16, values below 2^64 (those below 2^-56 may count as
  *      zero);  Y  device, [pairs][N] bf16
  *   starts  device, [E+1] int32
- * 1 <= E <= 1024, N >= 1, E*N < 2^31; K a multiple of 256, 256 .. 2^24; 1 <= pairs < 2^31.
+ * X and Y 16-byte aligned. 1 <= E <= 1024, N >= 1, E*N < 2^31; K a multiple of 256, 256 .. 2^24; 1 <= pairs < 2^31.
  */
 int q4k_experts_matmul(const void* W, int64_t E, int64_t N, int64_t K, const uint16_t* X, const int32_t* starts,
                        int64_t pairs, uint16_t* Y, void* stream);

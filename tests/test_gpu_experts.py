@@ -542,6 +542,22 @@ def test_combine(q4k, T, k, C, base):
 
 # ---------------------------------------------------------------- together ---
 
+def test_binding_refuses_another_device(q4k, monkeypatch):
+    """Rows on another device than the current one, which the kernels would run on."""
+    x, out = torch.zeros(4, 64, device=DEV), torch.zeros(4, 64, device=DEV)
+    q4k.q4k_add_norm(x, None, torch.ones(64, device=DEV), out=out)
+    monkeypatch.setattr(q4k, "_device", lambda: 1)
+    i, b = torch.zeros(4, 2, dtype=torch.int32, device=DEV), torch.zeros(8, 64, dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: q4k.q4k_add_norm(x, None, x[0], out=out),
+                 lambda: q4k.q4k_route(x, 2, 0, 1.0, i, out, i, i, i, i),
+                 lambda: q4k.q4k_experts_gather(b, i, 2, b),
+                 lambda: q4k.q4k_experts_matmul(i, 8, 64, b, i, b),
+                 lambda: q4k.q4k_experts_gated(i, i, 8, 64, b, i, b),
+                 lambda: q4k.q4k_experts_combine(b, i, x, out)):
+        with pytest.raises(ValueError, match="on device 0, the current one is 1"):
+            call()
+
+
 def test_binding_refuses_on_the_device(q4k):
     z = lambda *s, d=torch.float32: torch.zeros(*s, dtype=d, device=DEV)  # noqa: E731
     b16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
