@@ -170,8 +170,7 @@ def _eight(y):
     """e4m3 codes and the exponents of their scales, for each 32 columns (plain form)."""
     v = y.view(y.shape[0], -1, 32)
     m, e = torch.frexp(v.abs().amax(-1, keepdim=True))      # amax = m * 2^e, 1/2 <= m < 1
-    e = (e - 9 + (m > 0.875).to(torch.int32)).clamp(min=-127)  # amax <= 448 * 2^e
-    e = torch.where(m == 0, -127, e)
+    e = (e - 9 + (m > 0.875).to(torch.int32)).clamp(-127, 127)  # amax <= 448 * 2^e
     return torch.ldexp(v, -e).to(torch.float8_e4m3fn).view(y.shape), e.squeeze(-1)
 
 
