@@ -23,6 +23,9 @@ __host__ __device__ constexpr int pick_threads(int R) { return R <= 8 ? 1024 : 5
 // Steps of up to so many blocks have no scan of their own: each block adds up the
 // counts of the blocks before it (128 of them and 128 experts: two rounds of eight loads).
 constexpr int kRouteFew = 128;
+// Logits below this are masks, not scores (programs mask with -1e4, -1e9 or the type's lowest value, -65504 in
+// fp16): sigmoids over their sum are 0 for a token that has nothing else, as they are for one with only -inf.
+constexpr float kRouteMask = -1000.f;
 
 // ------------------------------------------------------------------- top k ---
 
@@ -81,10 +84,12 @@ __device__ __forceinline__ int pick_experts(const float* row, int E, int k, int 
                 if (logit_key(x[r]) != 0u) total += rel_exp(x[r], top);
         }
     } else {
-        // far below 0 the sigmoid is e^x: where they are divided by their sum, and would leave fp32's
-        // range first, they are taken relative to the largest
-        const bool far = weighting == Q4K_ROUTE_SIGMOID_TOP && top < -64.f && top >= -1000.f;
-        if (mine >= 0) rel = far ? rel_exp(mine_x, top) : 1.f / (1.f + expf(-mine_x));
+        // Where the sigmoids are divided by their sum and the largest logit is below 0, they are taken as
+        // e^(x - top) / (1 + e^x): the common factor e^top of sigmoid(x) goes with the sum, and
+        // nothing leaves fp32's range that the quotient does not. (From 0 up their sum is at least 1/2: what
+        // 1 / (1 + e^-x) loses below x = -88 is below 2^-125.)
+        const bool part = weighting == Q4K_ROUTE_SIGMOID_TOP && top < 0.f && top >= kRouteMask;
+        if (mine >= 0) rel = part ? rel_exp(mine_x, top) / (1.f + expf(mine_x)) : 1.f / (1.f + expf(-mine_x));
         total = rel;
     }
     if (weighting != Q4K_ROUTE_SIGMOID) {

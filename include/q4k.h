@@ -420,7 +420,7 @@ enum q4k_weighting {
     Q4K_ROUTE_SOFTMAX = 0,     /* softmax over all experts */
     Q4K_ROUTE_SOFTMAX_TOP = 1, /* softmax over the picked ones */
     Q4K_ROUTE_SIGMOID = 2,     /* 1 / (1 + exp(-logit)) */
-    Q4K_ROUTE_SIGMOID_TOP = 3  /* the same divided by their sum over the picked ones (0 where the largest logit is below -1000) */
+    Q4K_ROUTE_SIGMOID_TOP = 3  /* the same divided by their sum over the picked ones (0 where no logit is -1000 or more: a mask) */
 };
 
 /*
