@@ -79,6 +79,22 @@ __device__ __forceinline__ void store_eight(const float (&v)[8], uint8_t* codes,
     }
 }
 
+// The sum over a row's threads: a warp, or the whole block through `part` (32 floats).
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float s, float* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (!kWarp) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) part[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
+    return s;
+}
+
 // Rows of up to 8 * R columns a thread. kWarp: a warp per row, several rows a
 // block (the sum stays in the warp); else a block per row.
 template <typename X, typename O, int R, bool kWarp>
@@ -110,20 +126,20 @@ __global__ void __launch_bounds__(1024) q4k_add_norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(v[r][i], v[r][i], ss);
     }
+    __shared__ float part[2][32];
+    float mean = row_sum<kWarp>(ss, part[0]) / static_cast<float>(a.C);
+    if (!(mean < INFINITY)) {  // (the same for the whole row) the sum may pass fp32 where the mean does not
+        ss = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!kWarp) {
-        __shared__ float part[32];
-        if (lane == 0) part[warp] = ss;
-        __syncthreads();
-        ss = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : 0.f;
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[r][i] * 0x1p-8f, v[r][i] * 0x1p-8f, ss);
+        mean = row_sum<kWarp>(ss, part[1]) / static_cast<float>(a.C) * 0x1p16f;
     }
+    mean += a.eps;
     // 1 / sqrt(mean + eps) as the sum of two floats (a Newton step's correction of the rounded
     // root), and r * w * that with its products' errors taken along: y is the exact value but for its
     // last bit, so that codes and scales, which jump at borders, are those of the exact y almost always
-    const float mean = ss / static_cast<float>(a.C) + a.eps;
     const float rs = 1.f / sqrtf(mean);
     const float t = mean * rs, rest = fmaf(-t, rs, fmaf(-fmaf(mean, rs, -t), rs, 1.f));
     const float rs_lo = mean > 0.f && rs < INFINITY ? 0.5f * rs * rest : 0.f;

@@ -401,7 +401,8 @@ enum q4k_type { Q4K_F32 = 0, Q4K_BF16 = 1 };
  * bits: of every 32 columns the scale is the smallest power of two s >= 2^-127
  * with max|y| <= 448 s, held as the byte log2(s) + 127, and the codes are y / s
  * rounded to e4m3 (4 significant bits, to nearest even). 32 columns with an
- * infinity or a NaN have the scale byte 255 and codes of NaN.
+ * infinity or a NaN have the scale byte 255 and codes of NaN. Where mean(r^2)
+ * passes fp32, the row's y are 0 (those of infinities NaN).
  *   x       device, [T][C], fp32 or bf16 by x_type
  *   delta   device, [T][C] floats (what the layer before adds); NULL: 0
  *   weight  device, [C] floats

@@ -70,3 +70,21 @@ def test_sigmoids_of_masks_over_their_sum(q4k):
     ids, w, _, _, _ = route(q4k, logits, 3, q4k.ROUTE_SIGMOID_TOP)
     assert bool((w[:4] == 0).all())
     assert w[4:].tolist() == [[1.0, 0.0, 0.0]] * 4 and ids[4:].tolist() == [[2, 0, 1]] * 4
+
+
+# -------------------------------------------------------------------- norm ---
+
+@pytest.mark.parametrize("C", [512, 1056, 9216, 32768])
+@pytest.mark.parametrize("size", [1e18, 4e18])
+def test_norm_sums_past_fp32(q4k, C, size):
+    """Rows whose squares have a sum past fp32, but not a mean. The sum goes through a chain of at most 32 terms and two
+    trees of 5, half of which counts after the root; the mean, the root and the products add a rounding each: 2^-19."""
+    g = gen(C)
+    x = torch.randn(3, C, generator=g).clamp(-4, 4) * size
+    x[2] *= 2.0 ** -40  # (and one without)
+    w = 0.5 + torch.rand(C, generator=g)
+    out = new(3, C)
+    q4k.q4k_add_norm(x.to(DEV), None, w.to(DEV), 1e-6, out=out)
+    r = x.double()
+    y = r / (r.square().mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
+    assert bool(((out.cpu().double() - y).abs() <= 2.0 ** -19 * y.abs()).all())
