@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(1024) q4k_add_norm_kernel(const NormArgs a) {
     }
     mean += a.eps;
     // 1 / sqrt(mean + eps) as the sum of two floats (a Newton step's correction of the rounded
-    // root), and r * w * that with its products' errors taken along: y is the exact value but for its
-    // last bit, so that codes and scales, which jump at borders, are those of the exact y almost always
+    // root), and r times that as a product with its error, which nothing makes overflow (it is below
+    // sqrt(C)) before it meets the weight: y is the exact value but for its last bit, so that codes and
+    // scales, which jump at borders, are those of the exact y almost always
     const float rs = 1.f / sqrtf(mean);
     const float t = mean * rs, rest = fmaf(-t, rs, fmaf(-fmaf(mean, rs, -t), rs, 1.f));
     const float rs_lo = mean > 0.f && rs < INFINITY ? 0.5f * rs * rest : 0.f;
@@ -155,9 +156,9 @@ __global__ void __launch_bounds__(1024) q4k_add_norm_kernel(const NormArgs a) {
             w[4] = q.x; w[5] = q.y; w[6] = q.z; w[7] = q.w;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float m = v[r][i] * w[i], off_m = fmaf(v[r][i], w[i], -m);
-                const float y = fmaf(m, rs, fmaf(m, rs_lo, off_m * rs));
-                w[i] = isfinite(y) ? y : m * rs;
+                const float u = v[r][i] * rs, off_u = fmaf(v[r][i], rs_lo, fmaf(v[r][i], rs, -u));
+                const float y = fmaf(u, w[i], off_u * w[i]);
+                w[i] = isfinite(y) ? y : u * w[i];  // (a mean past fp32: rs = 0, its correction NaN)
             }
             if (a.out != nullptr) store8(static_cast<O*>(a.out) + off + c, w, a.stream);
         }

@@ -88,3 +88,33 @@ def test_norm_sums_past_fp32(q4k, C, size):
     r = x.double()
     y = r / (r.square().mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
     assert bool(((out.cpu().double() - y).abs() <= 2.0 ** -19 * y.abs()).all())
+
+
+@pytest.mark.parametrize("C", [64, 1056, 9216])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_norm_weights_past_the_row(q4k, C, kind):
+    """Weights and rows whose products leave fp32's range although the norm does not. The sum of squares goes through
+    a chain of at most 32 terms and two trees of 5, half of which counts after the root; the mean, the root and the
+    products add a rounding each: 2^-19."""
+    g = gen(C)
+    sizes = torch.tensor([1e18, 3e15, 1.0, 1e-9, 1e-15])
+    x = (torch.randn(5, C, generator=g).clamp(-4, 4) * sizes.unsqueeze(1)).to(kind)
+    for weight in (1e-30, 1e-20, 1e22, 1e30, 1e35):
+        w = (0.5 + torch.rand(C, generator=g)) * weight
+        out = new(5, C)
+        q4k.q4k_add_norm(x.to(DEV), None, w.to(DEV), 0.0, out=out)
+        r = x.double()
+        y = r / r.square().mean(1, keepdim=True).sqrt() * w.double()
+        far = y.abs() > 2.0 ** -120  # (below, fp32 has fewer bits)
+        assert bool(((out.cpu().double() - y).abs() <= 2.0 ** -19 * y.abs())[far].all())
+
+
+@pytest.mark.parametrize("weight", [0.25, 1.0, 4.0, -1e30])
+def test_norm_of_rows_past_fp32(q4k, weight):
+    """Squares past fp32: the root is infinite, the row 0, whatever the weight; codes and scales of zeros."""
+    C = 96
+    x = torch.full((2, C), 3e38)
+    x[1, 1:] = 1.0
+    out, codes, scales = new(2, C, fill=7), new(2, C, dtype=torch.uint8, fill=1), new(2, C // 32, dtype=torch.uint8, fill=1)
+    q4k.q4k_add_norm(x.to(DEV), None, new(C, fill=weight), 1e-6, out=out, codes=codes, scales=scales)
+    assert bool((out == 0).all()) and bool((codes & 127 == 0).all()) and bool((scales == 0).all())
