@@ -70,7 +70,9 @@ struct XMaps {
 };
 
 // The scale and min of 32 weights as bf16 pairs for dequant8: w = d1 q - m1 =
-// d1 (q - c) + r with the code c nearest to w = 0 and r = c d1 - m1, d1 the sum of two bf16.
+// d1 (q - c) + r with c the 16th of a code nearest to w = 0 and r = c d1 - m1, d1 the sum of two bf16.
+// (16 (q - c) has 8 bits, so q - c is exact in bf16; with whole codes for c, r is up to 16 times as large, and
+// its two roundings show.)
 struct EgScale {
     __nv_bfloat162 dh, dl, r, c;
 };
@@ -78,13 +80,13 @@ struct EgScale {
 __device__ __forceinline__ EgScale eg_scale(float d1, float m1, float unit) {
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d1));
-    const float c = fminf(fmaxf(rintf(m1 * inv), 0.f), 15.f);  // (0 where the quotient is not a number)
+    const float c = fminf(fmaxf(rintf(m1 * inv * 16.f), 0.f), 255.f);  // 16ths (0 where the quotient is not a number)
     const float d = d1 * (1.f / unit);
     EgScale s;
     s.dh = __float2bfloat162_rn(d);
     s.dl = __float2bfloat162_rn(d - __low2float(s.dh));
-    s.r = __float2bfloat162_rn(fmaf(c, d1, -m1));
-    s.c = __float2bfloat162_rn(-c * unit);
+    s.r = __float2bfloat162_rn(fmaf(c, d1 * 0.0625f, -m1));
+    s.c = __float2bfloat162_rn(-c * (unit * 0.0625f));
     return s;
 }
 
@@ -94,8 +96,9 @@ __device__ __forceinline__ EgScale eg_scale(float d1, float m1, float unit) {
 // (q - c) 2^-6 or 2^-2 of it, exactly, and w = (q - c) dh + ((q - c) dl + r) takes two more: per
 // weight 0.75 integer instructions, at half the rate of the FMAs' 1.5 (masks, fp32
 // FMAs and conversions take 1.75, and that pipe bound the kernel: 4096 tokens to 8 of 128
-// experts, gated 196 us, 182 this way). Either |r| <= |d1| / 2, or c is 0 or 15 and |r| <=
-// |w|; the two roundings are off by 2^-8 (|w| + |r|) at most.
+// experts, gated 196 us, 182 this way). Roundings: r, the inner FMA (about |r| too) and w, and
+// what is left of d1 (2^-16): off by 2^-8 (|w| + 2 |r|) to within 2 %. |r| <= |d1| / 32 where the weight 0
+// lies among the codes (0 <= m1 <= 15.96 d1); elsewhere c is at an end and |r| <= |w|.
 __device__ __forceinline__ void dequant8(uint32_t w, const EgScale& lo, const EgScale& hi, uint32_t* o) {
     const __nv_bfloat162 up = __float2bfloat162_rn(exp2i(127));
     const uint32_t p[2] = {__byte_perm(w, 0, 0x4140), __byte_perm(w, 0, 0x4342)};

@@ -462,9 +462,10 @@ int q4k_experts_gather(const void* X, const uint8_t* scales, const int32_t* orde
  * Y[p] = g / (1 + exp(-g)) * u with g = X[p] gate_e^T and u = X[p] up_e^T in fp32.
  * By the sizes (never by what the arrays hold) one of two kernels runs: for few
  * rows the weights enter exactly (the sums of x beside the mins as two bf16 each,
- * off by 2^-16); for many the tcgen05 tensor cores take them as bf16, off by
- * 2^-8 (|w| + |r|) at most, r the weight of the code nearest to 0 (as
- * q4k_matmul_bf16's, by 2^-8 |w|, for 17 rows and more).
+ * off by 2^-16); for many the tcgen05 tensor cores take them as bf16: with a =
+ * d sc and b = dmin m of a weight's sub-block, off by 2^-8 (|w| + |a| / 16) to
+ * within 3 % where 0 <= b <= 15.96 a, by 2^-8 3 |w| elsewhere (q4k_matmul_bf16's
+ * weights, for 17 rows and more, by 2^-8 |w|).
  * Rows before starts[0] and from starts[E] on are left as they are; starts is
  * taken as ascending and inside [0, pairs] (values are clamped to that).
  *   W, gate, up  device, E*N*K/256*144 bytes, 16-byte aligned

@@ -4,6 +4,9 @@ implementations in 64 bits. Tolerances count half a step for every rounding
 import pytest
 import torch
 
+from captured import kernels
+from gguf_q4_dequant_gb300 import synth
+
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
@@ -118,3 +121,78 @@ def test_norm_of_rows_past_fp32(q4k, weight):
     out, codes, scales = new(2, C, fill=7), new(2, C, dtype=torch.uint8, fill=1), new(2, C // 32, dtype=torch.uint8, fill=1)
     q4k.q4k_add_norm(x.to(DEV), None, new(C, fill=weight), 1e-6, out=out, codes=codes, scales=scales)
     assert bool((out == 0).all()) and bool((codes & 127 == 0).all()) and bool((scales == 0).all())
+
+
+# ---------------------------------------------------------------- products ---
+
+def fields(w):
+    """a = d sc, b = dmin m and the code q of each weight of packed rows [.., K / 256 * 144], in 64 bits: w = a q - b."""
+    blocks = w.reshape(w.shape[0], -1, 144)
+    d, dmin = blocks[..., :4].contiguous().view(torch.float16).double().unbind(-1)
+    s, qs = blocks[..., 4:16].long(), blocks[..., 16:].long().unflatten(-1, (4, 32))
+    sc = torch.cat((s[..., :4] % 64, s[..., 8:] % 16 + s[..., :4] // 64 * 16), -1)
+    m = torch.cat((s[..., 4:8] % 64, s[..., 8:] // 16 + s[..., 4:8] // 64 * 16), -1)
+    q = torch.stack((qs % 16, qs // 16), -2).flatten(-3, -2).double()
+    a, b = d.unsqueeze(-1) * sc, dmin.unsqueeze(-1) * m
+    return a.repeat_interleave(32, -1).flatten(1), b.repeat_interleave(32, -1).flatten(1), q.flatten(-2).flatten(1)
+
+
+def set_heads(w, heads):
+    """d and dmin of the super-blocks in turn, as fp16."""
+    blocks = w.view(-1, 144)
+    h = torch.tensor(heads, dtype=F64).to(torch.float16)
+    blocks[:, :4] = h[torch.arange(len(blocks)) % len(h)].view(torch.uint8)
+
+
+def many_bound(a, b, w):
+    """How far the weights of the kernel for many rows may be off: bf16 roundings of r, of the inner FMA (|r| and 2^-8 of
+    what d leaves) and of the weight; fp32 ones of a and b (2^-24), and a c on the other side of a tie, 2^-19 |a|."""
+    c = torch.where(a != 0, b / a, 0.0).mul(16).round().clamp(0, 255) / 16
+    return 2.0 ** -8 * (1 + 2.0 ** -6) * (w.abs() + 2 * (c * a - b).abs()) + 2.0 ** -19 * a.abs()
+
+
+def product(q4k, gated, w, w2, N, K, x, starts, y):
+    if gated:
+        q4k.q4k_experts_gated(w, w2, N, K, x, starts, y)
+    else:
+        q4k.q4k_experts_matmul(w, N, K, x, starts, y)
+
+
+def check_kernel(many, call):
+    """Which of the two kernels the call takes."""
+    name, = kernels(call)
+    assert ("experts_gemm_kernel" in name) == many, name
+
+
+def test_single_weights_of_many_rows(q4k):
+    """Rows of x with one power of two each: the outputs are the weights that the kernel for many rows takes, exactly."""
+    E, N, K = 2, 256, 512
+    w = torch.stack([synth.weight_rows(40 + e, N, K) for e in range(E)])
+    g = gen(4)
+    w.view(-1, 144)[:, 4:] = torch.randint(0, 256, (E * N * K // 256, 140), generator=g, dtype=torch.uint8)
+    d = torch.exp2(-14 * torch.rand(997, generator=g, dtype=F64))
+    odd = [[0.0, 1.0], [1.0, 0.0], [0.0, 0.0], [-1.0, 2.0], [2.0, -1.0], [-1.0, -4.0], [2.0 ** -24, 2.0 ** -24],
+           [2.0 ** -24, 1.0], [1.0, 2.0 ** -24], [60.0, 60.0], [6e4, 6e4], [0.830078125, 15.2265625], [0.00014150143, 0.0004968643]]
+    set_heads(w, odd + torch.stack((d, d * 16 * torch.rand(997, generator=g, dtype=F64)), 1).tolist())
+    # two sub-blocks whose errors are among the largest
+    for row, head, sc, m, q in ((3, odd[-2], 39, 34, 14), (5, odd[-1], 21, 8, 2)):
+        block = w[1].view(N, K // 256, 144)[row, 0]
+        block[:4] = torch.tensor(head, dtype=torch.float16).view(torch.uint8)
+        block[4], block[8], block[16] = sc, m, q
+    size = torch.exp2(torch.arange(4, dtype=F64) * 3 - 6).repeat_interleave(K) * (1 - 2 * (torch.arange(4 * K) % 2))
+    x = (torch.eye(K, dtype=F64).repeat(4, 1) * size.unsqueeze(1)).to(torch.bfloat16).repeat(E, 1).to(DEV)
+    starts = torch.tensor([0, 4 * K, 8 * K], dtype=torch.int32, device=DEV)
+    y = new(E * 4 * K, N, dtype=torch.bfloat16)
+    wd = w.to(DEV)
+    call = lambda: q4k.q4k_experts_matmul(wd, N, K, x, starts, y)  # noqa: E731
+    check_kernel(True, call)
+    for e in range(E):
+        a, b, q = fields(w[e].reshape(N, -1))
+        want = a * q - b
+        tol = many_bound(a, b, want)
+        got = y[4 * K * e:4 * K * (e + 1)].cpu().double() / size.unsqueeze(1)
+        assert bool(((got.view(4, K, N) - want.T).abs() <= tol.T).all())
+        # what the header says of weights around 0, and elsewhere
+        inside = (a != 0) & (b / a >= 0) & (b / a <= 15.96)
+        assert bool((tol <= 2.0 ** -8 * 1.03 * (want.abs() + a.abs() / 16))[inside].all())
+        assert bool((tol <= 2.0 ** -8 * 3.06 * want.abs() + 2.0 ** -19 * a.abs())[~inside].all())
