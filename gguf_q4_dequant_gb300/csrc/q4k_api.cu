@@ -23,6 +23,7 @@
 #include "q4k_device.cuh"
 #include "q4k_experts.h"
 #include "q4k_internal.h"
+#include "q4k_maps.h"
 #include "q4k_serve.h"
 
 namespace q4k {
@@ -145,26 +146,15 @@ int check_dims(int64_t N, int64_t K) {
     return Q4K_OK;
 }
 
-// Encoded tensor maps, cached per host thread. A map is a pure function of the
-// base address, the tensor's dimensions and the box (everything else is fixed
-// per kind), so a cached map is valid for any later call with the same key --
-// whatever the memory holds by then. Direct-mapped: a collision re-encodes.
+// Encoded tensor maps, cached per host thread, valid for any later call with the
+// same key -- whatever the memory holds by then. Direct-mapped: a collision re-encodes.
 // (A decode step issues one call per weight matrix, every token, with the same
 // pointers: the cache takes cuTensorMapEncodeTiled off that host path.)
-struct MapKey {
-    uintptr_t ptr;
-    int64_t a, b;
-    int box, kind;
-    bool operator==(const MapKey& o) const {
-        return ptr == o.ptr && a == o.a && b == o.b && box == o.box && kind == o.kind;
-    }
-};
 struct MapEntry {
     CUtensorMap map;
     MapKey key;
     bool valid;
 };
-constexpr int kMapCacheSize = 1024;
 
 MapEntry* map_slot(const MapKey& k) {
     thread_local std::unique_ptr<MapEntry[]> cache;
@@ -172,11 +162,7 @@ MapEntry* map_slot(const MapKey& k) {
         cache.reset(new MapEntry[kMapCacheSize]);
         for (int i = 0; i < kMapCacheSize; ++i) cache[i].valid = false;
     }
-    uint64_t h = static_cast<uint64_t>(k.ptr >> 4) * 0x9E3779B97F4A7C15ull;
-    h ^= static_cast<uint64_t>(k.a) * 0xBF58476D1CE4E5B9ull;
-    h ^= static_cast<uint64_t>(k.b) * 0x94D049BB133111EBull;
-    h ^= static_cast<uint64_t>(k.box * 4 + k.kind);
-    return &cache[(h >> 40) % kMapCacheSize];
+    return &cache[map_slot_index(k)];
 }
 
 // W as a 2-D byte tensor {K/256*144, N}; box = one super-block of `rows` rows.
