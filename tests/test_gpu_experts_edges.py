@@ -196,3 +196,102 @@ def test_single_weights_of_many_rows(q4k):
         inside = (a != 0) & (b / a >= 0) & (b / a <= 15.96)
         assert bool((tol <= 2.0 ** -8 * 1.03 * (want.abs() + a.abs() / 16))[inside].all())
         assert bool((tol <= 2.0 ** -8 * 3.06 * want.abs() + 2.0 ** -19 * a.abs())[~inside].all())
+
+
+class Experts:
+    """E packed matrices [N][K] (`distinct` different ones in turn), their products in 64 bits and how far each of the
+    two kernels may be off."""
+
+    def __init__(self, seed, E, N, K, distinct=None, change=None):
+        self.E, self.N, self.K = E, N, K
+        w = torch.stack([synth.weight_rows(seed + e, N, K).view(N, -1) for e in range(distinct or E)])
+        if change is not None:
+            change(w)
+        self.fields = [[t.to(DEV) for t in fields(m)] for m in w]
+        self.packed = w.repeat(E // len(w), 1, 1).to(DEV)
+
+    def product(self, e, x, many):
+        """x W_e^T, and the bound: the weights' error for many rows; for few each sum of 32 x as two bf16, 2^-16; fp32
+        sums over K / 16 products of 16 and what joins them, 2^-23 each."""
+        a, b, q = self.fields[e % len(self.fields)]
+        w, x = a * q - b, x.double()
+        tol = 2.0 ** -23 * (self.K / 16 + 64) * (x.abs() @ ((a * q).abs() + b.abs()).T)
+        if many:
+            tol += x.abs() @ many_bound(a, b, w).T
+        else:
+            tol += 2.0 ** -16 * (x.unflatten(1, (-1, 32)).sum(2).abs() @ b.abs()[:, ::32].T)
+        return x @ w.T, tol
+
+
+def gated_of(g, tg, u, tu):
+    """silu(g) u and its bound from those of the factors: |silu'| <= 1.1, |silu(g)| <= |g|, 2^-20 for silu itself."""
+    silu = g * torch.sigmoid(g)
+    return silu * u, 1.1 * tg * (u.abs() + tu) + silu.abs() * tu + 2.0 ** -20 * (silu * u).abs()
+
+
+def check_products(q4k, w, up, counts, x, many, lead=0):
+    """The product of every expert (gated with `up`), by the kernel that is meant; rows of no expert stay."""
+    starts = [lead]
+    for c in counts:
+        starts.append(starts[-1] + c)
+    assert len(x) >= starts[-1] and len(counts) == w.E
+    x[:lead], x[starts[-1]:] = float("nan"), float("nan")
+    y = new(len(x), w.N, dtype=torch.bfloat16, fill=-12345)
+    keep = y[0, 0].clone()
+    at = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    check_kernel(many, lambda: product(q4k, up is not None, w.packed, None if up is None else up.packed, w.N, w.K, x, at, y))
+    assert bool((y[:lead] == keep).all()) and bool((y[starts[-1]:] == keep).all())
+    for e, (a, b) in enumerate(zip(starts, starts[1:])):
+        if a == b:
+            continue
+        want, tol = w.product(e, x[a:b], many)
+        if up is not None:
+            want, tol = gated_of(want, tol, *up.product(e, x[a:b], many))
+        err = (y[a:b].double() - want).abs()
+        assert bool((err <= tol + 2.0 ** -8 * want.abs() + 1e-38).all()), (e, float((err - 2.0 ** -8 * want.abs()).div(tol).max()))
+
+
+def uneven(seed, E, rows, empty):
+    """E counts that add up to `rows`, a share of them 0 (the first and the last too)."""
+    g = gen(seed)
+    live = torch.rand(E, generator=g) >= empty
+    live[0] = live[-1] = False
+    cut = torch.sort(torch.randint(0, rows + 1, (int(live.sum()) - 1,), generator=g)).values.tolist()
+    counts = torch.zeros(E, dtype=torch.int64)
+    counts[live] = torch.tensor([0, *cut, rows]).diff()
+    return counts.tolist()
+
+
+def draw_x(seed, P, K, size=1.0):
+    return (torch.randn(P, K, generator=gen(seed)) * size).to(torch.bfloat16).to(DEV)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,N,K,rows,empty", [(128, 128, 256, 6000, 0.3), (40, 300, 4096, 1700, 0.2), (1024, 200, 256, 41000, 0.5),
+                                              (33, 129, 512, 4000, 0.8), (3, 144, 16384, 3300, 0.0), (64, 512, 1280, 3000, 0.1)])
+def test_many_rows_of_many_experts(q4k, E, N, K, rows, empty, gated):
+    """More experts than lanes, most of them or none empty, and long rows, in the kernel for many rows."""
+    distinct = 8 if E % 8 == 0 else E
+    w = Experts(E + N, E, N, K, distinct)
+    up = Experts(E + N + 5000, E, N, K, distinct) if gated else None
+    check_products(q4k, w, up, uneven(E, E, rows, empty), draw_x(E + K, rows + 7, K, 0.02 if gated else 1.0), True, lead=3)
+
+
+def odd_heads(w):
+    """Super-blocks whose d or dmin is 0, negative, the smallest number or large."""
+    set_heads(w, [[0.0, 1.0], [1.0, 0.0], [0.0, 0.0], [-1.0, 2.0], [2.0, -1.0], [-1.0, -4.0], [2.0 ** -24, 2.0 ** -24],
+                  [2.0 ** -24, 1.0], [1.0, 2.0 ** -24], [60.0, 60.0]])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts,many", [([3, 9], False), ([200, 90], False), ([6000, 4100], True)])
+def test_odd_heads(q4k, counts, many, gated):
+    w = Experts(31, 2, 40, 512, change=odd_heads)
+    up = Experts(35, 2, 40, 512, change=odd_heads) if gated else None
+    check_products(q4k, w, up, counts, draw_x(5, sum(counts), 512, 2.0 ** -6 if gated else 1.0), many)
+
+
+@pytest.mark.parametrize("counts", [[1, 192, 0, 2400], [193, 4000, 191, 1], [385, 2303, 2305, 16]])
+def test_tiles_of_many_rows(q4k, counts):
+    """Rows of an expert around the borders of the tiles that they are cut into."""
+    check_products(q4k, Experts(50, 4, 257, 512), None, counts, draw_x(9, sum(counts) + 1, 512), True)
