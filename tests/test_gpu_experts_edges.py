@@ -295,3 +295,31 @@ def test_odd_heads(q4k, counts, many, gated):
 def test_tiles_of_many_rows(q4k, counts):
     """Rows of an expert around the borders of the tiles that they are cut into."""
     check_products(q4k, Experts(50, 4, 257, 512), None, counts, draw_x(9, sum(counts) + 1, 512), True)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,N,K,counts", [(1, 64, 512, [1]), (2, 64, 512, [8, 7]), (4, 61, 2048, [8, 0, 1, 17]), (3, 36, 4352, [2, 1, 4]),
+                                          (2, 300, 256, [40, 25]), (40, 64, 512, [1, 2, 3, 0] * 10), (5, 640, 768, [16, 0, 9, 3, 1])])
+def test_weights_of_few_rows(q4k, E, N, K, counts, gated):
+    """The kernel for few rows takes weights as they are: no bf16 rounding of them would pass."""
+    w = Experts(E * N + K, E, N, K)
+    up = Experts(E * N + K + 5000, E, N, K) if gated else None
+    check_products(q4k, w, up, counts, draw_x(K, sum(counts), K, 0.02 if gated else 1.0), False)
+
+
+def large_mins(w):
+    """Mins as large as the codes' mean, so that a sum of x counts as much as all the products."""
+    set_heads(w, [[1.0, 7.5], [0.25, 1.875], [0.01, 0.075]])
+    blocks = w.view(-1, 144)
+    blocks[:, 8:12] = blocks[:, 4:8]
+    blocks[:, 12:16] = (blocks[:, 12:16] & 15) * 17  # (with the upper bits alike: every min as its scale)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,N,K,counts", [(1, 64, 256, [8]), (2, 64, 512, [8, 7]), (3, 61, 1024, [3, 0, 9]), (1, 640, 768, [21])])
+def test_sums_of_x_of_few_rows(q4k, E, N, K, counts, gated):
+    """x of one sign and large mins: the sums of x are kept to 2^-16, one bf16 each would not pass."""
+    w = Experts(E * N + K, E, N, K, change=large_mins)
+    up = Experts(E * N + K + 5000, E, N, K, change=large_mins) if gated else None
+    x = ((0.5 + torch.rand(sum(counts), K, generator=gen(K))) * (2.0 ** -14 if gated else 1.0)).to(torch.bfloat16).to(DEV)
+    check_products(q4k, w, up, counts, x, False)
