@@ -23,7 +23,10 @@ def kernels(call):
     nodes, names = (ctypes.c_void_p * n.value)(), []
     assert cuda.cuGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
     for node in nodes:
-        p, name = _KernelNode(), ctypes.c_char_p()
+        kind, p, name = ctypes.c_int(), _KernelNode(), ctypes.c_char_p()
+        assert cuda.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value != 0:  # no kernel
+            continue
         assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
         assert cuda.cuFuncGetName(ctypes.byref(name), ctypes.c_void_p(p.func)) == 0
         names.append(name.value.decode())

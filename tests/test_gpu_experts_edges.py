@@ -6,6 +6,7 @@ import torch
 
 from captured import kernels
 from gguf_q4_dequant_gb300 import synth
+from test_gpu_experts import Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -73,6 +74,79 @@ def test_sigmoids_of_masks_over_their_sum(q4k):
     ids, w, _, _, _ = route(q4k, logits, 3, q4k.ROUTE_SIGMOID_TOP)
     assert bool((w[:4] == 0).all())
     assert w[4:].tolist() == [[1.0, 0.0, 0.0]] * 4 and ids[4:].tolist() == [[2, 0, 1]] * 4
+
+
+def check_route(q4k, logits, k, weighting):
+    """Everything that a call gives, against a stable sort of 64-bit logits and of the pairs by expert."""
+    T, E = logits.shape
+    ids, weights, order, slots, starts = route(q4k, logits, k, weighting)
+    x = logits.to(DEV).double()
+    x = torch.where(x.isnan(), float("-inf"), x)
+    key, want = (t[:, :k] for t in torch.sort(x, dim=1, descending=True, stable=True))
+    live = key > float("-inf")
+    want = torch.where(live, want, -1)
+    assert torch.equal(ids.long(), want)
+    flat = want.flatten()
+    pairs = torch.sort(torch.where(flat < 0, E, flat), stable=True).indices
+    n = int(live.sum())
+    assert torch.equal(order[:n].long(), pairs[:n]) and bool((order[n:] == -1).all())
+    at = torch.full_like(flat, -1)
+    at[pairs[:n]] = torch.arange(n, device=DEV)
+    assert torch.equal(slots.flatten().long(), at)
+    counts = torch.bincount(flat[flat >= 0], minlength=E)
+    assert starts.tolist() == [0, *counts.cumsum(0).tolist()]
+    # exponentials to two steps, sums of at most 32 terms and a tree of 5 with a rounding each, and the quotient: 2^-18;
+    # a difference's rounding as many times as it is large
+    rel = torch.where(live, torch.exp(key - key[:, :1]), 0.0)
+    total = (torch.exp(x - key[:, :1]) if weighting == q4k.ROUTE_SOFTMAX else rel).nan_to_num(0).sum(1, keepdim=True)
+    w = torch.where(live, rel / total, 0.0)
+    d = torch.where(live, key - key[:, :1], 0.0).abs()
+    assert bool(((weights.double() - w).abs() <= (2.0 ** -18 + 2.0 ** -23 * d) * w + 1e-37).all())
+
+
+@pytest.mark.parametrize("T", [8191, 8192, 8193, 8257, 20011])
+@pytest.mark.parametrize("E,k", [(61, 4), (1000, 17), (128, 8), (1024, 32), (33, 1), (5, 5)])
+def test_route_of_many_groups(q4k, T, E, k):
+    """Both sides of 128 groups of 64 tokens, above which the counts are scanned by a kernel of their own."""
+    g = gen(T + E)
+    logits = torch.randn(T, E, generator=g) * 3
+    on_device = logits.to(DEV)
+    names = kernels(lambda: route(q4k, on_device, k, q4k.ROUTE_SOFTMAX))
+    assert any("route_scan" in n for n in names) == (T > 8192)
+    check_route(q4k, logits, k, q4k.ROUTE_SOFTMAX)
+    logits = torch.round(logits)  # ties, masks, tokens without an expert, experts without a token
+    logits[torch.rand(T, E, generator=g) < 0.6] = float("-inf")
+    logits[torch.rand(T, E, generator=g) < 0.1] = float("nan")
+    logits[::97] = float("-inf")
+    logits[:, ::7] = float("-inf")
+    if E > 5:
+        logits[:, 3] = 1e3
+    check_route(q4k, logits, k, q4k.ROUTE_SOFTMAX_TOP)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+def test_layer_of_many_groups_captured(q4k, mode):
+    """A layer whose route has all of its launches, captured twice in a row, in every launch mode."""
+    layer = Layer(q4k, 8300, 6, 2, 256, 256, True, seed=5)
+    old = q4k.q4k_set_pdl(mode)
+    try:
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            layer.run()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=side):
+                layer.run()
+                layer.run()
+        for _ in range(2):
+            layer.dx.normal_()
+            layer.out.fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            graph.replay()
+            torch.cuda.synchronize()
+            layer.check()
+    finally:
+        q4k.q4k_set_pdl(old)
 
 
 # -------------------------------------------------------------------- norm ---
