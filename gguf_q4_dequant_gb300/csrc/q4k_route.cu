@@ -489,7 +489,7 @@ cudaError_t route_r(const RouteArgs& a, cudaStream_t stream, const DeviceInfo& d
         const int spread = a.T > (a.E <= kOneSpreadExperts ? kOneSpread : 1) ? 8 : 1;
         return launch_serve(q4k_route_one_kernel<R>, dim3(spread), dim3(32 * warps), smem, stream, pdl, spread, a);
     }
-    const int blocks = (a.T + kRouteTokens - 1) / kRouteTokens;
+    const int blocks = (a.T - 1) / kRouteTokens + 1;  // (T may be 2^31 - 1)
     const size_t chosen = 2 * static_cast<size_t>(kRouteTokens) * a.k;
     int spread = 1;  // (1003 tokens, 61 experts: 8.1 us, 9.4 with 1)
     while (spread < 8 && 2 * spread * blocks <= dev.num_sms) spread *= 2;

@@ -149,6 +149,24 @@ def test_layer_of_many_groups_captured(q4k, mode):
         q4k.q4k_set_pdl(old)
 
 
+def test_route_of_the_most_tokens(q4k):
+    """2^31 - 1 tokens, every fifth without its expert: the count of the groups stays in 32 bits."""
+    T, i32 = (1 << 31) - 1, torch.int32
+    logits = new(T, 1)
+    logits[::5] = float("-inf")
+    ids, slots, order, starts = (new(n, dtype=i32, fill=-77) for n in (T, T, T, 2))
+    weights, ws = new(T, fill=7), new(q4k.q4k_route_workspace(T, 1), dtype=torch.uint8)
+    q4k.q4k_route(logits, 1, q4k.ROUTE_SOFTMAX, 1.0, ids, weights, order, slots, starts, ws)
+    n = T - (T + 4) // 5
+    assert starts.tolist() == [0, n]
+    for at in range(0, T, 1 << 28):
+        i = torch.arange(at, min(at + (1 << 28), T), device=DEV)
+        part, live = slice(at, at + len(i)), i % 5 != 0
+        assert torch.equal(ids[part], torch.where(live, 0, -1).to(i32)) and torch.equal(weights[part], live.float())
+        assert torch.equal(slots[part], torch.where(live, i - i // 5 - 1, -1).to(i32))
+        assert torch.equal(order[part], torch.where(i < n, i + i // 4 + 1, -1).to(i32))
+
+
 # -------------------------------------------------------------------- norm ---
 
 @pytest.mark.parametrize("C", [512, 1056, 9216, 32768])
