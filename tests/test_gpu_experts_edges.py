@@ -390,6 +390,16 @@ def test_tiles_of_many_rows(q4k, counts):
 
 
 @pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,N,counts,many", [(1, 65536, [24], True), (2, 40000, [3, 30], False), (1, 70001, [31], True),
+                                             (3, 30011, [0, 33, 20], False)])
+def test_many_columns_of_few_rows(q4k, E, N, counts, many, gated):
+    """Columns enough for the kernel of many rows, with fewer rows than its boxes of x have, and somewhat fewer."""
+    w = Experts(E + N, E, N, 256)
+    up = Experts(E + N + 5000, E, N, 256) if gated else None
+    check_products(q4k, w, up, counts, draw_x(N, sum(counts), 256, 0.02 if gated else 1.0), many)
+
+
+@pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("E,N,K,counts", [(1, 64, 512, [1]), (2, 64, 512, [8, 7]), (4, 61, 2048, [8, 0, 1, 17]), (3, 36, 4352, [2, 1, 4]),
                                           (2, 300, 256, [40, 25]), (40, 64, 512, [1, 2, 3, 0] * 10), (5, 640, 768, [16, 0, 9, 3, 1])])
 def test_weights_of_few_rows(q4k, E, N, K, counts, gated):
