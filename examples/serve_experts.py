@@ -1,7 +1,7 @@
 """The decoder of serve.py with a mixture of experts for its feed-forward part.
 
-Every layer's norm takes what attention adds and writes the router's rows in
-bf16 and the experts' in 8 bits; the router's picks put the rows in the order
+Every layer's norm takes what attention adds and writes the rows for the
+router and the experts in bf16; the router's picks put the rows in the order
 of their experts, whose packed Q4_K matrices give gate, up and down; the rows
 come back to their tokens with the picks' weights, onto the residual stream.
 
@@ -45,15 +45,15 @@ class Server(serve.Server):
         def new(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
         bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
-        h, codes, scales = new(T, C, dtype=bf16), new(T, C, dtype=u8), new(T, C // 32, dtype=u8)
-        q4k.q4k_add_norm(x, delta, m.norm, 1e-6, sum=x, out=h, codes=codes, scales=scales)
+        h = new(T, C, dtype=bf16)
+        q4k.q4k_add_norm(x, delta, m.norm, 1e-6, sum=x, out=h)
         logits = q4k.matmul(m.w[l, "router"], m.experts, C, h)
         ids, weights, slots = new(T, m.top, dtype=i32), new(T, m.top), new(T, m.top, dtype=i32)
         order, starts = new(P, dtype=i32), new(m.experts + 1, dtype=i32)
         q4k.q4k_route(logits, m.top, q4k.ROUTE_SOFTMAX_TOP, m.out_scale, ids, weights, order, slots, starts,
                       new(q4k.q4k_route_workspace(T, m.experts), dtype=u8))
         rows, act, y = new(P, C, dtype=bf16), new(P, m.ffn, dtype=bf16), new(P, C, dtype=bf16)
-        q4k.q4k_experts_gather(codes, order, m.top, rows, scales=scales)
+        q4k.q4k_experts_gather(h, order, m.top, rows)
         q4k.q4k_experts_gated(m.w[l, "gate"], m.w[l, "up"], m.ffn, C, rows, starts, act)
         q4k.q4k_experts_matmul(m.w[l, "down"], C, m.ffn, act, starts, y)
         out = new(T, C)

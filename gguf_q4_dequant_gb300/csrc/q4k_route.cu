@@ -180,7 +180,7 @@ __device__ __forceinline__ void scan_experts(const int* cnt, int E, int* base) {
 }
 
 // A step of a few tokens is one launch: a cluster's blocks share the picks, which
-// fill a block's integer pipe (48 tokens: 5.9 us, 8.6 by one block), and hand them
+// fill a block's integer pipe (48 tokens: 5.7 us, 8.4 by one block), and hand them
 // to the first one's shared memory, which does the rest.
 template <int R>
 __global__ void __launch_bounds__(pick_threads(R)) q4k_route_one_kernel(const RouteArgs a) {

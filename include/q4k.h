@@ -446,7 +446,9 @@ int q4k_route(const float* logits, int64_t T, int64_t E, int k, int weighting, f
  * Rows in the order of their experts: out[p] = X[order[p] / k] for p < T*k; rows
  * whose order is outside [0, T*k) are left as they are. X: bf16 (scales NULL), or
  * e4m3 codes with scales as q4k_add_norm writes them; a code times its scale is
- * exact in bf16 (down to 2^-126).
+ * exact in bf16 (down to 2^-126). (Codes are for rows that are kept or sent
+ * in 8 bits: they have 4 significant bits, and where the norm writes bf16 rows as well,
+ * gathering those is the faster and the more exact way.)
  *   X    device, [T][C] bf16 or codes;  scales  device, [T][C/32] bytes or NULL
  *   out  device, [T*k][C] bf16
  * 1 <= k <= 32, T >= 1, T*k < 2^31; C a multiple of 8 (of 32 with scales), 8 .. 32768.
